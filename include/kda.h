@@ -443,6 +443,135 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
                            float *dbeta, float *d_o_gate, float *d_conv_w, float *dS0, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence. Conventions as above, and: every
+ * output range is checked against every input range and the other outputs;
+ * calls whose ranges meet are refused (INVALID_VALUE) unless said otherwise.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Linear attention with one decay per head, no delta rule. Per sequence and
+ * head, with the state S in R^{K x V}:
+ *
+ *   S <- exp(g_t) S + k_t v_t^T,      o_t <- scale * S^T q_t
+ *
+ * What the g argument holds:
+ *   KDA_DECAY_PER_TOKEN  [B, T, H] in the I/O dtype: a log-decay per token
+ *   KDA_DECAY_PER_HEAD   [H] fp32: a constant of each head
+ * Log-decays are at most 0 in use; -inf (a token that clears the state) is
+ * allowed, everything below -104 counts as e^-104 = 0 in fp32. Positive ones
+ * are used as given as long as their sums stay in range.
+ */
+typedef enum {
+    KDA_DECAY_PER_TOKEN = 0,
+    KDA_DECAY_PER_HEAD = 1
+} kda_decay_t;
+
+/*
+ * Workspace bytes of kda_hd_chunk_fwd and kda_hd_chunk_bwd (arguments as
+ * there; packed: whether cu_seqlens is given, 0 or 1). Never 0 for sizes that
+ * are supported; 0 otherwise.
+ */
+size_t kda_hd_chunk_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                                        int32_t num_seqs, int32_t packed, kda_dtype_t io);
+size_t kda_hd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                                        int32_t num_seqs, int32_t packed, kda_dtype_t io);
+
+/*
+ * Chunked forward pass over whole sequences.
+ *   q, k       [B, T, Hk, K], v [B, T, H, V] in `io`; H % Hk == 0, head h
+ *              reads the q and k of head h / (H / Hk)
+ *   g          as `decay` says
+ *   S0         [num_seqs, H, K, V] fp32 or NULL (zero)
+ *   cu_seqlens as for kda_chunk_fwd (clamped, made non-decreasing on the
+ *              device; empty sequences allowed: their S_final is S0)
+ *   o          [B, T, H, V] in `io`; rows of tokens outside every sequence
+ *              are neither read nor written
+ *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
+ * The state is fp32 throughout; for bf16 I/O what is added to it is exact to
+ * fp32. A non-finite q, k, v or g spoils its own head and sequence, from the
+ * first token of its 64-token chunk on. Errors as for kda_chunk_fwd
+ * (INVALID_VALUE also for H % Hk != 0 and a scale that is not finite).
+ */
+kda_status_t kda_hd_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
+                              const int32_t *cu_seqlens, int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K,
+                              int32_t V, int32_t num_seqs, kda_dtype_t io, kda_decay_t decay, float scale, void *o,
+                              float *S_final, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients, given d_o = dL/do [B, T, H, V] in `io` and dS_final =
+ * dL/dS_final (fp32, or NULL: zero):
+ *   dq, dk     [B, T, Hk, K], dv [B, T, H, V] in `io` (dq and dk summed in
+ *              fp32 over the heads that share them), rounded once
+ *   dg         [B, T, H] in `io`, or NULL to skip; only with
+ *              KDA_DECAY_PER_TOKEN (a constant per head has no gradient
+ *              here: NOT_SUPPORTED)
+ *   dS0        [num_seqs, H, K, V] fp32, or NULL to skip
+ * Nothing from a forward call is needed; the result is deterministic. Rows of
+ * tokens outside every sequence are not written.
+ */
+kda_status_t kda_hd_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
+                              const int32_t *cu_seqlens, const void *d_o, const float *dS_final, int64_t B, int64_t T,
+                              int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs, kda_dtype_t io,
+                              kda_decay_t decay, float scale, void *dq, void *dk, void *dv, void *dg, float *dS0,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of N sequences: q, k [N, Hk, K], v [N, H, V], o [N, H, V] in
+ * `io`; g [N, H] in `io` or [H] fp32; S [N, H, K, V] fp32, in place.
+ */
+kda_status_t kda_hd_decode_step(const void *q, const void *k, const void *v, const void *g, float *S, void *o,
+                                int32_t N, int32_t H, int32_t Hk, int32_t K, int32_t V, kda_dtype_t io,
+                                kda_decay_t decay, float scale, void *stream);
+
+/*
+ * Rotary positions of q [tokens, Hq, D] and k [tokens, Hk, D] (Hk = 0 and
+ * NULL: q alone) in `io`. Of each head's D channels (2..512) the first R
+ * (even) turn in pairs j by the angle position * freqs[j]:
+ *   y1 = (x1 cos - x2 sin) * scale,  y2 = (x1 sin + x2 cos) * scale
+ *   KDA_ROTARY_HALF         pairs (j, j + R/2)
+ *   KDA_ROTARY_INTERLEAVED  pairs (2j, 2j + 1)
+ * and the others are copied. inverse = 1 turns back: with the same scale, the
+ * gradient of the call with inverse = 0 (and the other way round).
+ *   freqs      [R/2] fp64, radians per position: angles are reduced in
+ *              64-bit fixed point, exact at any 32-bit position
+ *   positions  [tokens] int32 (any sign), or NULL: token index modulo T
+ * q_out may be q and k_out may be k (in place).
+ */
+typedef enum {
+    KDA_ROTARY_HALF = 0,
+    KDA_ROTARY_INTERLEAVED = 1
+} kda_rotary_layout_t;
+kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const int32_t *positions, void *q_out,
+                        void *k_out, int64_t tokens, int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R,
+                        kda_dtype_t io, kda_rotary_layout_t layout, int32_t inverse, float scale, void *stream);
+
+/*
+ * Layer norm of rows of C channels (1..16384), and the output gate behind it:
+ *   n = (x - mean) / sqrt(mean((x - mean)^2) + eps)   (center = 0: mean = 0)
+ *   y = n * weight + bias,   with o_gate z:  y * sigmoid(z)
+ *   x, o_gate, y  [rows, C] in `io` (o_gate or NULL)
+ *   weight, bias  [groups, C] fp32 or NULL (1 and 0); row r has those of
+ *                 group r % groups (groups = heads for rows [.., H, C]);
+ *                 rows % groups == 0
+ * Statistics and sums are fp32, the variance from the centered values.
+ */
+kda_status_t kda_layer_norm_fwd(const void *x, const float *weight, const float *bias, const void *o_gate, void *y,
+                                int64_t rows, int32_t groups, int32_t C, float eps, int32_t center, kda_dtype_t io,
+                                void *stream);
+
+/*
+ * Its gradients given dy [rows, C] in `io`: dx [rows, C] in `io`; dweight,
+ * dbias [groups, C] fp32 (or NULL to skip; summed in a fixed order, zeros
+ * where there are no rows); d_o_gate [rows, C] in `io`, required with o_gate
+ * (else ignored). weight, bias and o_gate as the forward had them.
+ */
+size_t kda_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t groups, int32_t C);
+kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *bias,
+                                const void *o_gate, void *dx, float *dweight, float *dbias, void *d_o_gate,
+                                int64_t rows, int32_t groups, int32_t C, float eps, int32_t center, kda_dtype_t io,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

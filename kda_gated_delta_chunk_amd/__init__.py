@@ -9,6 +9,9 @@ performs no arithmetic of the method itself.
 Shapes (contiguous): q, k, g [B, T, H, K]; v [B, T, H, V]; beta [B, T, H];
 states [num_seqs, H, K, V] fp32. With cu_seqlens (int32 [num_seqs+1], on the
 device), B must be 1 and sequences are packed along T.
+
+The operators around it (linear attention with one decay per head, rotary
+positions, layer norm) are in layers.py and exported here.
 """
 from __future__ import annotations
 
@@ -19,7 +22,8 @@ from ._lib import KDAError, KDA_DTYPE_BF16, KDA_DTYPE_FP32
 
 __all__ = ["chunk_fwd", "chunk_prep", "chunk_state", "chunk_bwd", "decode_step", "workspace_bytes",
            "min_workspace_bytes", "prep_workspace_bytes", "workspace_status", "bwd_workspace_bytes", "KDAError",
-           "abi_version"]
+           "abi_version", "hd_chunk_fwd", "hd_chunk_bwd", "hd_decode_step", "hd_workspace_bytes",
+           "hd_bwd_workspace_bytes", "rotary", "rotary_freqs", "layer_norm_fwd", "layer_norm_bwd"]
 
 _DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_FP32}
 _NAME = {"bf16": torch.bfloat16, "fp32": torch.float32}
@@ -375,3 +379,8 @@ def chunk_bwd(q, k, v, g, beta, do, S0=None, dS_final=None, cu_seqlens=None, wan
                            _ptr(out.get("dS0")), _ptr(workspace), workspace.numel(), _stream(dev))
     _lib.check(st, "kda_chunk_bwd")
     return out
+
+
+# layers.py uses the argument helpers above
+from .layers import (hd_bwd_workspace_bytes, hd_chunk_bwd, hd_chunk_fwd, hd_decode_step,  # noqa: E402
+                     hd_workspace_bytes, layer_norm_bwd, layer_norm_fwd, rotary, rotary_freqs)

@@ -20,6 +20,9 @@ KDA_QK_AS_GIVEN = 0
 KDA_QK_L2NORM = 1
 CONVS = {"none": 0, "short4": 1, "short4_silu": 2}
 OPERANDS = {"bf16": 0, "fp16": 1}
+KDA_DECAY_PER_TOKEN = 0
+KDA_DECAY_PER_HEAD = 1
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 # device-side error bits of a prefill workspace (kda_workspace_status)
 WS_ERR_WAIT_TIMEOUT = 1
 WS_ERR_HEADER_MISMATCH = 2
@@ -29,7 +32,10 @@ EXPORTS = ("kda_abi_version", "kda_status_string", "kda_chunk_fwd_workspace_byte
            "kda_chunk_prep_workspace_bytes",
            "kda_workspace_status", "kda_chunk_fwd", "kda_chunk_prep", "kda_chunk_state", "kda_decode_step",
            "kda_chunk_bwd_workspace_bytes", "kda_chunk_bwd_segmented_workspace_bytes", "kda_chunk_bwd",
-           "kda_chunk_fwd_no_alloc")
+           "kda_chunk_fwd_no_alloc",
+           "kda_hd_chunk_fwd_workspace_bytes", "kda_hd_chunk_bwd_workspace_bytes", "kda_hd_chunk_fwd",
+           "kda_hd_chunk_bwd", "kda_hd_decode_step", "kda_rotary", "kda_layer_norm_fwd",
+           "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd")
 
 NO_ALLOC_SCRATCH_BYTES = 16 * 1024 * 1024  # KDA_NO_ALLOC_SCRATCH_BYTES
 
@@ -92,6 +98,26 @@ def load() -> ctypes.CDLL:
                                   ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                   sz, vp]
     lib.kda_chunk_bwd.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    for fn in (lib.kda_hd_chunk_fwd_workspace_bytes, lib.kda_hd_chunk_bwd_workspace_bytes):
+        fn.argtypes = [i64, i64, i32, i32, i32, i32, i32, i32, ci]
+        fn.restype = sz
+    lib.kda_hd_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, ci, ci, f32, vp, vp, vp,
+                                     sz, vp]
+    lib.kda_hd_chunk_fwd.restype = ci
+    lib.kda_hd_chunk_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, ci, ci, f32, vp,
+                                     vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_hd_chunk_bwd.restype = ci
+    lib.kda_hd_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ci, ci, f32, vp]
+    lib.kda_hd_decode_step.restype = ci
+    lib.kda_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, ci, ci, i32, f32, vp]
+    lib.kda_rotary.restype = ci
+    lib.kda_layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, ci, vp]
+    lib.kda_layer_norm_fwd.restype = ci
+    lib.kda_layer_norm_bwd_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.kda_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.kda_layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, ci, vp, sz, vp]
+    lib.kda_layer_norm_bwd.restype = ci
     _lib = lib
     return lib
 

@@ -1,0 +1,68 @@
+// Linear attention with one decay per head: what its translation units share (segments, the chunk kernel's arguments).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_layer.hpp"
+
+namespace kda {
+namespace hd {
+
+// A sequence is cut into segments of `seg` tokens (a multiple of 64) that run as workgroups of their own. Slot i of a
+// batch is segment i % nseg of row i / nseg; of packed sequences, entry i of a table that a first kernel makes from
+// cu_seqlens (slots behind the last segment have seq -1). An empty sequence is one empty segment.
+struct Segment {
+    int32_t seq, j, nseg, pad;
+    int64_t t0, t1;  // tokens of the flattened [B * T]
+};
+
+enum class Kind { fwd, rev, fwd_inc, rev_inc, fwd_dg, rev_dg };
+
+struct CoreArgs {
+    const void *a, *b, *c;      // rows [B*T, H / g?, KD | KD | VD]
+    int32_t ga, gb, gc;         // heads that share a row of a, b, c
+    int32_t H, VD, tiles;       // heads; columns of c and y; tiles of VT columns
+    void *y;                    // [B*T, H, VD]
+    bool y_fp32;                // y in fp32 whatever the I/O type
+    bool g_head;
+    const void *g;              // [B*T, H] I/O type, or [H] fp32 (g_head)
+    const float *s_init;        // state before the first segment (REV: after the last), or null
+    const float *s_seg;         // states the other segments start from, per slot and head
+    float *s_out;               // state after the last segment (REV: before the first), or null
+    float *s_inc;               // what a segment adds (the increment passes), per slot and head
+    float *seg_decay;           // log2 of a segment's decay, per slot and head
+    int64_t sr, sc;             // strides of a state's rows and columns
+    const Segment *table;       // or null: rows of T tokens
+    int64_t slots, T, seg, ntok;
+    int32_t nseg;
+    float s_intra, s_inter, s_up;
+    // the log-decays' gradient
+    const void *x;              // rows [B*T, H / gx, VD] that y is multiplied with
+    int32_t gx, share_tiles;
+    float *share;               // [tiles][H][B*T]: x.y of the state's part, from the pass over dq
+    float *dg_part;             // [tiles][H][B*T]
+    const float *s_end;         // the sequences' last states (read where s_init is not null)
+    const float *s_seg_fwd;     // the forward states the segments start from
+};
+
+#ifdef __HIPCC__
+__device__ __forceinline__ Segment segment_of(const CoreArgs &A, int64_t slot) {
+    if (A.table) return A.table[slot];
+    Segment s;
+    s.seq = (int32_t)(slot / A.nseg);
+    s.j = (int32_t)(slot - (int64_t)s.seq * A.nseg);
+    s.nseg = A.nseg;
+    s.pad = 0;
+    const int64_t row = (int64_t)s.seq * A.T, e = (int64_t)(s.j + 1) * A.seg;
+    s.t0 = row + (int64_t)s.j * A.seg;
+    s.t1 = row + (e < A.T ? e : A.T);
+    return s;
+}
+#endif
+
+hipError_t core_bf16(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st);
+hipError_t core_fp32(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st);
+
+}  // namespace hd
+}  // namespace kda

@@ -1,0 +1,529 @@
+// Linear attention with one decay per head: the chunk kernel that its forward pass and every gradient share.
+//
+// With b_t the sum of the log-decays up to token t, the forward pass is
+//   o_t = scale ( sum_{s<=t} e^{b_t - b_s} (q_t.k_s) v_s + e^{b_t} S_0^T q_t ),   S = sum e^{b_T - b_s} k_s v_s^T + e^{b_T} S_0
+// and its gradients have the same form, with the roles of the tensors exchanged and, for dk and dv, time reversed:
+//   dq: rows do against v, summing k;   dv: rows k against q, summing do;   dk: rows v against do, summing q.
+// So one kernel computes, for rows a, b (KD channels) and c (VD channels) of a head,
+//   y_t = s_intra sum_s D_ts (a_t.b_s) c_s + s_inter win_t St^T a_t,    St <- e^{b_C} St + s_up sum_s wup_s b_s c_s^T
+// chunk by chunk: forward in time (s <= t, win = e^{b_t}, wup = e^{b_C - b_s}) or backward (REV: s >= t,
+// win = e^{b_C - b_t}, wup = e^{b_s}). The differences of b are at most 0 wherever they are used, so no weight
+// overflows however strong the decay; b is kept as a whole part and a rest in [0, 1) (base 2), whose differences are
+// exact, so a token that decays everything (down to -inf, held at e^-104 = 0) does not cost its neighbours precision.
+//
+// Layout (16x16 matrix-core tiles, see kda_common.hpp). A workgroup owns one (segment of a sequence, head, tile of VT
+// columns); each wavefront owns CT 16-column tiles of the state, all KD rows, as fp32 accumulators. An accumulator
+// tile St[4g+i][l%16] is at once the left operand of St^T a, so the state never leaves the registers; y comes out
+// transposed (four adjacent columns of one token per lane: one 8-byte store). The rows lie in LDS as loaded; operands
+// that run along tokens come through the transposing LDS read (bf16) or element reads (fp32). The chunk's weighted
+// products D (a.b) go through LDS once, shared by all wavefronts.
+//
+// Precision (bf16 I/O). Products of inputs are exact in the matrix cores' fp32 sums. Three operands are computed
+// values: the weighted products D (a.b) and the state as an operand are rounded to bf16 pairs or singles (PLO, SLO:
+// whether the rounding's rest is multiplied too), and wup c, which everything later in the sequence is summed from,
+// goes in as three bf16 parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
+#pragma once
+
+#include "kda_common.hpp"
+#include "kda_hd.hpp"
+
+namespace kda {
+namespace hd {
+
+// ------------------------------------------------------------------ rows in LDS
+// NCOL elements a row. bf16: 16-byte slots permuted within the row by its index, so that both the row reads (16 rows
+// at one slot) and the transposing reads (8 rows at two adjacent slots) of a half wavefront touch every bank once.
+// fp32: rows padded by 16 bytes to the same end.
+template <bool BF, int NCOL> struct Rows;
+template <int NCOL> struct Rows<true, NCOL> {
+    static constexpr int NS = NCOL / 8, RB = NCOL * 2;
+    static constexpr int LB = NS == 16 ? 4 : NS == 8 ? 3 : 2;  // log2(NS)
+    static constexpr int bytes(int rows) { return rows * RB; }
+    static __device__ __forceinline__ int swz(int row) {
+        const int x = row >> (4 - LB);  // rows that share their banks
+        return ((x << 1) & (NS - 1)) | ((x >> (LB - 1)) & 1);
+    }
+    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + ((s ^ swz(row)) << 4); }
+    // column of four adjacent elements (a multiple of 4)
+    static __device__ __forceinline__ int quad(int row, int col) { return slot(row, col >> 3) + ((col & 4) << 1); }
+    // operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of one row per lane
+    static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int row, int c, int g) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, 32 * c + 4 * g));
+        const uint2 w = *reinterpret_cast<const uint2 *>(t + quad(row, 32 * c + 16 + 4 * g));
+        Frag8<true> f;
+        f.p[0] = u.x; f.p[1] = u.y; f.p[2] = w.x; f.p[3] = w.y;
+        return f;
+    }
+    // operand with the same slot map along the rows 32s .. 32s+31, column 16c + l%16
+    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int s, int c, int lane) {
+        typedef __attribute__((address_space(3))) s16x4 *lds4;
+        const int g = lane >> 4, i = lane & 15;
+        const int row = 32 * s + 4 * g + (i >> 2), col = 16 * c + 4 * (i & 3);
+        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + quad(row, col)));
+        const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + quad(row + 16, col)));
+        const uint2 a = __builtin_bit_cast(uint2, u), b = __builtin_bit_cast(uint2, w);
+        Frag8<true> f;
+        f.p[0] = a.x; f.p[1] = a.y; f.p[2] = b.x; f.p[3] = b.y;
+        return f;
+    }
+    static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
+        *reinterpret_cast<uint2 *>(t + quad(row, col)) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+    }
+    static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, col));
+        x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+    }
+};
+template <int NCOL> struct Rows<false, NCOL> {
+    static constexpr int NS = NCOL / 4, RB = (NCOL + 4) * 4;
+    static constexpr int bytes(int rows) { return rows * RB; }
+    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + (s << 4); }
+    static __device__ __forceinline__ int quad(int row, int col) { return row * RB + col * 4; }
+    static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int row, int c, int g) {
+        const float4 u = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 4 * g));
+        const float4 w = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 16 + 4 * g));
+        return Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
+    }
+    static __device__ __forceinline__ Frag8<false> col_frag(const char *t, int s, int c, int lane) {
+        const int g = lane >> 4, i = lane & 15;
+        Frag8<false> f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.f[j] = *reinterpret_cast<const float *>(t + quad(32 * s + 4 * g + j, 16 * c + i));
+            f.f[4 + j] = *reinterpret_cast<const float *>(t + quad(32 * s + 16 + 4 * g + j, 16 * c + i));
+        }
+        return f;
+    }
+    static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
+        *reinterpret_cast<float4 *>(t + quad(row, col)) = make_float4(a, b, c, d);
+    }
+    static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
+        const float4 u = *reinterpret_cast<const float4 *>(t + quad(row, col));
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    }
+};
+
+// C rows of `n` valid ones from global memory (first row at p, `pitch` elements apart) into LDS; the others are zero.
+template <bool BF, int NCOL, int C, int NT>
+__device__ __forceinline__ void load_rows(char *t, const typename IO<BF>::T *p, int64_t pitch, int n) {
+    constexpr int NS = Rows<BF, NCOL>::NS, EL = BF ? 8 : 4;
+    static_assert((C * NS) % NT == 0, "whole loads");
+#pragma unroll
+    for (int i = 0; i < C * NS / NT; ++i) {
+        const int e = threadIdx.x + i * NT, row = e / NS, s = e % NS;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (row < n) w = *reinterpret_cast<const uint4 *>(p + row * pitch + s * EL);
+        *reinterpret_cast<uint4 *>(t + Rows<BF, NCOL>::slot(row, s)) = w;
+    }
+}
+
+// Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
+__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<true> &hi, Frag8<true> &lo) {
+    split_bf16(u.x, u.y, hi.p[0], lo.p[0]);
+    split_bf16(u.z, u.w, hi.p[1], lo.p[1]);
+    split_bf16(w.x, w.y, hi.p[2], lo.p[2]);
+    split_bf16(w.z, w.w, hi.p[3], lo.p[3]);
+}
+__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<false> &hi, Frag8<false> &lo) {
+    hi = Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
+    lo = hi;
+}
+// w c as three bf16 operands whose sum has all 24 bits (fp32: as it is)
+__device__ __forceinline__ void scaled_frags(const Frag8<true> &c, const float (&w)[8], Frag8<true> (&f)[3]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = bf_lo(c.p[i]) * w[2 * i], y = bf_hi(c.p[i]) * w[2 * i + 1];
+        f[0].p[i] = pack_bf16(x, y);
+        const float x1 = x - bf_lo(f[0].p[i]), y1 = y - bf_hi(f[0].p[i]);
+        split_bf16(x1, y1, f[1].p[i], f[2].p[i]);
+    }
+}
+__device__ __forceinline__ void scaled_frags(const Frag8<false> &c, const float (&w)[8], Frag8<false> (&f)[1]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[0].f[i] = c.f[i] * w[i];
+}
+
+template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG>
+__global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs A) {
+    constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
+    constexpr int C = BF ? 64 : 32, TT = C / 16, SC = C / 32;  // tokens per chunk; token tiles; 32-token steps
+    constexpr int NPART = BF ? 3 : 1;
+    constexpr bool PLO = BF, SLO = BF && DG;
+    static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
+    using E = typename IO<BF>::T;
+    using RK = Rows<BF, KD>;
+    using RV = Rows<BF, VT>;
+    using RP = Rows<BF, C>;
+    constexpr int SZ_K = RK::bytes(C), SZ_V = RV::bytes(C), SZ_P = RP::bytes(C);
+    __shared__ __align__(16) char s_b[SZ_K], s_c[SZ_V];
+    __shared__ __align__(16) char s_a[INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
+    __shared__ __align__(16) char s_x[DG && REV ? SZ_V : 16];
+    __shared__ __align__(16) float s_win[C], s_wup[C], s_bh[C], s_bl[C];
+    __shared__ float s_ec;
+    __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
+    (void)s_pl; (void)s_x; (void)s_u; (void)s_red;
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    // tiles of one (segment, head) sit 8 workgroups apart: the same XCD, whose L2 then holds their common rows
+    const int64_t items = A.slots * A.H;
+    const int64_t blk = blockIdx.x, grp = blk / (8 * A.tiles);
+    const int in = (int)(blk - grp * 8 * A.tiles);
+    const int64_t item = grp * 8 + (in & 7);
+    const int vt = in >> 3;
+    if (item >= items) return;
+    const int64_t slot = item / A.H;
+    const int h = (int)(item - slot * A.H);
+    const Segment sg = segment_of(A, slot);
+    if (sg.seq < 0) return;
+    if (INC && (REV ? sg.j == 0 : sg.j == sg.nseg - 1)) return;  // no segment needs what it would add
+
+    const int64_t nh = (int64_t)sg.seq * A.H + h;
+    const int64_t sstate = (int64_t)KD * A.VD;
+    const int col0 = vt * VT + wave * CT * 16;  // this wavefront's first column
+    const int len = (int)(sg.t1 - sg.t0), nch = (len + C - 1) / C;
+
+    // ---- the state at the segment's start (REV: at its end)
+    f32x4 st[KT][CT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) st[kt][ct] = zero4();
+    if (!INC) {
+        const bool first = REV ? sg.j == sg.nseg - 1 : sg.j == 0;
+        const float *s0 = first ? (A.s_init ? A.s_init + nh * sstate : nullptr)
+                                : A.s_seg + (slot * A.H + h) * sstate;
+        if (s0) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st[kt][ct][i] = s0[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc];
+        }
+    }
+    // ---- what the borders behind the segment pass on to its log-decays: <state gradient, state> at its end
+    float carry = 0.f;
+    if constexpr (DG && REV) {
+        const bool last = sg.j == sg.nseg - 1;
+        const float *se = last ? (A.s_init ? A.s_end + nh * sstate : nullptr)
+                               : A.s_seg_fwd + ((slot + 1) * A.H + h) * sstate;
+        if (se) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        carry += st[kt][ct][i] * se[(int64_t)(16 * kt + 4 * g + i) * A.sr +
+                                                    (int64_t)(col0 + 16 * ct + li) * A.sc];
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) carry += __shfl_xor(carry, d);
+        if (lane == 0) s_red[wave] = carry;
+        __syncthreads();
+        carry = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) carry += s_red[w];
+    }
+
+    const E *pa = reinterpret_cast<const E *>(A.a) + (int64_t)(h / A.ga) * KD;
+    const E *pb = reinterpret_cast<const E *>(A.b) + (int64_t)(h / A.gb) * KD;
+    const E *pc = reinterpret_cast<const E *>(A.c) + (int64_t)(h / A.gc) * A.VD + vt * VT;
+    const int64_t la = (int64_t)(A.H / A.ga) * KD, lb = (int64_t)(A.H / A.gb) * KD, lc = (int64_t)(A.H / A.gc) * A.VD;
+
+    if constexpr (!INC) {  // tiles across the diagonal that are read but never computed
+        for (int i = threadIdx.x; i < SZ_P / 16; i += NT) {
+            reinterpret_cast<uint4 *>(s_p)[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (PLO) reinterpret_cast<uint4 *>(s_pl)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    double btot = 0.0;  // lane 0 of wavefront 0
+
+    for (int cc = 0; cc < nch; ++cc) {
+        const int64_t tc = sg.t0 + (int64_t)(REV ? nch - 1 - cc : cc) * C;
+        const int n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
+        __syncthreads();  // the last chunk's reads are done
+        if constexpr (!INC) load_rows<BF, KD, C, NT>(s_a, pa + tc * la, la, n);
+        load_rows<BF, KD, C, NT>(s_b, pb + tc * lb, lb, n);
+        load_rows<BF, VT, C, NT>(s_c, pc + tc * lc, lc, n);
+        if constexpr (DG && REV) {
+            const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
+            load_rows<BF, VT, C, NT>(s_x, reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD + vt * VT + tc * lx,
+                                     lx, n);
+        }
+        if (wave == 0) {  // the chunk's decays: sums in fp64, in base 2
+            double x = 0.0;
+            if (lane < n) {
+                float gv = A.g_head ? reinterpret_cast<const float *>(A.g)[h]
+                                    : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
+                gv = gv < -104.f ? -104.f : gv;  // e^-104 is 0 in fp32; NaN stays
+                x = (double)gv * 1.4426950408889634;
+            }
+#pragma unroll
+            for (int d = 1; d < C; d <<= 1) {
+                const double y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            const double xc = __shfl(x, C - 1);
+            if (lane < C) {
+                const double f = floor(x);
+                s_bh[lane] = (float)f;
+                s_bl[lane] = (float)(x - f);
+                const float ein = __builtin_amdgcn_exp2f((float)x), eout = __builtin_amdgcn_exp2f((float)(xc - x));
+                s_win[lane] = (REV ? eout : ein) * A.s_inter;
+                s_wup[lane] = (REV ? ein : eout) * A.s_up;
+            }
+            if (lane == 0) s_ec = __builtin_amdgcn_exp2f((float)xc);
+            if constexpr (INC) btot += xc;
+        }
+        __syncthreads();
+
+        // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
+        if constexpr (!INC) {
+            if constexpr (DG && REV)
+                if (lane < C) s_u[wave][lane] = 0.f;
+            constexpr int NTILE = TT * (TT + 1) / 2;
+            for (int p = wave; p < NTILE; p += NW) {
+                int x = 0, y = p;
+                while (y > x) { y -= x + 1; ++x; }  // p-th pair (x, y <= x)
+                const int tt = REV ? y : x, ts = REV ? x : y;
+                f32x4 acc = zero4(), acd = zero4();
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+                    acc = mma32(acc, RK::row_frag(s_b, 16 * ts + li, c, g), RK::row_frag(s_a, 16 * tt + li, c, g));
+                if constexpr (DG && REV) {
+#pragma unroll
+                    for (int c = 0; c < VT / 32; ++c)
+                        acd = mma32(acd, RV::row_frag(s_c, 16 * ts + li, c, g), RV::row_frag(s_x, 16 * tt + li, c, g));
+                }
+                mfma_fence(acc, acd);
+                const int t = 16 * tt + li;
+                const float th = s_bh[t], tl = s_bl[t];
+                float w[4], csum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int s = 16 * ts + 4 * g + i;
+                    const float d = REV ? (s_bh[s] - th) + (s_bl[s] - tl) : (th - s_bh[s]) + (tl - s_bl[s]);
+                    const bool in_past = REV ? s >= t : s <= t;
+                    w[i] = in_past ? acc[i] * (__builtin_amdgcn_exp2f(d) * A.s_intra) : 0.f;
+                    if constexpr (DG && REV) {
+                        // pair (row s, column t) of the log-decays' gradient: + at its row, - at its column
+                        const float X = in_past ? w[i] * acd[i] : 0.f;
+                        csum += X;
+                        float r = X;
+#pragma unroll
+                        for (int m = 8; m >= 1; m >>= 1) r += __shfl_xor(r, m);
+                        if (li == 0) s_u[wave][s] += r;
+                    }
+                }
+                if constexpr (DG && REV) {
+                    csum += __shfl_xor(csum, 16);
+                    csum += __shfl_xor(csum, 32);
+                    __builtin_amdgcn_wave_barrier();
+                    if (g == 0) s_u[wave][t] -= csum;
+                    __builtin_amdgcn_wave_barrier();
+                }
+                if constexpr (PLO) {
+                    uint2 hi, lo;
+                    split_bf16(w[0], w[1], hi.x, lo.x);
+                    split_bf16(w[2], w[3], hi.y, lo.y);
+                    const int at = RP::quad(t, 16 * ts + 4 * g);
+                    *reinterpret_cast<uint2 *>(s_p + at) = hi;
+                    *reinterpret_cast<uint2 *>(s_pl + at) = lo;
+                } else {
+                    RP::store_quad(s_p, t, 16 * ts + 4 * g, w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        // ---- what the state gives: y^T = win (St^T a)
+        f32x4 y[CT][TT];
+        if constexpr (!INC) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) y[ct][tt] = zero4();
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                Frag8<BF> hi[CT], lo[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) state_frag(st[2 * c][ct], st[2 * c + 1][ct], hi[ct], lo[ct]);
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    const Frag8<BF> f = RK::row_frag(s_a, 16 * tt + li, c, g);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        y[ct][tt] = mma32(y[ct][tt], hi[ct], f);
+                        if constexpr (SLO) y[ct][tt] = mma32(y[ct][tt], lo[ct], f);
+                    }
+                }
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    mfma_fence(y[ct][tt]);
+                    y[ct][tt] *= s_win[16 * tt + li];
+                }
+            if constexpr (DG) {
+                // the state's share of a token in its log-decay: x_t . y_t over this workgroup's columns
+                const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
+                const E *px = reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD + col0 + 4 * g;
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    const int t = 16 * tt + li;
+                    float d = 0.f;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        float x[4] = {0.f, 0.f, 0.f, 0.f};
+                        if constexpr (REV) {
+                            RV::load_quad(s_x, t, wave * CT * 16 + 16 * ct + 4 * g, x);
+                        } else if (t < n) {
+                            const E *p = px + (tc + t) * lx + 16 * ct;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[i] = IO<BF>::ld(p, i);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d = fmaf(x[i], y[ct][tt][i], d);
+                    }
+                    d += __shfl_xor(d, 16);
+                    d += __shfl_xor(d, 32);
+                    if (g == 0) {
+                        if constexpr (REV) s_u[wave][t] -= d;
+                        else s_u[wave][t] = d;
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the weighted products (and the shares) of every wavefront are there
+
+        if constexpr (DG) {
+            if (wave == 0 && lane < C) {
+                float u = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) u += s_u[w][lane];
+                const int64_t at = (int64_t)h * A.ntok + tc + lane;
+                if constexpr (!REV) {
+                    if (lane < n) A.share[vt * A.ntok * A.H + at] = u;
+                } else {
+                    if (vt == 0 && lane < n)  // the forward states' shares, from the pass before
+                        for (int w = 0; w < A.share_tiles; ++w) u += A.share[w * A.ntok * A.H + at];
+                    // sum over the tokens from this one to the segment's end
+#pragma unroll
+                    for (int d = 1; d < C; d <<= 1) {
+                        const float v = __shfl_down(u, d);
+                        if (lane + d < C) u += v;
+                    }
+                    if (lane < n) A.dg_part[vt * A.ntok * A.H + at] = u + carry;
+                }
+                if constexpr (REV) carry += __shfl(u, 0);
+            }
+        }
+        // ---- the chunk's own products, and the state's update
+        const float ec = s_ec;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) st[kt][ct] *= ec;
+#pragma unroll
+        for (int s = 0; s < SC; ++s) {
+            Frag8<BF> cw[CT][NPART];
+            float w[8];
+            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + 4 * g);
+            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + 16 + 4 * g);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const Frag8<BF> cf = RV::col_frag(s_c, s, wave * CT + ct, lane);
+                if constexpr (!INC) {
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt) {
+                        if (REV ? 2 * s + 1 < tt : 2 * s > tt) continue;
+                        y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p, 16 * tt + li, s, g));
+                        if constexpr (PLO) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl, 16 * tt + li, s, g));
+                    }
+                }
+                scaled_frags(cf, w, cw[ct]);
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const Frag8<BF> bf = RK::col_frag(s_b, s, kt, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int q = 0; q < NPART; ++q) st[kt][ct] = mma32(st[kt][ct], bf, cw[ct][q]);
+            }
+        }
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) mfma_fence(st[kt][ct]);
+        if constexpr (!INC) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    mfma_fence(y[ct][tt]);
+                    const int t = 16 * tt + li;
+                    if (t >= n) continue;
+                    const f32x4 v = y[ct][tt];
+                    const int64_t at = ((tc + t) * A.H + h) * A.VD + col0 + 16 * ct + 4 * g;
+                    if (BF && !A.y_fp32)
+                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(A.y) + at) =
+                            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                    else
+                        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.y) + at) = make_float4(v.x, v.y, v.z, v.w);
+                }
+        }
+    }
+    // ---- the state at the other end
+    float *so = nullptr;
+    if (INC) so = A.s_inc + (slot * A.H + h) * sstate;
+    else if (REV ? sg.j == 0 : sg.j == sg.nseg - 1) so = A.s_out ? A.s_out + nh * sstate : nullptr;
+    if (so) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    so[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
+    }
+    if (INC && threadIdx.x == 0 && vt == 0) A.seg_decay[slot * A.H + h] = (float)btot;
+}
+
+template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
+hipError_t launch_one(const CoreArgs &a, hipStream_t st) {
+    constexpr int NW = VT >= 64 ? 4 : VT / 16;
+    const int64_t groups = (a.slots * a.H + 7) / 8;
+    const int64_t blocks = groups * 8 * a.tiles;
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((kda_hd_chunk_kernel<BF, KD, VT, NW, REV, INC, DG>), dim3((uint32_t)blocks), dim3(NW * 64), 0, st,
+                       a);
+    return hipGetLastError();
+}
+template <bool BF, int KD, int VT>
+hipError_t launch_kind(const CoreArgs &a, Kind k, hipStream_t st) {
+    switch (k) {
+        case Kind::fwd: return launch_one<BF, KD, VT, false, false, false>(a, st);
+        case Kind::rev: return launch_one<BF, KD, VT, true, false, false>(a, st);
+        case Kind::fwd_inc: return launch_one<BF, KD, VT, false, true, false>(a, st);
+        case Kind::rev_inc: return launch_one<BF, KD, VT, true, true, false>(a, st);
+        case Kind::fwd_dg: return launch_one<BF, KD, VT, false, false, true>(a, st);
+        default: return launch_one<BF, KD, VT, true, false, true>(a, st);
+    }
+}
+template <bool BF, int KD>
+hipError_t launch_vt(const CoreArgs &a, int vt, Kind k, hipStream_t st) {
+    return vt == 32 ? launch_kind<BF, KD, 32>(a, k, st) : launch_kind<BF, KD, 64>(a, k, st);
+}
+template <bool BF>
+hipError_t launch_core(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st) {
+    switch (kd) {
+        case 32: return launch_vt<BF, 32>(a, vt, k, st);
+        case 64: return launch_vt<BF, 64>(a, vt, k, st);
+        default: return launch_vt<BF, 128>(a, vt, k, st);
+    }
+}
+
+}  // namespace hd
+}  // namespace kda

@@ -1,0 +1,10 @@
+// The chunk kernel of linear attention with one decay per head, fp32 I/O.
+#include "kda_hd_core.hpp"
+
+namespace kda {
+namespace hd {
+hipError_t core_fp32(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st) {
+    return launch_core<false>(a, kd, vt, k, st);
+}
+}  // namespace hd
+}  // namespace kda

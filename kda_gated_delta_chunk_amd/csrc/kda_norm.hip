@@ -1,0 +1,326 @@
+// Layer norm over rows of C channels, its output gate, and its gradient, for gfx950.
+//
+//   n = (x - mean) r,  r = (mean((x - mean)^2) + eps)^(-1/2)   (mean = 0 without centering)
+//   y = n w + b,  and with a gate's pre-activation z:  y sigmoid(z)
+// backward, with dy the gradient of what was returned and a = sigmoid(z) (1 without a gate):
+//   dz = dy (n w + b) a (1 - a);  e = dy a;  dw = sum_rows e n;  db = sum_rows e;
+//   d = e w;  dx = r (d - n mean(d n) - mean(d))              (the last term only with centering)
+//
+// Both directions are bound by bytes: every row is read once, held in registers through its reductions (the variance
+// is the mean square of the centered values, not a difference of sums), and written once. The backward recomputes
+// the statistics, so nothing is kept from the forward. All arithmetic is fp32.
+//
+// Row r has the parameters of group r % G. A row is handled by TPR threads; a thread's rows are a whole multiple of G
+// apart, so its parameters, and its sums for their gradients, stay in registers over all of its rows. The sums leave
+// as one partial row per row slot of the grid and a second kernel adds those in a fixed order (no atomics: the same
+// inputs give the same bits).
+#include "kda_common.hpp"
+#include "kda_layer.hpp"
+
+namespace kda {
+namespace {
+
+constexpr int kMaxWG = 1024;  // row slots of the backward's grid are at most this many workgroups (and G's multiple)
+
+template <int TPR, int NT, int NS>
+__device__ __forceinline__ void row_sums(float (&x)[NS], float *lds) {
+#pragma unroll
+    for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) x[i] += __shfl_xor(x[i], d);
+    if constexpr (TPR > 64) {
+        constexpr int NW = TPR / 64;
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();  // the last sums have been read
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) lds[wave * NS + i] = x[i];
+        __syncthreads();
+        const int w0 = wave / NW * NW;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            float s = lds[w0 * NS + i];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) s += lds[(w0 + w) * NS + i];
+            x[i] = s;
+        }
+    }
+}
+
+// A thread's EPT elements of a row. VEC: runs of 16 bytes, run i at 16-byte slot i * TPR + t; else element i at
+// i * TPR + t (rows that are no whole number of 16-byte runs).
+template <bool BF, bool VEC, int TPR, int EPT>
+struct Slice {
+    static constexpr int EL = BF ? 8 : 4;
+    static __device__ __forceinline__ int at(int i, int t) {
+        return VEC ? ((i / EL) * TPR + t) * EL + i % EL : i * TPR + t;
+    }
+    static __device__ __forceinline__ void load(const void *p, int64_t row, int C, int t, float (&x)[EPT]) {
+        using E = typename IO<BF>::T;
+        const E *r = reinterpret_cast<const E *>(p) + row * C;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += EL) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (at(i, t) < C) w = *reinterpret_cast<const uint4 *>(r + at(i, t));
+                E e[EL];
+                __builtin_memcpy(e, &w, 16);
+#pragma unroll
+                for (int j = 0; j < EL; ++j) x[i + j] = IO<BF>::ld(e, j);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x[i] = at(i, t) < C ? IO<BF>::ld(r, at(i, t)) : 0.f;
+        }
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t row, int C, int t, const float (&x)[EPT]) {
+        using E = typename IO<BF>::T;
+        E *r = reinterpret_cast<E *>(p) + row * C;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += EL) {
+                E e[EL];
+#pragma unroll
+                for (int j = 0; j < EL; ++j) IO<BF>::st(e, j, x[i + j]);
+                uint4 w;
+                __builtin_memcpy(&w, e, 16);
+                if (at(i, t) < C) *reinterpret_cast<uint4 *>(r + at(i, t)) = w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                if (at(i, t) < C) IO<BF>::st(r, at(i, t), x[i]);
+        }
+    }
+    // fp32 parameters (a row of C), or a constant where they are absent
+    static __device__ __forceinline__ void param(const float *p, int64_t g, int C, int t, float absent, float (&x)[EPT]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += 4) {
+                float4 w = make_float4(absent, absent, absent, absent);
+                if (p && at(i, t) < C) w = *reinterpret_cast<const float4 *>(p + g * C + at(i, t));
+                x[i] = w.x; x[i + 1] = w.y; x[i + 2] = w.z; x[i + 3] = w.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x[i] = p && at(i, t) < C ? p[g * C + at(i, t)] : absent;
+        }
+    }
+    static __device__ __forceinline__ void store_param(float *p, int64_t row, int C, int t, const float (&x)[EPT]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += 4)
+                if (at(i, t) < C)
+                    *reinterpret_cast<float4 *>(p + row * C + at(i, t)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                if (at(i, t) < C) p[row * C + at(i, t)] = x[i];
+        }
+    }
+};
+
+// Statistics of a row in registers: x becomes x - mean, the result is r.
+template <bool BF, bool VEC, int TPR, int NT, int EPT>
+__device__ __forceinline__ float normalise(float (&x)[EPT], int C, int t, int center, float eps, float *lds) {
+    using SL = Slice<BF, VEC, TPR, EPT>;
+    const float inv = 1.f / (float)C;
+    if (center) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) s[0] += x[i];  // elements past the row are 0
+        row_sums<TPR, NT>(s, lds);
+        const float mean = s[0] * inv;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) x[i] = SL::at(i, t) < C ? x[i] - mean : 0.f;
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) s[0] = fmaf(x[i], x[i], s[0]);
+    row_sums<TPR, NT>(s, lds);
+    return rsqrtf(s[0] * inv + eps);
+}
+
+template <bool BF, bool VEC, int TPR, int NT, int EPT>
+__global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict__ xp, const void *__restrict__ zp,
+                                                          const float *__restrict__ wp, const float *__restrict__ bp,
+                                                          void *__restrict__ yp, int64_t rows, int G, int C, float eps,
+                                                          int center) {
+    using SL = Slice<BF, VEC, TPR, EPT>;
+    constexpr int RPW = NT / TPR;
+    __shared__ float lds[NT / 64];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int64_t slot = (int64_t)blockIdx.x * RPW + sub, slots = (int64_t)gridDim.x * RPW;
+    float w[EPT], b[EPT];
+    SL::param(wp, slot % G, C, t, 1.f, w);
+    SL::param(bp, slot % G, C, t, 0.f, b);
+    const int64_t turns = (rows + slots - 1) / slots;  // the same for all threads: the sums hold barriers
+    for (int64_t i = 0; i < turns; ++i) {
+        const int64_t row = i * slots + slot;
+        const bool mine = row < rows;
+        float x[EPT], z[EPT];
+        SL::load(xp, mine ? row : 0, C, t, x);
+        if (zp) SL::load(zp, mine ? row : 0, C, t, z);
+        const float r = normalise<BF, VEC, TPR, NT>(x, C, t, center, eps, lds);
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            x[e] = fmaf(x[e] * r, w[e], b[e]);
+            if (zp) x[e] *= sigmoid_f(z[e]);
+        }
+        if (mine) SL::store(yp, row, C, t, x);
+    }
+}
+
+// part: [2][slots][C] fp32, the sums of e n and of e over the rows of each slot
+template <bool BF, bool VEC, int TPR, int NT, int EPT>
+__global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict__ dyp, const void *__restrict__ xp,
+                                                          const void *__restrict__ zp, const float *__restrict__ wp,
+                                                          const float *__restrict__ bp, void *__restrict__ dxp,
+                                                          void *__restrict__ dzp, float *__restrict__ part,
+                                                          int want_dw, int want_db, int64_t rows, int G, int C,
+                                                          float eps, int center) {
+    using SL = Slice<BF, VEC, TPR, EPT>;
+    constexpr int RPW = NT / TPR;
+    __shared__ float lds[2 * (NT / 64)];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int64_t slot = (int64_t)blockIdx.x * RPW + sub, slots = (int64_t)gridDim.x * RPW;
+    const float inv = 1.f / (float)C;
+    float w[EPT], b[EPT], dw[EPT], db[EPT];
+    SL::param(wp, slot % G, C, t, 1.f, w);
+    SL::param(bp, slot % G, C, t, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) dw[e] = db[e] = 0.f;
+    const int64_t turns = (rows + slots - 1) / slots;
+    for (int64_t i = 0; i < turns; ++i) {
+        const int64_t row = i * slots + slot;
+        const bool mine = row < rows;
+        float x[EPT], d[EPT], z[EPT];
+        SL::load(xp, mine ? row : 0, C, t, x);
+        SL::load(dyp, mine ? row : 0, C, t, d);
+        if (zp) SL::load(zp, mine ? row : 0, C, t, z);
+        const float r = normalise<BF, VEC, TPR, NT>(x, C, t, center, eps, lds);
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            x[e] *= r;  // n
+            if (zp) {
+                const float a = sigmoid_f(z[e]);
+                z[e] = d[e] * fmaf(x[e], w[e], b[e]) * a * (1.f - a);
+                d[e] *= a;
+            }
+            if (mine) {
+                dw[e] = fmaf(d[e], x[e], dw[e]);
+                db[e] += d[e];
+            }
+            d[e] *= w[e];
+            s[0] = fmaf(d[e], x[e], s[0]);
+            s[1] += d[e];
+        }
+        row_sums<TPR, NT>(s, lds);
+        const float m1 = s[0] * inv, m2 = center ? s[1] * inv : 0.f;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) x[e] = r * (d[e] - fmaf(x[e], m1, m2));
+        if (mine) {
+            SL::store(dxp, row, C, t, x);
+            if (zp) SL::store(dzp, row, C, t, z);
+        }
+    }
+    if (want_dw) SL::store_param(part, slot, C, t, dw);
+    if (want_db) SL::store_param(part + slots * C, slot, C, t, db);
+}
+
+// dw[g][c], db[g][c] = sum over the slots s with s % G == g, in order: 16 wavefronts take every 16th of them, then
+// one adds the wavefronts.
+__global__ __launch_bounds__(1024) void kda_norm_param_kernel(const float *__restrict__ part, float *__restrict__ dw,
+                                                              float *__restrict__ db, int64_t slots, int G, int C) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)G * C;
+    float *out = blockIdx.y ? db : dw;
+    if (!out) return;  // uniform
+    const float *p = part + (blockIdx.y ? slots * C : 0);
+    float a = 0.f;
+    if (col < cols) {
+        const int64_t n = slots / G;
+#pragma unroll 4
+        for (int64_t i = wave; i < n; i += 16) a += p[i * cols + col];
+    }
+    s[wave][lane] = a;
+    __syncthreads();
+    if (wave == 0 && col < cols) {
+#pragma unroll
+        for (int w = 1; w < 16; ++w) a += s[w][lane];
+        out[col] = a;
+    }
+}
+
+// Row slots of a grid over `rows` rows: workgroups times rows per workgroup, a multiple of G.
+int64_t grid_for(int64_t rows, int G, int rpw, int64_t most) {
+    int64_t a = G, b = rpw;
+    while (b) { const int64_t c = a % b; a = b; b = c; }
+    const int64_t step = G / a;  // workgroups whose slots are a multiple of G
+    int64_t wgs = (rows + rpw - 1) / rpw;
+    if (wgs > most) wgs = most;
+    wgs = (wgs + step - 1) / step * step;
+    return wgs;
+}
+
+template <bool BF, bool VEC, int TPR, int NT, int EPT>
+hipError_t run_norm(const NormArgs &a, bool bwd, hipStream_t st) {
+    constexpr int RPW = NT / TPR;
+    if (!bwd) {
+        const int64_t wgs = grid_for(a.rows, a.G, RPW, 2048);
+        hipLaunchKernelGGL((kda_norm_fwd_kernel<BF, VEC, TPR, NT, EPT>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.x,
+                           a.gate, a.weight, a.bias, a.y, a.rows, a.G, a.C, a.eps, (int)a.center);
+        return hipGetLastError();
+    }
+    const int64_t wgs = grid_for(a.rows, a.G, RPW, kMaxWG);
+    float *part = reinterpret_cast<float *>(a.workspace);
+    hipLaunchKernelGGL((kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.dy, a.x,
+                       a.gate, a.weight, a.bias, a.dx, a.dgate, part, (int)(a.dweight != nullptr),
+                       (int)(a.dbias != nullptr), a.rows, a.G, a.C, a.eps, (int)a.center);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
+    const int64_t cols = (int64_t)a.G * a.C;
+    hipLaunchKernelGGL(kda_norm_param_kernel, dim3((uint32_t)((cols + 63) / 64), 2), dim3(1024), 0, st, part,
+                       a.dweight, a.dbias, wgs * RPW, a.G, a.C);
+    return hipGetLastError();
+}
+
+template <bool BF, bool VEC>
+hipError_t by_width(const NormArgs &a, bool bwd, hipStream_t st) {
+    const int C = a.C;
+    if (C <= 8 * 8) return run_norm<BF, VEC, 8, 256, 8>(a, bwd, st);
+    if (C <= 16 * 8) return run_norm<BF, VEC, 16, 256, 8>(a, bwd, st);
+    if (C <= 64 * 8) return run_norm<BF, VEC, 64, 256, 8>(a, bwd, st);
+    if (C <= 256 * 8) return run_norm<BF, VEC, 256, 256, 8>(a, bwd, st);
+    if (C <= 256 * 16) return run_norm<BF, VEC, 256, 256, 16>(a, bwd, st);
+    if (C <= 512 * 16) return run_norm<BF, VEC, 512, 512, 16>(a, bwd, st);
+    return run_norm<BF, VEC, 1024, 1024, 16>(a, bwd, st);
+}
+hipError_t by_type(const NormArgs &a, bool bwd, hipStream_t st) {
+    if (a.io_bf16) return a.C % 8 == 0 ? by_width<true, true>(a, bwd, st) : by_width<true, false>(a, bwd, st);
+    return a.C % 4 == 0 ? by_width<false, true>(a, bwd, st) : by_width<false, false>(a, bwd, st);
+}
+
+}  // namespace
+
+size_t norm_bwd_workspace_bytes(int64_t rows, int32_t G, int32_t C) {
+    const int rpw = C <= 64 ? 32 : C <= 128 ? 16 : C <= 512 ? 4 : 1;  // NT / TPR of by_width
+    return (size_t)(grid_for(rows, G, rpw, kMaxWG) * rpw) * C * 2 * sizeof(float);
+}
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
+    return a.rows == 0 ? hipSuccess : by_type(a, false, st);
+}
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
+    if (a.rows == 0) {  // no rows: the parameters' gradients are zero
+        const int64_t cols = (int64_t)a.G * a.C;
+        if (!a.dweight && !a.dbias) return hipSuccess;
+        hipLaunchKernelGGL(kda_norm_param_kernel, dim3((uint32_t)((cols + 63) / 64), 2), dim3(1024), 0, st, nullptr,
+                           a.dweight, a.dbias, (int64_t)0, a.G, a.C);
+        return hipGetLastError();
+    }
+    return by_type(a, true, st);
+}
+
+}  // namespace kda
