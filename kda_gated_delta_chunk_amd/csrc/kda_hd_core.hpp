@@ -30,22 +30,29 @@
 namespace kda {
 namespace hd {
 
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
 // ------------------------------------------------------------------ rows in LDS
-// NCOL elements a row. bf16: 16-byte slots permuted within the row by its index, so that both the row reads (16 rows
-// at one slot) and the transposing reads (8 rows at two adjacent slots) of a half wavefront touch every bank once.
-// fp32: rows padded by 16 bytes to the same end.
+// NCOL elements a row. bf16: the 8-byte units of a row are permuted by an exclusive or with bits of the row's index,
+// chosen (r0..r3: the index's low bits) so that 16 rows at one unit (a row read's 16 lanes), those at two adjacent ones
+// (32 lanes), 4 rows at 4 adjacent units (a transposing read's 16 lanes) and 8 rows at 4 (32 lanes) all fall on
+// different banks, whatever the row's length adds. fp32: rows padded by 16 bytes to the same end.
 template <bool BF, int NCOL> struct Rows;
 template <int NCOL> struct Rows<true, NCOL> {
     static constexpr int NS = NCOL / 8, RB = NCOL * 2;
-    static constexpr int LB = NS == 16 ? 4 : NS == 8 ? 3 : 2;  // log2(NS)
     static constexpr int bytes(int rows) { return rows * RB; }
     static __device__ __forceinline__ int swz(int row) {
-        const int x = row >> (4 - LB);  // rows that share their banks
-        return ((x << 1) & (NS - 1)) | ((x >> (LB - 1)) & 1);
+        const int r0 = row & 1, r1 = (row >> 1) & 1, r2 = (row >> 2) & 1, r3 = (row >> 3) & 1;
+        if (NCOL == 128) return (r2 << 4) | (r1 << 3) | (r0 << 2) | (r3 << 1) | r2;
+        if (NCOL == 64) return (r1 << 3) | ((r0 ^ r2) << 2) | (r3 << 1) | r2;
+        return ((r1 ^ r2) << 2) | (r3 << 1) | r2;
     }
-    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + ((s ^ swz(row)) << 4); }
-    // column of four adjacent elements (a multiple of 4)
-    static __device__ __forceinline__ int quad(int row, int col) { return slot(row, col >> 3) + ((col & 4) << 1); }
+    static __device__ __forceinline__ int quad(int row, int col) { return row * RB + (((col >> 2) ^ swz(row)) << 3); }
+    // 16 bytes from column 8s on: two units that stay neighbours, in either order
+    static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
+        const int f = swz(row);
+        *reinterpret_cast<u32x4 *>(t + row * RB + ((s ^ (f >> 1)) << 4)) = (f & 1) ? u32x4{w.z, w.w, w.x, w.y} : w;
+    }
     // operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of one row per lane
     static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int row, int c, int g) {
         const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, 32 * c + 4 * g));
@@ -77,8 +84,10 @@ template <int NCOL> struct Rows<true, NCOL> {
 template <int NCOL> struct Rows<false, NCOL> {
     static constexpr int NS = NCOL / 4, RB = (NCOL + 4) * 4;
     static constexpr int bytes(int rows) { return rows * RB; }
-    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + (s << 4); }
     static __device__ __forceinline__ int quad(int row, int col) { return row * RB + col * 4; }
+    static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
+        *reinterpret_cast<u32x4 *>(t + row * RB + (s << 4)) = w;
+    }
     static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int row, int c, int g) {
         const float4 u = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 4 * g));
         const float4 w = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 16 + 4 * g));
@@ -103,18 +112,53 @@ template <int NCOL> struct Rows<false, NCOL> {
     }
 };
 
-// C rows of `n` valid ones from global memory (first row at p, `pitch` elements apart) into LDS; the others are zero.
+// C rows of a chunk on their way to LDS: `n` valid ones (the others are zero) from p, `pitch` elements apart. take()
+// issues the loads, put() waits for them: a chunk's rows travel while the one before it is worked on.
 template <bool BF, int NCOL, int C, int NT>
-__device__ __forceinline__ void load_rows(char *t, const typename IO<BF>::T *p, int64_t pitch, int n) {
-    constexpr int NS = Rows<BF, NCOL>::NS, EL = BF ? 8 : 4;
+struct Stage {
+    static constexpr int NS = Rows<BF, NCOL>::NS, EL = BF ? 8 : 4, NL = C * NS / NT;
     static_assert((C * NS) % NT == 0, "whole loads");
+    u32x4 w[NL];
+    __device__ __forceinline__ void take(const typename IO<BF>::T *p, int64_t pitch, int n) {
 #pragma unroll
-    for (int i = 0; i < C * NS / NT; ++i) {
-        const int e = threadIdx.x + i * NT, row = e / NS, s = e % NS;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (row < n) w = *reinterpret_cast<const uint4 *>(p + row * pitch + s * EL);
-        *reinterpret_cast<uint4 *>(t + Rows<BF, NCOL>::slot(row, s)) = w;
+        for (int i = 0; i < NL; ++i) {  // rows behind the last one load that one again
+            const int e = threadIdx.x + i * NT, row = e / NS, s = e % NS;
+            w[i] = *reinterpret_cast<const u32x4 *>(p + (row < n ? row : n - 1) * pitch + s * EL);
+        }
     }
+    __device__ __forceinline__ void put(char *t, int n) const {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = threadIdx.x + i * NT, row = e / NS;
+            Rows<BF, NCOL>::put16(t, row, e % NS, row < n ? w[i] : u32x4{0, 0, 0, 0});
+        }
+    }
+};
+
+// Sums of a chunk's log-decays (base 2) over the lanes 0 .. C-1 of a wavefront: exact whole multiples of 2^-8 (at most
+// 64 * 151 in size: 22 bits) and a rest of at most 2^-3, each summed in fp32.
+struct Decay { float hi, lo; };
+__device__ __forceinline__ Decay decay_base2(float g) {
+    g = g < -104.f ? -104.f : g;  // e^-104 is 0 in fp32; NaN stays
+    constexpr float L2E = 1.4426950408889634f, L2E_LO = 1.9259629911266175e-8f;  // log2(e) in two parts
+    const float x = g * L2E, rest = fmaf(g, L2E, -x) + g * L2E_LO;
+    const float hi = rintf(x * 256.f) * 0.00390625f;
+    return Decay{hi, (x - hi) + rest};
+}
+template <int C>
+__device__ __forceinline__ Decay decay_scan(Decay d, int lane) {
+    d.hi = row_scan16(d.hi);
+    d.lo = row_scan16(d.lo);
+#pragma unroll
+    for (int w = 16; w < C; w <<= 1) {
+        const int from = (lane & ~(2 * w - 1)) + w - 1;  // the last lane of the lower half
+        const float h = __shfl(d.hi, from), l = __shfl(d.lo, from);
+        if (lane & w) {
+            d.hi += h;
+            d.lo += l;
+        }
+    }
+    return d;
 }
 
 // Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
@@ -158,8 +202,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
     __shared__ __align__(16) char s_b[SZ_K], s_c[SZ_V];
     __shared__ __align__(16) char s_a[INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
     __shared__ __align__(16) char s_x[DG && REV ? SZ_V : 16];
-    __shared__ __align__(16) float s_win[C], s_wup[C], s_bh[C], s_bl[C];
-    __shared__ float s_ec;
+    __shared__ __align__(16) float s_win2[2][C], s_wup2[2][C], s_bh2[2][C], s_bl2[2][C];
+    __shared__ float s_ec2[2];
     __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
     (void)s_pl; (void)s_x; (void)s_u; (void)s_red;
 
@@ -238,45 +282,67 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
             if constexpr (PLO) reinterpret_cast<uint4 *>(s_pl)[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    double btot = 0.0;  // lane 0 of wavefront 0
+    const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
+    const E *px = reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD;
+    float btot = 0.f;
+    auto chunk_at = [&](int i, int64_t &tc, int &n) __attribute__((always_inline)) {  // its first token and how many
+        tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
+        n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
+    };
+    // wavefront 0 keeps the decays: a token's log-decay per lane, two chunks ahead; their sums and weights, one ahead
+    auto take_decay = [&](int i) __attribute__((always_inline)) -> float {
+        int64_t tc;
+        int n;
+        chunk_at(i, tc, n);
+        if (lane >= n) return 0.f;
+        return A.g_head ? reinterpret_cast<const float *>(A.g)[h]
+                        : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
+    };
+    auto put_decay = [&](float gv, int buf) __attribute__((always_inline)) {
+        const Decay d = decay_scan<C>(decay_base2(gv), lane);
+        const float hc = __shfl(d.hi, C - 1), lc2 = __shfl(d.lo, C - 1);
+        if (lane < C) {
+            s_bh2[buf][lane] = d.hi;
+            s_bl2[buf][lane] = d.lo;
+            const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
+            const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
+            s_win2[buf][lane] = (REV ? eout : ein) * A.s_inter;
+            s_wup2[buf][lane] = (REV ? ein : eout) * A.s_up;
+        }
+        if (lane == 0) s_ec2[buf] = __builtin_amdgcn_exp2f(hc + lc2);
+        if constexpr (INC) btot += hc + lc2;
+    };
+    Stage<BF, KD, C, NT> ra, rb;
+    Stage<BF, VT, C, NT> rc, rx;
+    auto take_rows = [&](int i) __attribute__((always_inline)) {
+        int64_t tc;
+        int n;
+        chunk_at(i, tc, n);
+        if constexpr (!INC) ra.take(pa + tc * la, la, n);
+        rb.take(pb + tc * lb, lb, n);
+        rc.take(pc + tc * lc, lc, n);
+        if constexpr (DG && REV) rx.take(px + vt * VT + tc * lx, lx, n);
+    };
+    float gnext = 0.f;
+    if (nch > 0) {
+        take_rows(0);
+        if (wave == 0) {
+            put_decay(take_decay(0), 0);
+            if (nch > 1) gnext = take_decay(1);
+        }
+    }
 
     for (int cc = 0; cc < nch; ++cc) {
-        const int64_t tc = sg.t0 + (int64_t)(REV ? nch - 1 - cc : cc) * C;
-        const int n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
+        int64_t tc;
+        int n;
+        chunk_at(cc, tc, n);
+        const float *s_win = s_win2[cc & 1], *s_wup = s_wup2[cc & 1], *s_bh = s_bh2[cc & 1], *s_bl = s_bl2[cc & 1];
         __syncthreads();  // the last chunk's reads are done
-        if constexpr (!INC) load_rows<BF, KD, C, NT>(s_a, pa + tc * la, la, n);
-        load_rows<BF, KD, C, NT>(s_b, pb + tc * lb, lb, n);
-        load_rows<BF, VT, C, NT>(s_c, pc + tc * lc, lc, n);
-        if constexpr (DG && REV) {
-            const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
-            load_rows<BF, VT, C, NT>(s_x, reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD + vt * VT + tc * lx,
-                                     lx, n);
-        }
-        if (wave == 0) {  // the chunk's decays: sums in fp64, in base 2
-            double x = 0.0;
-            if (lane < n) {
-                float gv = A.g_head ? reinterpret_cast<const float *>(A.g)[h]
-                                    : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
-                gv = gv < -104.f ? -104.f : gv;  // e^-104 is 0 in fp32; NaN stays
-                x = (double)gv * 1.4426950408889634;
-            }
-#pragma unroll
-            for (int d = 1; d < C; d <<= 1) {
-                const double y = __shfl_up(x, d);
-                if (lane >= d) x += y;
-            }
-            const double xc = __shfl(x, C - 1);
-            if (lane < C) {
-                const double f = floor(x);
-                s_bh[lane] = (float)f;
-                s_bl[lane] = (float)(x - f);
-                const float ein = __builtin_amdgcn_exp2f((float)x), eout = __builtin_amdgcn_exp2f((float)(xc - x));
-                s_win[lane] = (REV ? eout : ein) * A.s_inter;
-                s_wup[lane] = (REV ? ein : eout) * A.s_up;
-            }
-            if (lane == 0) s_ec = __builtin_amdgcn_exp2f((float)xc);
-            if constexpr (INC) btot += xc;
-        }
+        if constexpr (!INC) ra.put(s_a, n);
+        rb.put(s_b, n);
+        rc.put(s_c, n);
+        if constexpr (DG && REV) rx.put(s_x, n);
+        if (cc + 1 < nch) take_rows(cc + 1);
         __syncthreads();
 
         // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
@@ -367,8 +433,6 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 }
             if constexpr (DG) {
                 // the state's share of a token in its log-decay: x_t . y_t over this workgroup's columns
-                const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
-                const E *px = reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD + col0 + 4 * g;
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
                     const int t = 16 * tt + li;
@@ -379,7 +443,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                         if constexpr (REV) {
                             RV::load_quad(s_x, t, wave * CT * 16 + 16 * ct + 4 * g, x);
                         } else if (t < n) {
-                            const E *p = px + (tc + t) * lx + 16 * ct;
+                            const E *p = px + col0 + 4 * g + (tc + t) * lx + 16 * ct;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) x[i] = IO<BF>::ld(p, i);
                         }
@@ -419,8 +483,12 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 if constexpr (REV) carry += __shfl(u, 0);
             }
         }
+        if (wave == 0 && cc + 1 < nch) {  // the next chunk's decays, and the loads of those behind it
+            put_decay(gnext, (cc + 1) & 1);
+            if (cc + 2 < nch) gnext = take_decay(cc + 2);
+        }
         // ---- the chunk's own products, and the state's update
-        const float ec = s_ec;
+        const float ec = s_ec2[cc & 1];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -488,7 +556,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 for (int i = 0; i < 4; ++i)
                     so[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
     }
-    if (INC && threadIdx.x == 0 && vt == 0) A.seg_decay[slot * A.H + h] = (float)btot;
+    if (INC && threadIdx.x == 0 && vt == 0) A.seg_decay[slot * A.H + h] = btot;
 }
 
 template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
