@@ -13,7 +13,7 @@ namespace kda {
 namespace hd {
 namespace {
 
-constexpr int kWantedGroups = 768;  // workgroups of a pass that fill 256 CUs evenly
+constexpr int64_t kResident = 512;  // workgroups of the chunk kernel that run at a time: two per CU
 constexpr int64_t kLeastSegment = 256;
 
 struct Plan {
@@ -24,26 +24,33 @@ struct Plan {
     int vk, vv;         // column tile over K and over V columns
 };
 
-int tile_of(int cols) { return cols < 64 ? cols : 64; }
+int tile_of(int cols, bool bf16) { return bf16 || cols < 64 ? cols : 64; }
 
 int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
 
-Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool packed) {
+// How long a call with n segments per row takes, in tokens of one workgroup: its rounds over the chip's resident
+// workgroups; with several segments also the increments' rounds (about a third of the work), two more launches and the
+// states' traffic.
+int64_t cost(int64_t rows, int64_t T, int64_t n) {
+    const int64_t seg = round64((T + n - 1) / n);
+    int64_t c = (rows * n + kResident - 1) / kResident * seg;
+    if (n > 1) c += (rows * (n - 1) + kResident - 1) / kResident * seg / 3 + 100 + rows * n / 3;
+    return c;
+}
+
+Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool packed, bool bf16) {
     Plan p;
-    p.vk = tile_of(K);
-    p.vv = tile_of(V);
-    const int64_t per_token = (int64_t)H * (V / p.vv);
-    const int64_t groups = packed ? 1 : B * per_token;  // packed: one sequence may be nearly all of the batch
+    p.vk = tile_of(K, bf16);
+    p.vv = tile_of(V, bf16);
     const int64_t whole = round64(T > 0 ? T : 1);
-    int64_t seg = whole;
-    if (groups < kWantedGroups / 2) {
-        seg = round64((B * T * per_token + kWantedGroups - 1) / kWantedGroups);
-        if (seg < kLeastSegment) seg = kLeastSegment;
-        if (seg > whole) seg = whole;
-    }
-    p.seg = seg;
-    p.nseg = (int32_t)(T > 0 ? (T + seg - 1) / seg : 1);
-    p.slots = packed ? T / seg + N : B * p.nseg;
+    // workgroups of one segment per row (packed: one sequence may be nearly all of the batch)
+    const int64_t rows = (packed ? 1 : B) * H * (V / p.vv);
+    int64_t best = 1;
+    for (int64_t n = 2; n <= whole / kLeastSegment && rows * (n - 1) < 2 * kResident; ++n)
+        if (cost(rows, whole, n) < cost(rows, whole, best)) best = n;
+    p.seg = round64((whole + best - 1) / best);
+    p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
+    p.slots = packed ? T / p.seg + N : B * p.nseg;
     p.several = p.nseg > 1;
     return p;
 }
@@ -248,7 +255,7 @@ struct Call {
 Call prepare(const HdArgs &a, bool bwd) {
     Call c;
     const bool packed = a.cu_seqlens != nullptr;
-    c.p = plan(a.B, a.T, a.H, a.K, a.V, a.num_seqs, packed);
+    c.p = plan(a.B, a.T, a.H, a.K, a.V, a.num_seqs, packed, a.io_bf16);
     c.l = layout(c.p, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd);
     c.ws = reinterpret_cast<char *>(a.workspace);
     c.table = packed ? reinterpret_cast<const Segment *>(c.ws + c.l.table) : nullptr;
@@ -299,13 +306,13 @@ hipError_t forward_states(const HdArgs &a, const Call &c, hipStream_t st) {
 }  // namespace hd
 
 size_t hd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
-                              bool packed, bool) {
-    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed);
+                              bool packed, bool io_bf16) {
+    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16);
     return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, false).total;
 }
 size_t hd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
-                              bool packed, bool) {
-    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed);
+                              bool packed, bool io_bf16) {
+    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16);
     return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, true).total;
 }
 

@@ -31,6 +31,9 @@ namespace kda {
 namespace hd {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
+constexpr int kChunk = 32;  // tokens per chunk
 
 // ------------------------------------------------------------------ rows in LDS
 // NCOL elements a row. bf16: the 8-byte units of a row are permuted by an exclusive or with bits of the row's index,
@@ -50,8 +53,9 @@ template <int NCOL> struct Rows<true, NCOL> {
     static __device__ __forceinline__ int quad(int row, int col) { return row * RB + (((col >> 2) ^ swz(row)) << 3); }
     // 16 bytes from column 8s on: two units that stay neighbours, in either order
     static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
-        const int f = swz(row);
-        *reinterpret_cast<u32x4 *>(t + row * RB + ((s ^ (f >> 1)) << 4)) = (f & 1) ? u32x4{w.z, w.w, w.x, w.y} : w;
+        const int at = quad(row, 8 * s);
+        *reinterpret_cast<u32x2 *>(t + at) = u32x2{w.x, w.y};
+        *reinterpret_cast<u32x2 *>(t + (at ^ 8)) = u32x2{w.z, w.w};
     }
     // operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of one row per lane
     static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int row, int c, int g) {
@@ -116,21 +120,36 @@ template <int NCOL> struct Rows<false, NCOL> {
 // issues the loads, put() waits for them: a chunk's rows travel while the one before it is worked on.
 template <bool BF, int NCOL, int C, int NT>
 struct Stage {
-    static constexpr int NS = Rows<BF, NCOL>::NS, EL = BF ? 8 : 4, NL = C * NS / NT;
-    static_assert((C * NS) % NT == 0, "whole loads");
+    static constexpr int NS = Rows<BF, NCOL>::NS, EB = BF ? 2 : 4, RL = NT / NS;  // rows per round of loads
+    static constexpr int NL = C > RL ? C / RL : 1;
+    static_assert(NT % NS == 0 && C % (RL < C ? RL : C) == 0, "whole rounds of whole rows");
     u32x4 w[NL];
+    // A full chunk's addresses are one lane offset (under 2^32: 64 rows) from bases that all lanes share.
     __device__ __forceinline__ void take(const typename IO<BF>::T *p, int64_t pitch, int n) {
+        const int row = threadIdx.x / NS, s = threadIdx.x % NS;
+        const char *base = reinterpret_cast<const char *>(p);
+        if (n == C) {
+            const uint32_t off = (uint32_t)(RL > C ? row & (C - 1) : row) * (uint32_t)(pitch * EB) + (uint32_t)s * 16;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {  // rows behind the last one load that one again
-            const int e = threadIdx.x + i * NT, row = e / NS, s = e % NS;
-            w[i] = *reinterpret_cast<const u32x4 *>(p + (row < n ? row : n - 1) * pitch + s * EL);
+            for (int i = 0; i < NL; ++i) w[i] = *reinterpret_cast<const u32x4 *>(base + i * RL * pitch * EB + off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {  // rows behind the last one load that one again
+                const int r = row + i * RL;
+                w[i] = *reinterpret_cast<const u32x4 *>(base + (r < n ? r : n - 1) * pitch * EB + s * 16);
+            }
         }
     }
     __device__ __forceinline__ void put(char *t, int n) const {
+        const int row = threadIdx.x / NS, s = threadIdx.x % NS;
+        if (RL > C && row >= C) return;
+        if (n == C) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int e = threadIdx.x + i * NT, row = e / NS;
-            Rows<BF, NCOL>::put16(t, row, e % NS, row < n ? w[i] : u32x4{0, 0, 0, 0});
+            for (int i = 0; i < NL; ++i) Rows<BF, NCOL>::put16(t, row + i * RL, s, w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                Rows<BF, NCOL>::put16(t, row + i * RL, s, row + i * RL < n ? w[i] : u32x4{0, 0, 0, 0});
         }
     }
 };
@@ -145,10 +164,9 @@ __device__ __forceinline__ Decay decay_base2(float g) {
     const float hi = rintf(x * 256.f) * 0.00390625f;
     return Decay{hi, (x - hi) + rest};
 }
+// d: the sums within a tile of 16 tokens on entry
 template <int C>
-__device__ __forceinline__ Decay decay_scan(Decay d, int lane) {
-    d.hi = row_scan16(d.hi);
-    d.lo = row_scan16(d.lo);
+__device__ __forceinline__ Decay decay_join(Decay d, int lane) {
 #pragma unroll
     for (int w = 16; w < C; w <<= 1) {
         const int from = (lane & ~(2 * w - 1)) + w - 1;  // the last lane of the lower half
@@ -160,6 +178,8 @@ __device__ __forceinline__ Decay decay_scan(Decay d, int lane) {
     }
     return d;
 }
+// Sum over the 16 lanes of a row, in its last lane.
+__device__ __forceinline__ float row_sum_last(float x) { return row_scan16(x); }
 
 // Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
 __device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<true> &hi, Frag8<true> &lo) {
@@ -187,25 +207,45 @@ __device__ __forceinline__ void scaled_frags(const Frag8<false> &c, const float 
     for (int i = 0; i < 8; ++i) f[0].f[i] = c.f[i] * w[i];
 }
 
+// One wait for a whole register tile of products (see mfma_fence).
+template <int M, int N>
+__device__ __forceinline__ void mfma_fence_state(f32x4 (&x)[M][N]) {
+    if constexpr (M * N <= 4) {
+        f32x4 *f = &x[0][0];
+        if constexpr (M * N == 2) mfma_fence(f[0], f[1]);
+        else mfma_fence(f[0], f[1], f[2], f[3]);
+    } else {
+        f32x4 *f = &x[0][0];
+#pragma unroll
+        for (int i = 0; i < M * N; i += 8)
+            asm volatile("s_nop 7\n\ts_nop 7"
+                         : "+v"(f[i]), "+v"(f[i + 1]), "+v"(f[i + 2]), "+v"(f[i + 3]), "+v"(f[i + 4]), "+v"(f[i + 5]),
+                           "+v"(f[i + 6]), "+v"(f[i + 7]));
+    }
+}
+
 template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG>
 __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs A) {
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
-    constexpr int C = BF ? 64 : 32, TT = C / 16, SC = C / 32;  // tokens per chunk; token tiles; 32-token steps
+    constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
+    constexpr int DW = NW - 1;                            // the wavefront that keeps the decays
     constexpr int NPART = BF ? 3 : 1;
-    constexpr bool PLO = BF, SLO = BF && DG;
+    constexpr bool PLO = BF && DG, SLO = BF && DG;
     static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
     using E = typename IO<BF>::T;
     using RK = Rows<BF, KD>;
     using RV = Rows<BF, VT>;
     using RP = Rows<BF, C>;
     constexpr int SZ_K = RK::bytes(C), SZ_V = RV::bytes(C), SZ_P = RP::bytes(C);
-    __shared__ __align__(16) char s_b[SZ_K], s_c[SZ_V];
-    __shared__ __align__(16) char s_a[INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
-    __shared__ __align__(16) char s_x[DG && REV ? SZ_V : 16];
-    __shared__ __align__(16) float s_win2[2][C], s_wup2[2][C], s_bh2[2][C], s_bl2[2][C];
+    // bf16: rows twice, the next chunk's arrive while this one's are read (fp32's would leave one workgroup per CU)
+    constexpr int NB = BF ? 2 : 1;
+    __shared__ __align__(16) char s_b2[NB][SZ_K], s_c2[NB][SZ_V];
+    __shared__ __align__(16) char s_a2[NB][INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
+    __shared__ __align__(16) char s_x2[NB][DG && REV ? SZ_V : 16];
+    __shared__ __align__(16) float s_win2[2][C], s_wup2[2][C], s_bh2[2][C], s_bl2[2][C], s_f2[2][C];
     __shared__ float s_ec2[2];
     __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
-    (void)s_pl; (void)s_x; (void)s_u; (void)s_red;
+    (void)s_pl; (void)s_x2; (void)s_u; (void)s_red;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
     // tiles of one (segment, head) sit 8 workgroups apart: the same XCD, whose L2 then holds their common rows
@@ -289,7 +329,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
         n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
     };
-    // wavefront 0 keeps the decays: a token's log-decay per lane, two chunks ahead; their sums and weights, one ahead
+    // one wavefront keeps the decays: a token's log-decay per lane, two chunks ahead; their sums and weights, one ahead
     auto take_decay = [&](int i) __attribute__((always_inline)) -> float {
         int64_t tc;
         int n;
@@ -299,11 +339,18 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                         : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
     };
     auto put_decay = [&](float gv, int buf) __attribute__((always_inline)) {
-        const Decay d = decay_scan<C>(decay_base2(gv), lane);
+        Decay d = decay_base2(gv);
+        d.hi = row_scan16(d.hi);
+        d.lo = row_scan16(d.lo);
+        // a source's weight up to its tile's edge on the output's side
+        const float f = REV ? __builtin_amdgcn_exp2f(d.hi + d.lo)
+                            : __builtin_amdgcn_exp2f((row_last(d.hi) - d.hi) + (row_last(d.lo) - d.lo));
+        d = decay_join<C>(d, lane);
         const float hc = __shfl(d.hi, C - 1), lc2 = __shfl(d.lo, C - 1);
         if (lane < C) {
             s_bh2[buf][lane] = d.hi;
             s_bl2[buf][lane] = d.lo;
+            s_f2[buf][lane] = f * A.s_intra;
             const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
             const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
             s_win2[buf][lane] = (REV ? eout : ein) * A.s_inter;
@@ -323,12 +370,26 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         rc.take(pc + tc * lc, lc, n);
         if constexpr (DG && REV) rx.take(px + vt * VT + tc * lx, lx, n);
     };
+    auto put_rows = [&](int i) __attribute__((always_inline)) {
+        int64_t tc;
+        int n;
+        chunk_at(i, tc, n);
+        const int j = i & (NB - 1);
+        if constexpr (!INC) ra.put(s_a2[j], n);
+        rb.put(s_b2[j], n);
+        rc.put(s_c2[j], n);
+        if constexpr (DG && REV) rx.put(s_x2[j], n);
+    };
     float gnext = 0.f;
     if (nch > 0) {
         take_rows(0);
-        if (wave == 0) {
+        if (wave == DW) {
             put_decay(take_decay(0), 0);
             if (nch > 1) gnext = take_decay(1);
+        }
+        if constexpr (NB == 2) {
+            put_rows(0);
+            if (nch > 1) take_rows(1);
         }
     }
 
@@ -336,14 +397,26 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         int64_t tc;
         int n;
         chunk_at(cc, tc, n);
-        const float *s_win = s_win2[cc & 1], *s_wup = s_wup2[cc & 1], *s_bh = s_bh2[cc & 1], *s_bl = s_bl2[cc & 1];
-        __syncthreads();  // the last chunk's reads are done
-        if constexpr (!INC) ra.put(s_a, n);
-        rb.put(s_b, n);
-        rc.put(s_c, n);
-        if constexpr (DG && REV) rx.put(s_x, n);
-        if (cc + 1 < nch) take_rows(cc + 1);
-        __syncthreads();
+        const int buf = cc & 1, rbuf = cc & (NB - 1);
+        const float *s_win = s_win2[buf], *s_wup = s_wup2[buf], *s_bh = s_bh2[buf], *s_bl = s_bl2[buf], *s_f = s_f2[buf];
+        const char *s_a = s_a2[rbuf], *s_b = s_b2[rbuf], *s_c = s_c2[rbuf], *s_x = s_x2[rbuf];
+        (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
+        __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
+        if constexpr (NB == 1) {
+            put_rows(cc);
+            if (cc + 1 < nch) take_rows(cc + 1);
+            __syncthreads();
+        }
+        if (cc + 1 < nch) {
+            if constexpr (NB == 2) {
+                put_rows(cc + 1);
+                if (cc + 2 < nch) take_rows(cc + 2);
+            }
+            if (wave == DW) {  // the next chunk's decays, and the loads of those behind it
+                put_decay(gnext, buf ^ 1);
+                if (cc + 2 < nch) gnext = take_decay(cc + 2);
+            }
+        }
 
         // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
         if constexpr (!INC) {
@@ -366,24 +439,35 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 mfma_fence(acc, acd);
                 const int t = 16 * tt + li;
                 const float th = s_bh[t], tl = s_bl[t];
-                float w[4], csum = 0.f;
+                float w[4];
+                if (tt == ts) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s = 16 * ts + 4 * g + i;
-                    const float d = REV ? (s_bh[s] - th) + (s_bl[s] - tl) : (th - s_bh[s]) + (tl - s_bl[s]);
-                    const bool in_past = REV ? s >= t : s <= t;
-                    w[i] = in_past ? acc[i] * (__builtin_amdgcn_exp2f(d) * A.s_intra) : 0.f;
-                    if constexpr (DG && REV) {
-                        // pair (row s, column t) of the log-decays' gradient: + at its row, - at its column
-                        const float X = in_past ? w[i] * acd[i] : 0.f;
-                        csum += X;
-                        float r = X;
-#pragma unroll
-                        for (int m = 8; m >= 1; m >>= 1) r += __shfl_xor(r, m);
-                        if (li == 0) s_u[wave][s] += r;
+                    for (int i = 0; i < 4; ++i) {
+                        const int s = 16 * ts + 4 * g + i;
+                        const float d = REV ? (s_bh[s] - th) + (s_bl[s] - tl) : (th - s_bh[s]) + (tl - s_bl[s]);
+                        const bool in_past = REV ? s >= t : s <= t;
+                        w[i] = in_past ? acc[i] * (__builtin_amdgcn_exp2f(d) * A.s_intra) : 0.f;
+                        if constexpr (DG && REV) acd[i] = in_past ? acd[i] : 0.f;
                     }
+                } else {
+                    // over the edge between the tiles: the source's weight up to it, the output's from there
+                    const int e = REV ? 16 * ts - 1 : 16 * ts + 15;
+                    const float f = __builtin_amdgcn_exp2f(REV ? (s_bh[e] - th) + (s_bl[e] - tl)
+                                                               : (th - s_bh[e]) + (tl - s_bl[e]));
+                    const f32x4 fs = *reinterpret_cast<const f32x4 *>(s_f + 16 * ts + 4 * g);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = acc[i] * (f * fs[i]);
                 }
                 if constexpr (DG && REV) {
+                    // pairs (row s, column t) of the log-decays' gradient: + at the row, - at the column
+                    float csum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float X = w[i] * acd[i];
+                        csum += X;
+                        const float r = row_sum_last(X);
+                        if (li == 15) s_u[wave][16 * ts + 4 * g + i] += r;
+                    }
                     csum += __shfl_xor(csum, 16);
                     csum += __shfl_xor(csum, 32);
                     __builtin_amdgcn_wave_barrier();
@@ -424,13 +508,13 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                     }
                 }
             }
+            mfma_fence_all(y);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int tt = 0; tt < TT; ++tt) {
+                const float w = s_win[16 * tt + li];
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
-                    mfma_fence(y[ct][tt]);
-                    y[ct][tt] *= s_win[16 * tt + li];
-                }
+                for (int ct = 0; ct < CT; ++ct) y[ct][tt] *= w;
+            }
             if constexpr (DG) {
                 // the state's share of a token in its log-decay: x_t . y_t over this workgroup's columns
 #pragma unroll
@@ -459,7 +543,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 }
             }
         }
-        __syncthreads();  // the weighted products (and the shares) of every wavefront are there
+        if constexpr (!INC) __syncthreads();  // the weighted products (and the shares) of every wavefront are there
 
         if constexpr (DG) {
             if (wave == 0 && lane < C) {
@@ -483,12 +567,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 if constexpr (REV) carry += __shfl(u, 0);
             }
         }
-        if (wave == 0 && cc + 1 < nch) {  // the next chunk's decays, and the loads of those behind it
-            put_decay(gnext, (cc + 1) & 1);
-            if (cc + 2 < nch) gnext = take_decay(cc + 2);
-        }
         // ---- the chunk's own products, and the state's update
-        const float ec = s_ec2[cc & 1];
+        const float ec = s_ec2[buf];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -521,27 +601,27 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                     for (int q = 0; q < NPART; ++q) st[kt][ct] = mma32(st[kt][ct], bf, cw[ct][q]);
             }
         }
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) mfma_fence(st[kt][ct]);
         if constexpr (!INC) {
+            mfma_fence_all(y);
+            // a lane's offset within the chunk (under 2^32: 64 rows) from bases that all lanes share
+            const uint32_t lane_off = (uint32_t)li * (uint32_t)(A.H * A.VD) + (uint32_t)(col0 + 4 * g);
+            const int64_t base = (tc * A.H + h) * A.VD;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int tt = 0; tt < TT; ++tt) {
+                if (16 * tt + li >= n) continue;
+                const int64_t row = base + (int64_t)(16 * tt) * A.H * A.VD;
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
-                    mfma_fence(y[ct][tt]);
-                    const int t = 16 * tt + li;
-                    if (t >= n) continue;
+                for (int ct = 0; ct < CT; ++ct) {
                     const f32x4 v = y[ct][tt];
-                    const int64_t at = ((tc + t) * A.H + h) * A.VD + col0 + 16 * ct + 4 * g;
                     if (BF && !A.y_fp32)
-                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(A.y) + at) =
-                            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                        *reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(A.y) + row * 2 + lane_off * 2u + 32 * ct) =
+                            u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
                     else
-                        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.y) + at) = make_float4(v.x, v.y, v.z, v.w);
+                        *reinterpret_cast<f32x4 *>(reinterpret_cast<char *>(A.y) + row * 4 + lane_off * 4u + 64 * ct) = v;
                 }
+            }
         }
+        mfma_fence_state(st);
     }
     // ---- the state at the other end
     float *so = nullptr;
@@ -556,7 +636,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 for (int i = 0; i < 4; ++i)
                     so[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
     }
-    if (INC && threadIdx.x == 0 && vt == 0) A.seg_decay[slot * A.H + h] = btot;
+    if (INC && threadIdx.x == DW * 64 && vt == 0) A.seg_decay[slot * A.H + h] = btot;
 }
 
 template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
@@ -582,7 +662,11 @@ hipError_t launch_kind(const CoreArgs &a, Kind k, hipStream_t st) {
 }
 template <bool BF, int KD>
 hipError_t launch_vt(const CoreArgs &a, int vt, Kind k, hipStream_t st) {
-    return vt == 32 ? launch_kind<BF, KD, 32>(a, k, st) : launch_kind<BF, KD, 64>(a, k, st);
+    switch (vt) {
+        case 32: return launch_kind<BF, KD, 32>(a, k, st);
+        case 64: return launch_kind<BF, KD, 64>(a, k, st);
+        default: return launch_kind<BF, KD, 128>(a, k, st);
+    }
 }
 template <bool BF>
 hipError_t launch_core(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st) {

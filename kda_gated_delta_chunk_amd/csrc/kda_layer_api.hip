@@ -62,7 +62,8 @@ kda_status_t check_hd_sizes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t
     // element counts; cu_seqlens and a sequence's chunks are 32-bit; workgroups of a pass (at most one per 256 tokens
     // of a sequence, head and 32 columns) stay launchable
     if (T >= ((int64_t)1 << 31) || T > kMaxElems / B || B * T > kMaxElems / H / 512) return KDA_ERROR_INVALID_VALUE;
-    if ((int64_t)num_seqs * H >= ((int64_t)1 << 26)) return KDA_ERROR_INVALID_VALUE;
+    // 64 tokens of all heads stay below 2^32 bytes (the kernels' offsets within a chunk)
+    if (H >= (1 << 16) || (int64_t)num_seqs * H >= ((int64_t)1 << 26)) return KDA_ERROR_INVALID_VALUE;
     if ((B * ((T + 255) / 256) + num_seqs) > ((int64_t)1 << 28) / H) return KDA_ERROR_INVALID_VALUE;
     return KDA_SUCCESS;
 }
