@@ -26,6 +26,9 @@ struct Plan {
 
 int tile_of(int cols, bool bf16) { return bf16 || cols < 64 ? cols : 64; }
 
+// The increment passes have no weighted products to share, only the rows b: narrower tiles, more workgroups.
+int inc_tile_of(int cols) { return cols < 64 ? cols : 64; }
+
 int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
 
 // How long a call with n segments per row takes, in tokens of one workgroup: its rounds over the chip's resident
@@ -298,7 +301,8 @@ hipError_t forward_states(const HdArgs &a, const Call &c, hipStream_t st) {
     x.c = a.v;
     x.s_inc = reinterpret_cast<float *>(c.ws + c.l.seg);
     x.seg_decay = reinterpret_cast<float *>(c.ws + c.l.decay);
-    KDA_TRY(core(a, x, a.K, c.p.vv, Kind::fwd_inc, st));
+    x.tiles = a.V / inc_tile_of(a.V);
+    KDA_TRY(core(a, x, a.K, inc_tile_of(a.V), Kind::fwd_inc, st));
     return launch_carry(x.s_inc, x.seg_decay, a.S0, c.seqs, c.p, a, false, st);
 }
 
@@ -350,7 +354,8 @@ hipError_t launch_hd_bwd(const HdArgs &a, hipStream_t st) {
         x.s_up = a.scale;
         x.s_inc = dseg;
         x.seg_decay = reinterpret_cast<float *>(c.ws + c.l.ddecay);
-        KDA_TRY(core(a, x, a.K, c.p.vv, Kind::rev_inc, st));
+        x.tiles = a.V / inc_tile_of(a.V);
+        KDA_TRY(core(a, x, a.K, inc_tile_of(a.V), Kind::rev_inc, st));
         KDA_TRY(launch_carry(dseg, x.seg_decay, a.dS_final, c.seqs, c.p, a, true, st));
     }
     const bool grouped = group > 1;

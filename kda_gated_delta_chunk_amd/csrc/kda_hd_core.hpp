@@ -116,41 +116,30 @@ template <int NCOL> struct Rows<false, NCOL> {
     }
 };
 
-// C rows of a chunk on their way to LDS: `n` valid ones (the others are zero) from p, `pitch` elements apart. take()
-// issues the loads, put() waits for them: a chunk's rows travel while the one before it is worked on.
+// C rows of a chunk on their way to LDS: from p, `pitch` bytes apart; rows behind the last of `n` repeat it (their
+// weights are zero). take() issues the loads, put() waits for them: a chunk's rows travel while the one before it is
+// worked on. A lane's offsets (under 2^32: 64 rows) grow with the row, so holding them to the last row's is a minimum;
+// the base is the same for all lanes.
 template <bool BF, int NCOL, int C, int NT>
 struct Stage {
-    static constexpr int NS = Rows<BF, NCOL>::NS, EB = BF ? 2 : 4, RL = NT / NS;  // rows per round of loads
+    static constexpr int NS = Rows<BF, NCOL>::NS, RL = NT / NS;  // rows per round of loads
     static constexpr int NL = C > RL ? C / RL : 1;
     static_assert(NT % NS == 0 && C % (RL < C ? RL : C) == 0, "whole rounds of whole rows");
     u32x4 w[NL];
-    // A full chunk's addresses are one lane offset (under 2^32: 64 rows) from bases that all lanes share.
-    __device__ __forceinline__ void take(const typename IO<BF>::T *p, int64_t pitch, int n) {
-        const int row = threadIdx.x / NS, s = threadIdx.x % NS;
-        const char *base = reinterpret_cast<const char *>(p);
-        if (n == C) {
-            const uint32_t off = (uint32_t)(RL > C ? row & (C - 1) : row) * (uint32_t)(pitch * EB) + (uint32_t)s * 16;
+    __device__ __forceinline__ void take(const char *p, uint32_t pitch, int n) {
+        const uint32_t col = (threadIdx.x % NS) * 16u, off = (threadIdx.x / NS) * pitch + col;
+        const uint32_t last = (uint32_t)(n - 1) * pitch + col;
 #pragma unroll
-            for (int i = 0; i < NL; ++i) w[i] = *reinterpret_cast<const u32x4 *>(base + i * RL * pitch * EB + off);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {  // rows behind the last one load that one again
-                const int r = row + i * RL;
-                w[i] = *reinterpret_cast<const u32x4 *>(base + (r < n ? r : n - 1) * pitch * EB + s * 16);
-            }
+        for (int i = 0; i < NL; ++i) {
+            const uint32_t at = off + (uint32_t)i * RL * pitch;
+            w[i] = *reinterpret_cast<const u32x4 *>(p + (at < last ? at : last));
         }
     }
-    __device__ __forceinline__ void put(char *t, int n) const {
+    __device__ __forceinline__ void put(char *t) const {
         const int row = threadIdx.x / NS, s = threadIdx.x % NS;
         if (RL > C && row >= C) return;
-        if (n == C) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) Rows<BF, NCOL>::put16(t, row + i * RL, s, w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-                Rows<BF, NCOL>::put16(t, row + i * RL, s, row + i * RL < n ? w[i] : u32x4{0, 0, 0, 0});
-        }
+        for (int i = 0; i < NL; ++i) Rows<BF, NCOL>::put16(t, row + i * RL, s, w[i]);
     }
 };
 
@@ -311,10 +300,14 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         for (int w = 0; w < NW; ++w) carry += s_red[w];
     }
 
-    const E *pa = reinterpret_cast<const E *>(A.a) + (int64_t)(h / A.ga) * KD;
-    const E *pb = reinterpret_cast<const E *>(A.b) + (int64_t)(h / A.gb) * KD;
-    const E *pc = reinterpret_cast<const E *>(A.c) + (int64_t)(h / A.gc) * A.VD + vt * VT;
-    const int64_t la = (int64_t)(A.H / A.ga) * KD, lb = (int64_t)(A.H / A.gb) * KD, lc = (int64_t)(A.H / A.gc) * A.VD;
+    // the head's rows and the bytes from one token's to the next
+    constexpr int EB = BF ? 2 : 4;
+    const uint32_t la = (uint32_t)(A.H / A.ga) * (KD * EB), lb = (uint32_t)(A.H / A.gb) * (KD * EB);
+    const uint32_t lc = (uint32_t)(A.H / A.gc) * (uint32_t)(A.VD * EB), lx = (uint32_t)(A.H / A.gx) * (uint32_t)(A.VD * EB);
+    const char *pa = reinterpret_cast<const char *>(A.a) + (int64_t)(h / A.ga) * (KD * EB);
+    const char *pb = reinterpret_cast<const char *>(A.b) + (int64_t)(h / A.gb) * (KD * EB);
+    const char *pc = reinterpret_cast<const char *>(A.c) + ((int64_t)(h / A.gc) * A.VD + vt * VT) * EB;
+    const char *px = reinterpret_cast<const char *>(A.x) + ((int64_t)(h / A.gx) * A.VD + vt * VT) * EB;
 
     if constexpr (!INC) {  // tiles across the diagonal that are read but never computed
         for (int i = threadIdx.x; i < SZ_P / 16; i += NT) {
@@ -322,8 +315,6 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
             if constexpr (PLO) reinterpret_cast<uint4 *>(s_pl)[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    const int64_t lx = (int64_t)(A.H / A.gx) * A.VD;
-    const E *px = reinterpret_cast<const E *>(A.x) + (int64_t)(h / A.gx) * A.VD;
     float btot = 0.f;
     auto chunk_at = [&](int i, int64_t &tc, int &n) __attribute__((always_inline)) {  // its first token and how many
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
@@ -338,7 +329,13 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         return A.g_head ? reinterpret_cast<const float *>(A.g)[h]
                         : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
     };
-    auto put_decay = [&](float gv, int buf) __attribute__((always_inline)) {
+    // tokens behind the chunk's last carry no weight, into the state, out of it or to each other
+    auto put_decay = [&](float gv, int i) __attribute__((always_inline)) {
+        const int buf = i & 1;
+        int64_t tc;
+        int n;
+        chunk_at(i, tc, n);
+        const bool live = lane < n;
         Decay d = decay_base2(gv);
         d.hi = row_scan16(d.hi);
         d.lo = row_scan16(d.lo);
@@ -350,11 +347,11 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         if (lane < C) {
             s_bh2[buf][lane] = d.hi;
             s_bl2[buf][lane] = d.lo;
-            s_f2[buf][lane] = f * A.s_intra;
+            s_f2[buf][lane] = live ? f * A.s_intra : 0.f;
             const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
             const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
-            s_win2[buf][lane] = (REV ? eout : ein) * A.s_inter;
-            s_wup2[buf][lane] = (REV ? ein : eout) * A.s_up;
+            s_win2[buf][lane] = live ? (REV ? eout : ein) * A.s_inter : 0.f;
+            s_wup2[buf][lane] = live ? (REV ? ein : eout) * A.s_up : 0.f;
         }
         if (lane == 0) s_ec2[buf] = __builtin_amdgcn_exp2f(hc + lc2);
         if constexpr (INC) btot += hc + lc2;
@@ -368,17 +365,14 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         if constexpr (!INC) ra.take(pa + tc * la, la, n);
         rb.take(pb + tc * lb, lb, n);
         rc.take(pc + tc * lc, lc, n);
-        if constexpr (DG && REV) rx.take(px + vt * VT + tc * lx, lx, n);
+        if constexpr (DG && REV) rx.take(px + tc * lx, lx, n);
     };
     auto put_rows = [&](int i) __attribute__((always_inline)) {
-        int64_t tc;
-        int n;
-        chunk_at(i, tc, n);
         const int j = i & (NB - 1);
-        if constexpr (!INC) ra.put(s_a2[j], n);
-        rb.put(s_b2[j], n);
-        rc.put(s_c2[j], n);
-        if constexpr (DG && REV) rx.put(s_x2[j], n);
+        if constexpr (!INC) ra.put(s_a2[j]);
+        rb.put(s_b2[j]);
+        rc.put(s_c2[j]);
+        if constexpr (DG && REV) rx.put(s_x2[j]);
     };
     float gnext = 0.f;
     if (nch > 0) {
@@ -413,7 +407,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 if (cc + 2 < nch) take_rows(cc + 2);
             }
             if (wave == DW) {  // the next chunk's decays, and the loads of those behind it
-                put_decay(gnext, buf ^ 1);
+                put_decay(gnext, cc + 1);
                 if (cc + 2 < nch) gnext = take_decay(cc + 2);
             }
         }
@@ -445,7 +439,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                     for (int i = 0; i < 4; ++i) {
                         const int s = 16 * ts + 4 * g + i;
                         const float d = REV ? (s_bh[s] - th) + (s_bl[s] - tl) : (th - s_bh[s]) + (tl - s_bl[s]);
-                        const bool in_past = REV ? s >= t : s <= t;
+                        const bool in_past = REV ? s >= t && s < n : s <= t;
                         w[i] = in_past ? acc[i] * (__builtin_amdgcn_exp2f(d) * A.s_intra) : 0.f;
                         if constexpr (DG && REV) acd[i] = in_past ? acd[i] : 0.f;
                     }
@@ -527,7 +521,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                         if constexpr (REV) {
                             RV::load_quad(s_x, t, wave * CT * 16 + 16 * ct + 4 * g, x);
                         } else if (t < n) {
-                            const E *p = px + col0 + 4 * g + (tc + t) * lx + 16 * ct;
+                            const E *p = reinterpret_cast<const E *>(px + (tc + t) * lx) + wave * CT * 16 + 16 * ct + 4 * g;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) x[i] = IO<BF>::ld(p, i);
                         }
@@ -592,13 +586,18 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 }
                 scaled_frags(cf, w, cw[ct]);
             }
+            constexpr int KG = KT < 4 ? KT : 4;  // products of different tiles follow each other
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Frag8<BF> bf = RK::col_frag(s_b, s, kt, lane);
+            for (int k0 = 0; k0 < KT; k0 += KG) {
+                Frag8<BF> bf[KG];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
+                for (int j = 0; j < KG; ++j) bf[j] = RK::col_frag(s_b, s, k0 + j, lane);
 #pragma unroll
-                    for (int q = 0; q < NPART; ++q) st[kt][ct] = mma32(st[kt][ct], bf, cw[ct][q]);
+                for (int q = 0; q < NPART; ++q)
+#pragma unroll
+                    for (int j = 0; j < KG; ++j)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) st[k0 + j][ct] = mma32(st[k0 + j][ct], bf[j], cw[ct][q]);
             }
         }
         if constexpr (!INC) {
