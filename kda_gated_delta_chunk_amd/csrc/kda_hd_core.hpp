@@ -57,21 +57,22 @@ template <int NCOL> struct Rows<true, NCOL> {
         *reinterpret_cast<u32x2 *>(t + at) = u32x2{w.x, w.y};
         *reinterpret_cast<u32x2 *>(t + (at ^ 8)) = u32x2{w.z, w.w};
     }
-    // operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of one row per lane
-    static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int row, int c, int g) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, 32 * c + 4 * g));
-        const uint2 w = *reinterpret_cast<const uint2 *>(t + quad(row, 32 * c + 16 + 4 * g));
+    // Operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of row l%16 (+ what is added to t).
+    // at: row_at(lane), the lane's address for c = 0; the others differ from it in the bits of c alone.
+    static __device__ __forceinline__ int row_at(int lane) { return quad(lane & 15, 4 * (lane >> 4)); }
+    static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int at, int c) {
+        const u32x2 u = *reinterpret_cast<const u32x2 *>(t + (at ^ (c << 6)));
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(t + (at ^ (c << 6 | 32)));
         Frag8<true> f;
         f.p[0] = u.x; f.p[1] = u.y; f.p[2] = w.x; f.p[3] = w.y;
         return f;
     }
-    // operand with the same slot map along the rows 32s .. 32s+31, column 16c + l%16
-    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int s, int c, int lane) {
+    // Operand with the same slot map along 32 rows, column 16c + l%16; at: col_at(lane).
+    static __device__ __forceinline__ int col_at(int lane) { return quad(4 * (lane >> 4) + ((lane >> 2) & 3), 4 * (lane & 3)); }
+    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int at, int c) {
         typedef __attribute__((address_space(3))) s16x4 *lds4;
-        const int g = lane >> 4, i = lane & 15;
-        const int row = 32 * s + 4 * g + (i >> 2), col = 16 * c + 4 * (i & 3);
-        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + quad(row, col)));
-        const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + quad(row + 16, col)));
+        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + (at ^ (c << 5))));
+        const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + (at ^ (c << 5)) + 16 * RB));
         const uint2 a = __builtin_bit_cast(uint2, u), b = __builtin_bit_cast(uint2, w);
         Frag8<true> f;
         f.p[0] = a.x; f.p[1] = a.y; f.p[2] = b.x; f.p[3] = b.y;
@@ -92,18 +93,19 @@ template <int NCOL> struct Rows<false, NCOL> {
     static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
         *reinterpret_cast<u32x4 *>(t + row * RB + (s << 4)) = w;
     }
-    static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int row, int c, int g) {
-        const float4 u = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 4 * g));
-        const float4 w = *reinterpret_cast<const float4 *>(t + quad(row, 32 * c + 16 + 4 * g));
+    static __device__ __forceinline__ int row_at(int lane) { return quad(lane & 15, 4 * (lane >> 4)); }
+    static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int at, int c) {
+        const f32x4 u = *reinterpret_cast<const f32x4 *>(t + at + 128 * c);
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(t + at + 128 * c + 64);
         return Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
     }
-    static __device__ __forceinline__ Frag8<false> col_frag(const char *t, int s, int c, int lane) {
-        const int g = lane >> 4, i = lane & 15;
+    static __device__ __forceinline__ int col_at(int lane) { return quad(4 * (lane >> 4), lane & 15); }
+    static __device__ __forceinline__ Frag8<false> col_frag(const char *t, int at, int c) {
         Frag8<false> f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f.f[j] = *reinterpret_cast<const float *>(t + quad(32 * s + 4 * g + j, 16 * c + i));
-            f.f[4 + j] = *reinterpret_cast<const float *>(t + quad(32 * s + 16 + 4 * g + j, 16 * c + i));
+            f.f[j] = *reinterpret_cast<const float *>(t + at + 64 * c + j * RB);
+            f.f[4 + j] = *reinterpret_cast<const float *>(t + at + 64 * c + (16 + j) * RB);
         }
         return f;
     }
@@ -214,7 +216,7 @@ __device__ __forceinline__ void mfma_fence_state(f32x4 (&x)[M][N]) {
 }
 
 template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG>
-__global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs A) {
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(const CoreArgs A) {
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
     constexpr int DW = NW - 1;                            // the wavefront that keeps the decays
@@ -316,6 +318,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         }
     }
     float btot = 0.f;
+    const int rowk0 = RK::row_at(lane), colk0 = RK::col_at(lane), rowv0 = RV::row_at(lane), rowp0 = RP::row_at(lane);
+    const int colv0 = BF ? RV::col_at(lane) ^ (wave * CT << 5) : RV::col_at(lane) + 64 * wave * CT;
     auto chunk_at = [&](int i, int64_t &tc, int &n) __attribute__((always_inline)) {  // its first token and how many
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
         n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
@@ -393,8 +397,16 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
         chunk_at(cc, tc, n);
         const int buf = cc & 1, rbuf = cc & (NB - 1);
         const float *s_win = s_win2[buf], *s_wup = s_wup2[buf], *s_bh = s_bh2[buf], *s_bl = s_bl2[buf], *s_f = s_f2[buf];
-        const char *s_a = s_a2[rbuf], *s_b = s_b2[rbuf], *s_c = s_c2[rbuf], *s_x = s_x2[rbuf];
-        (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
+        // The rows' buffer enters the lanes' addresses (its size is above all their bits), and they are made anew each
+        // chunk: kept, the some twenty that are derived from them would take the registers the products need.
+        int rowk = rowk0, colk = colk0, rowv = rowv0, colv = colv0, rowp = rowp0;
+        if constexpr (NB == 2) {
+            rowk += rbuf * SZ_K; colk += rbuf * SZ_K;
+            rowv += rbuf * SZ_V; colv += rbuf * SZ_V;
+        }
+        asm volatile("" : "+v"(rowk), "+v"(colk), "+v"(rowv), "+v"(colv), "+v"(rowp));
+        const char *s_a = s_a2[0], *s_b = s_b2[0], *s_c = s_c2[0], *s_x = s_x2[0];
+        (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
         if constexpr (NB == 1) {
             put_rows(cc);
@@ -424,11 +436,11 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 f32x4 acc = zero4(), acd = zero4();
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
-                    acc = mma32(acc, RK::row_frag(s_b, 16 * ts + li, c, g), RK::row_frag(s_a, 16 * tt + li, c, g));
+                    acc = mma32(acc, RK::row_frag(s_b + 16 * ts * RK::RB, rowk, c), RK::row_frag(s_a + 16 * tt * RK::RB, rowk, c));
                 if constexpr (DG && REV) {
 #pragma unroll
                     for (int c = 0; c < VT / 32; ++c)
-                        acd = mma32(acd, RV::row_frag(s_c, 16 * ts + li, c, g), RV::row_frag(s_x, 16 * tt + li, c, g));
+                        acd = mma32(acd, RV::row_frag(s_c + 16 * ts * RV::RB, rowv, c), RV::row_frag(s_x + 16 * tt * RV::RB, rowv, c));
                 }
                 mfma_fence(acc, acd);
                 const int t = 16 * tt + li;
@@ -494,7 +506,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                 for (int ct = 0; ct < CT; ++ct) state_frag(st[2 * c][ct], st[2 * c + 1][ct], hi[ct], lo[ct]);
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
-                    const Frag8<BF> f = RK::row_frag(s_a, 16 * tt + li, c, g);
+                    const Frag8<BF> f = RK::row_frag(s_a + 16 * tt * RK::RB, rowk, c);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         y[ct][tt] = mma32(y[ct][tt], hi[ct], f);
@@ -519,7 +531,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
                     for (int ct = 0; ct < CT; ++ct) {
                         float x[4] = {0.f, 0.f, 0.f, 0.f};
                         if constexpr (REV) {
-                            RV::load_quad(s_x, t, wave * CT * 16 + 16 * ct + 4 * g, x);
+                            RV::load_quad(s_x2[rbuf], t, wave * CT * 16 + 16 * ct + 4 * g, x);
                         } else if (t < n) {
                             const E *p = reinterpret_cast<const E *>(px + (tc + t) * lx) + wave * CT * 16 + 16 * ct + 4 * g;
 #pragma unroll
@@ -575,13 +587,13 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
             *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + 16 + 4 * g);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const Frag8<BF> cf = RV::col_frag(s_c, s, wave * CT + ct, lane);
+                const Frag8<BF> cf = RV::col_frag(s_c + 32 * s * RV::RB, colv, ct);
                 if constexpr (!INC) {
 #pragma unroll
                     for (int tt = 0; tt < TT; ++tt) {
                         if (REV ? 2 * s + 1 < tt : 2 * s > tt) continue;
-                        y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p, 16 * tt + li, s, g));
-                        if constexpr (PLO) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl, 16 * tt + li, s, g));
+                        y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p + 16 * tt * RP::RB, rowp, s));
+                        if constexpr (PLO) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl + 16 * tt * RP::RB, rowp, s));
                     }
                 }
                 scaled_frags(cf, w, cw[ct]);
@@ -591,7 +603,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
             for (int k0 = 0; k0 < KT; k0 += KG) {
                 Frag8<BF> bf[KG];
 #pragma unroll
-                for (int j = 0; j < KG; ++j) bf[j] = RK::col_frag(s_b, s, k0 + j, lane);
+                for (int j = 0; j < KG; ++j) bf[j] = RK::col_frag(s_b + 32 * s * RK::RB, colk, k0 + j);
 #pragma unroll
                 for (int q = 0; q < NPART; ++q)
 #pragma unroll
@@ -640,7 +652,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kda_hd_chunk_kernel(const CoreArgs
 
 template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
 hipError_t launch_one(const CoreArgs &a, hipStream_t st) {
-    constexpr int NW = VT >= 64 ? 4 : VT / 16;
+    constexpr int NW = VT / 16;
     const int64_t groups = (a.slots * a.H + 7) / 8;
     const int64_t blocks = groups * 8 * a.tiles;
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
