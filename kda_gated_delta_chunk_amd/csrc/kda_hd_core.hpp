@@ -155,20 +155,10 @@ __device__ __forceinline__ Decay decay_base2(float g) {
     const float hi = rintf(x * 256.f) * 0.00390625f;
     return Decay{hi, (x - hi) + rest};
 }
-// d: the sums within a tile of 16 tokens on entry
-template <int C>
-__device__ __forceinline__ Decay decay_join(Decay d, int lane) {
-#pragma unroll
-    for (int w = 16; w < C; w <<= 1) {
-        const int from = (lane & ~(2 * w - 1)) + w - 1;  // the last lane of the lower half
-        const float h = __shfl(d.hi, from), l = __shfl(d.lo, from);
-        if (lane & w) {
-            d.hi += h;
-            d.lo += l;
-        }
-    }
-    return d;
+__device__ __forceinline__ float lane_value(float x, int lane) {  // the same for all lanes
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
+
 // Sum over the 16 lanes of a row, in its last lane.
 __device__ __forceinline__ float row_sum_last(float x) { return row_scan16(x); }
 
@@ -346,8 +336,11 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         // a source's weight up to its tile's edge on the output's side
         const float f = REV ? __builtin_amdgcn_exp2f(d.hi + d.lo)
                             : __builtin_amdgcn_exp2f((row_last(d.hi) - d.hi) + (row_last(d.lo) - d.lo));
-        d = decay_join<C>(d, lane);
-        const float hc = __shfl(d.hi, C - 1), lc2 = __shfl(d.lo, C - 1);
+        static_assert(C == 32, "two tiles");
+        const float h0 = lane_value(d.hi, 15), l0 = lane_value(d.lo, 15);
+        d.hi += lane & 16 ? h0 : 0.f;
+        d.lo += lane & 16 ? l0 : 0.f;
+        const float hc = lane_value(d.hi, C - 1), lc2 = lane_value(d.lo, C - 1);
         if (lane < C) {
             s_bh2[buf][lane] = d.hi;
             s_bl2[buf][lane] = d.lo;
