@@ -209,7 +209,7 @@ template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG>
 __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(const CoreArgs A) {
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
-    constexpr int DW = NW - 1;                            // the wavefront that keeps the decays
+    constexpr int DB = 2 * NW;                            // chunks whose decays are made at a time
     constexpr int NPART = BF ? 3 : 1;
     constexpr bool PLO = BF && DG, SLO = BF && DG;
     static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
@@ -223,8 +223,9 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     __shared__ __align__(16) char s_b2[NB][SZ_K], s_c2[NB][SZ_V];
     __shared__ __align__(16) char s_a2[NB][INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
     __shared__ __align__(16) char s_x2[NB][DG && REV ? SZ_V : 16];
-    __shared__ __align__(16) float s_win2[2][C], s_wup2[2][C], s_bh2[2][C], s_bl2[2][C], s_f2[2][C];
-    __shared__ float s_ec2[2];
+    __shared__ __align__(16) float s_wup2[DB][C], s_win2[INC ? 1 : DB][C], s_bh2[INC ? 1 : DB][C], s_bl2[INC ? 1 : DB][C],
+        s_f2[INC ? 1 : DB][C];
+    __shared__ float s_ec2[DB];
     __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
     (void)s_pl; (void)s_x2; (void)s_u; (void)s_red;
 
@@ -314,44 +315,47 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
         n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
     };
-    // one wavefront keeps the decays: a token's log-decay per lane, two chunks ahead; their sums and weights, one ahead
-    auto take_decay = [&](int i) __attribute__((always_inline)) -> float {
+    // The decays of DB chunks are made at a time, two by each wavefront (a token per lane), from log-decays that were
+    // loaded while the DB chunks before were worked on.
+    static_assert(C == 32, "two chunks of two tiles per wavefront");
+    auto take_decay = [&](int first) __attribute__((always_inline)) -> float {
+        const int i = first + 2 * wave + (lane >> 5), t = lane & 31;
         int64_t tc;
         int n;
         chunk_at(i, tc, n);
-        if (lane >= n) return 0.f;
+        if (i >= nch || t >= n) return 0.f;
         return A.g_head ? reinterpret_cast<const float *>(A.g)[h]
-                        : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + lane) * A.H + h);
+                        : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + t) * A.H + h);
     };
-    // tokens behind the chunk's last carry no weight, into the state, out of it or to each other
-    auto put_decay = [&](float gv, int i) __attribute__((always_inline)) {
-        const int buf = i & 1;
+    auto put_decay = [&](float gv, int first) __attribute__((always_inline)) {
+        const int i = first + 2 * wave + (lane >> 5), t = lane & 31, at = 2 * wave + (lane >> 5);
         int64_t tc;
         int n;
         chunk_at(i, tc, n);
-        const bool live = lane < n;
+        const bool live = i < nch && t < n;  // the others carry no weight, into the state, out of it or to each other
         Decay d = decay_base2(gv);
         d.hi = row_scan16(d.hi);
         d.lo = row_scan16(d.lo);
         // a source's weight up to its tile's edge on the output's side
         const float f = REV ? __builtin_amdgcn_exp2f(d.hi + d.lo)
                             : __builtin_amdgcn_exp2f((row_last(d.hi) - d.hi) + (row_last(d.lo) - d.lo));
-        static_assert(C == 32, "two tiles");
-        const float h0 = lane_value(d.hi, 15), l0 = lane_value(d.lo, 15);
+        const float h0 = lane < 32 ? lane_value(d.hi, 15) : lane_value(d.hi, 47);
+        const float l0 = lane < 32 ? lane_value(d.lo, 15) : lane_value(d.lo, 47);
         d.hi += lane & 16 ? h0 : 0.f;
         d.lo += lane & 16 ? l0 : 0.f;
-        const float hc = lane_value(d.hi, C - 1), lc2 = lane_value(d.lo, C - 1);
-        if (lane < C) {
-            s_bh2[buf][lane] = d.hi;
-            s_bl2[buf][lane] = d.lo;
-            s_f2[buf][lane] = live ? f * A.s_intra : 0.f;
-            const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
-            const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
-            s_win2[buf][lane] = live ? (REV ? eout : ein) * A.s_inter : 0.f;
-            s_wup2[buf][lane] = live ? (REV ? ein : eout) * A.s_up : 0.f;
+        const float hc = lane < 32 ? lane_value(d.hi, 31) : lane_value(d.hi, 63);
+        const float lc2 = lane < 32 ? lane_value(d.lo, 31) : lane_value(d.lo, 63);
+        const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
+        const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
+        s_wup2[at][t] = live ? (REV ? ein : eout) * A.s_up : 0.f;
+        if constexpr (!INC) {
+            s_bh2[at][t] = d.hi;
+            s_bl2[at][t] = d.lo;
+            s_f2[at][t] = live ? f * A.s_intra : 0.f;
+            s_win2[at][t] = live ? (REV ? eout : ein) * A.s_inter : 0.f;
         }
-        if (lane == 0) s_ec2[buf] = __builtin_amdgcn_exp2f(hc + lc2);
-        if constexpr (INC) btot += hc + lc2;
+        if (t == 0) s_ec2[at] = __builtin_amdgcn_exp2f(hc + lc2);
+        if constexpr (INC) btot += hc + lc2;  // lanes 0 and 32: this wavefront's chunks
     };
     Stage<BF, KD, C, NT> ra, rb;
     Stage<BF, VT, C, NT> rc, rx;
@@ -374,10 +378,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     float gnext = 0.f;
     if (nch > 0) {
         take_rows(0);
-        if (wave == DW) {
-            put_decay(take_decay(0), 0);
-            if (nch > 1) gnext = take_decay(1);
-        }
+        gnext = take_decay(0);
         if constexpr (NB == 2) {
             put_rows(0);
             if (nch > 1) take_rows(1);
@@ -388,8 +389,9 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         int64_t tc;
         int n;
         chunk_at(cc, tc, n);
-        const int buf = cc & 1, rbuf = cc & (NB - 1);
-        const float *s_win = s_win2[buf], *s_wup = s_wup2[buf], *s_bh = s_bh2[buf], *s_bl = s_bl2[buf], *s_f = s_f2[buf];
+        const int buf = cc & (DB - 1), rbuf = cc & (NB - 1);
+        const float *s_wup = s_wup2[buf], *s_win = s_win2[INC ? 0 : buf], *s_bh = s_bh2[INC ? 0 : buf],
+                    *s_bl = s_bl2[INC ? 0 : buf], *s_f = s_f2[INC ? 0 : buf];
         // The rows' buffer enters the lanes' addresses (its size is above all their bits), and they are made anew each
         // chunk: kept, the some twenty that are derived from them would take the registers the products need.
         int rowk = rowk0, colk = colk0, rowv = rowv0, colv = colv0, rowp = rowp0;
@@ -401,20 +403,18 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         const char *s_a = s_a2[0], *s_b = s_b2[0], *s_c = s_c2[0], *s_x = s_x2[0];
         (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
+        if (buf == 0) {
+            put_decay(gnext, cc);
+            if (cc + DB < nch) gnext = take_decay(cc + DB);
+        }
         if constexpr (NB == 1) {
             put_rows(cc);
             if (cc + 1 < nch) take_rows(cc + 1);
-            __syncthreads();
         }
-        if (cc + 1 < nch) {
-            if constexpr (NB == 2) {
-                put_rows(cc + 1);
-                if (cc + 2 < nch) take_rows(cc + 2);
-            }
-            if (wave == DW) {  // the next chunk's decays, and the loads of those behind it
-                put_decay(gnext, cc + 1);
-                if (cc + 2 < nch) gnext = take_decay(cc + 2);
-            }
+        if (NB == 1 || buf == 0) __syncthreads();
+        if (NB == 2 && cc + 1 < nch) {
+            put_rows(cc + 1);
+            if (cc + 2 < nch) take_rows(cc + 2);
         }
 
         // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
@@ -435,27 +435,31 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                     for (int c = 0; c < VT / 32; ++c)
                         acd = mma32(acd, RV::row_frag(s_c + 16 * ts * RV::RB, rowv, c), RV::row_frag(s_x + 16 * tt * RV::RB, rowv, c));
                 }
-                mfma_fence(acc, acd);
                 const int t = 16 * tt + li;
                 const float th = s_bh[t], tl = s_bl[t];
-                float w[4];
+                f32x4 w;
                 if (tt == ts) {
+                    const f32x4 sh = *reinterpret_cast<const f32x4 *>(s_bh + 16 * ts + 4 * g);
+                    const f32x4 sl = *reinterpret_cast<const f32x4 *>(s_bl + 16 * ts + 4 * g);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = __builtin_amdgcn_exp2f(REV ? (sh[i] - th) + (sl[i] - tl) : (th - sh[i]) + (tl - sl[i])) *
+                               A.s_intra;
+                    mfma_fence(acc, acd);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int s = 16 * ts + 4 * g + i;
-                        const float d = REV ? (s_bh[s] - th) + (s_bl[s] - tl) : (th - s_bh[s]) + (tl - s_bl[s]);
                         const bool in_past = REV ? s >= t && s < n : s <= t;
-                        w[i] = in_past ? acc[i] * (__builtin_amdgcn_exp2f(d) * A.s_intra) : 0.f;
+                        w[i] = in_past ? acc[i] * w[i] : 0.f;
                         if constexpr (DG && REV) acd[i] = in_past ? acd[i] : 0.f;
                     }
                 } else {
                     // over the edge between the tiles: the source's weight up to it, the output's from there
                     const int e = REV ? 16 * ts - 1 : 16 * ts + 15;
-                    const float f = __builtin_amdgcn_exp2f(REV ? (s_bh[e] - th) + (s_bl[e] - tl)
-                                                               : (th - s_bh[e]) + (tl - s_bl[e]));
-                    const f32x4 fs = *reinterpret_cast<const f32x4 *>(s_f + 16 * ts + 4 * g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = acc[i] * (f * fs[i]);
+                    w = *reinterpret_cast<const f32x4 *>(s_f + 16 * ts + 4 * g) *
+                        __builtin_amdgcn_exp2f(REV ? (s_bh[e] - th) + (s_bl[e] - tl) : (th - s_bh[e]) + (tl - s_bl[e]));
+                    mfma_fence(acc, acd);
+                    w *= acc;
                 }
                 if constexpr (DG && REV) {
                     // pairs (row s, column t) of the log-decays' gradient: + at the row, - at the column
@@ -640,7 +644,16 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                 for (int i = 0; i < 4; ++i)
                     so[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
     }
-    if (INC && threadIdx.x == DW * 64 && vt == 0) A.seg_decay[slot * A.H + h] = btot;
+    if constexpr (INC) {  // the segment's whole decay: the wavefronts' sums
+        btot = lane_value(btot, 0) + lane_value(btot, 32);
+        if (lane == 0) s_red[wave] = btot;
+        __syncthreads();
+        if (threadIdx.x == 0 && vt == 0) {
+#pragma unroll
+            for (int w = 1; w < NW; ++w) btot += s_red[w];
+            A.seg_decay[slot * A.H + h] = btot;
+        }
+    }
 }
 
 template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
