@@ -611,22 +611,30 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         }
         if constexpr (!INC) {
             mfma_fence_all(y);
-            // a lane's offset within the chunk (under 2^32: 64 rows) from bases that all lanes share
-            const uint32_t lane_off = (uint32_t)li * (uint32_t)(A.H * A.VD) + (uint32_t)(col0 + 4 * g);
-            const int64_t base = (tc * A.H + h) * A.VD;
+            // Stores of all lanes, the hardware drops those behind the chunk's last row (past the buffer's end): a branch
+            // around them would make the next chunk's rows, which were asked for before, wait for them too. (The whole
+            // offset is in the lane's part: the scalar part is not held against the buffer's end.)
+            const int eb = BF && !A.y_fp32 ? 2 : 4;
+            const uint32_t pitch = (uint32_t)A.H * (uint32_t)(A.VD * eb);  // 64 rows: under 2^32
+            const auto out = __builtin_amdgcn_make_buffer_rsrc(
+                reinterpret_cast<char *>(A.y) + ((int64_t)tc * A.H + h) * A.VD * eb, 0, (n - 1) * pitch + A.VD * eb,
+                0x00027000);
+            const uint32_t lane_off = li * pitch + (uint32_t)(col0 + 4 * g) * eb;
+            if (BF && !A.y_fp32) {
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                if (16 * tt + li >= n) continue;
-                const int64_t row = base + (int64_t)(16 * tt) * A.H * A.VD;
+                for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const f32x4 v = y[ct][tt];
-                    if (BF && !A.y_fp32)
-                        *reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(A.y) + row * 2 + lane_off * 2u + 32 * ct) =
-                            u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
-                    else
-                        *reinterpret_cast<f32x4 *>(reinterpret_cast<char *>(A.y) + row * 4 + lane_off * 4u + 64 * ct) = v;
-                }
+                    for (int ct = 0; ct < CT; ++ct)
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            u32x2{pack_bf16(y[ct][tt].x, y[ct][tt].y), pack_bf16(y[ct][tt].z, y[ct][tt].w)}, out,
+                            lane_off + 16 * tt * pitch + 32 * ct, 0, 0);
+            } else {
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[ct][tt]), out,
+                                                               lane_off + 16 * tt * pitch + 64 * ct, 0, 0);
             }
         }
         mfma_fence_state(st);
