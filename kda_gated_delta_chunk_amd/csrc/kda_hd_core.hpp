@@ -128,8 +128,8 @@ struct Stage {
     static constexpr int NL = C > RL ? C / RL : 1;
     static_assert(NT % NS == 0 && C % (RL < C ? RL : C) == 0, "whole rounds of whole rows");
     u32x4 w[NL];
-    __device__ __forceinline__ void take(const char *p, uint32_t pitch, int n) {
-        const uint32_t col = (threadIdx.x % NS) * 16u, off = (threadIdx.x / NS) * pitch + col;
+    __device__ __forceinline__ void take(int tid, const char *p, uint32_t pitch, int n) {
+        const uint32_t col = ((uint32_t)tid % NS) * 16u, off = ((uint32_t)tid / NS) * pitch + col;
         const uint32_t last = (uint32_t)(n - 1) * pitch + col;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
@@ -137,8 +137,8 @@ struct Stage {
             w[i] = *reinterpret_cast<const u32x4 *>(p + (at < last ? at : last));
         }
     }
-    __device__ __forceinline__ void put(char *t) const {
-        const int row = threadIdx.x / NS, s = threadIdx.x % NS;
+    __device__ __forceinline__ void put(int tid, char *t) const {
+        const int row = (uint32_t)tid / NS, s = (uint32_t)tid % NS;
         if (RL > C && row >= C) return;
 #pragma unroll
         for (int i = 0; i < NL; ++i) Rows<BF, NCOL>::put16(t, row + i * RL, s, w[i]);
@@ -205,7 +205,7 @@ __device__ __forceinline__ void mfma_fence_state(f32x4 (&x)[M][N]) {
     }
 }
 
-template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG>
+template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG, bool YF>
 __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(const CoreArgs A) {
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
@@ -229,7 +229,8 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
     (void)s_pl; (void)s_x2; (void)s_u; (void)s_red;
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4,
+              li = lane & 15;
     // tiles of one (segment, head) sit 8 workgroups apart: the same XCD, whose L2 then holds their common rows
     const int64_t items = A.slots * A.H;
     const int64_t blk = blockIdx.x, grp = blk / (8 * A.tiles);
@@ -268,6 +269,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                         st[kt][ct][i] = s0[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc];
         }
     }
+    mfma_fence_state(st);  // the loads end here: a wait for them inside the loop would hold up the rows under way
     // ---- what the borders behind the segment pass on to its log-decays: <state gradient, state> at its end
     float carry = 0.f;
     if constexpr (DG && REV) {
@@ -309,8 +311,6 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         }
     }
     float btot = 0.f;
-    const int rowk0 = RK::row_at(lane), colk0 = RK::col_at(lane), rowv0 = RV::row_at(lane), rowp0 = RP::row_at(lane);
-    const int colv0 = BF ? RV::col_at(lane) ^ (wave * CT << 5) : RV::col_at(lane) + 64 * wave * CT;
     auto chunk_at = [&](int i, int64_t &tc, int &n) __attribute__((always_inline)) {  // its first token and how many
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
         n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     // The decays of DB chunks are made at a time, two by each wavefront (a token per lane), from log-decays that were
     // loaded while the DB chunks before were worked on.
     static_assert(C == 32, "two chunks of two tiles per wavefront");
-    auto take_decay = [&](int first) __attribute__((always_inline)) -> float {
+    auto take_decay = [&](int lane, int first) __attribute__((always_inline)) -> float {
         const int i = first + 2 * wave + (lane >> 5), t = lane & 31;
         int64_t tc;
         int n;
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         return A.g_head ? reinterpret_cast<const float *>(A.g)[h]
                         : IO<BF>::ld(reinterpret_cast<const E *>(A.g), (tc + t) * A.H + h);
     };
-    auto put_decay = [&](float gv, int first) __attribute__((always_inline)) {
+    auto put_decay = [&](int lane, float gv, int first) __attribute__((always_inline)) {
         const int i = first + 2 * wave + (lane >> 5), t = lane & 31, at = 2 * wave + (lane >> 5);
         int64_t tc;
         int n;
@@ -359,29 +359,29 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     };
     Stage<BF, KD, C, NT> ra, rb;
     Stage<BF, VT, C, NT> rc, rx;
-    auto take_rows = [&](int i) __attribute__((always_inline)) {
+    auto take_rows = [&](int tid, int i) __attribute__((always_inline)) {
         int64_t tc;
         int n;
         chunk_at(i, tc, n);
-        if constexpr (!INC) ra.take(pa + tc * la, la, n);
-        rb.take(pb + tc * lb, lb, n);
-        rc.take(pc + tc * lc, lc, n);
-        if constexpr (DG && REV) rx.take(px + tc * lx, lx, n);
+        if constexpr (!INC) ra.take(tid, pa + tc * la, la, n);
+        rb.take(tid, pb + tc * lb, lb, n);
+        rc.take(tid, pc + tc * lc, lc, n);
+        if constexpr (DG && REV) rx.take(tid, px + tc * lx, lx, n);
     };
-    auto put_rows = [&](int i) __attribute__((always_inline)) {
+    auto put_rows = [&](int tid, int i) __attribute__((always_inline)) {
         const int j = i & (NB - 1);
-        if constexpr (!INC) ra.put(s_a2[j]);
-        rb.put(s_b2[j]);
-        rc.put(s_c2[j]);
-        if constexpr (DG && REV) rx.put(s_x2[j]);
+        if constexpr (!INC) ra.put(tid, s_a2[j]);
+        rb.put(tid, s_b2[j]);
+        rc.put(tid, s_c2[j]);
+        if constexpr (DG && REV) rx.put(tid, s_x2[j]);
     };
     float gnext = 0.f;
     if (nch > 0) {
-        take_rows(0);
-        gnext = take_decay(0);
+        take_rows(threadIdx.x, 0);
+        gnext = take_decay(lane, 0);
         if constexpr (NB == 2) {
-            put_rows(0);
-            if (nch > 1) take_rows(1);
+            put_rows(threadIdx.x, 0);
+            if (nch > 1) take_rows(threadIdx.x, 1);
         }
     }
 
@@ -392,29 +392,30 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         const int buf = cc & (DB - 1), rbuf = cc & (NB - 1);
         const float *s_wup = s_wup2[buf], *s_win = s_win2[INC ? 0 : buf], *s_bh = s_bh2[INC ? 0 : buf],
                     *s_bl = s_bl2[INC ? 0 : buf], *s_f = s_f2[INC ? 0 : buf];
-        // The rows' buffer enters the lanes' addresses (its size is above all their bits), and they are made anew each
-        // chunk: kept, the some twenty that are derived from them would take the registers the products need.
-        int rowk = rowk0, colk = colk0, rowv = rowv0, colv = colv0, rowp = rowp0;
-        if constexpr (NB == 2) {
-            rowk += rbuf * SZ_K; colk += rbuf * SZ_K;
-            rowv += rbuf * SZ_V; colv += rbuf * SZ_V;
-        }
-        asm volatile("" : "+v"(rowk), "+v"(colk), "+v"(rowv), "+v"(colv), "+v"(rowp));
+        // The lanes' addresses are made anew each chunk, from the lane's number that the compiler cannot see through:
+        // kept over the loop, the some forty of them would take the registers the products need. The rows' buffer
+        // enters them too (its size is above all their bits).
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, g = lane >> 4, li = lane & 15;
+        const int rowk = RK::row_at(lane) + rbuf * SZ_K, colk = RK::col_at(lane) + rbuf * SZ_K;
+        const int rowv = RV::row_at(lane) + rbuf * SZ_V, rowp = RP::row_at(lane);
+        const int colv = (BF ? RV::col_at(lane) ^ (wave * CT << 5) : RV::col_at(lane) + 64 * wave * CT) + rbuf * SZ_V;
         const char *s_a = s_a2[0], *s_b = s_b2[0], *s_c = s_c2[0], *s_x = s_x2[0];
         (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
         if (buf == 0) {
-            put_decay(gnext, cc);
-            if (cc + DB < nch) gnext = take_decay(cc + DB);
+            put_decay(lane, gnext, cc);
+            if (cc + DB < nch) gnext = take_decay(lane, cc + DB);
         }
         if constexpr (NB == 1) {
-            put_rows(cc);
-            if (cc + 1 < nch) take_rows(cc + 1);
+            put_rows(tid, cc);
+            if (cc + 1 < nch) take_rows(tid, cc + 1);
         }
         if (NB == 1 || buf == 0) __syncthreads();
         if (NB == 2 && cc + 1 < nch) {
-            put_rows(cc + 1);
-            if (cc + 2 < nch) take_rows(cc + 2);
+            put_rows(tid, cc + 1);
+            if (cc + 2 < nch) take_rows(tid, cc + 2);
         }
 
         // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
@@ -427,9 +428,14 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                 while (y > x) { y -= x + 1; ++x; }  // p-th pair (x, y <= x)
                 const int tt = REV ? y : x, ts = REV ? x : y;
                 f32x4 acc = zero4(), acd = zero4();
+                Frag8<BF> fb[KC], fa[KC];
 #pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    acc = mma32(acc, RK::row_frag(s_b + 16 * ts * RK::RB, rowk, c), RK::row_frag(s_a + 16 * tt * RK::RB, rowk, c));
+                for (int c = 0; c < KC; ++c) {
+                    fb[c] = RK::row_frag(s_b + 16 * ts * RK::RB, rowk, c);
+                    fa[c] = RK::row_frag(s_a + 16 * tt * RK::RB, rowk, c);
+                }
+#pragma unroll
+                for (int c = 0; c < KC; ++c) acc = mma32(acc, fb[c], fa[c]);
                 if constexpr (DG && REV) {
 #pragma unroll
                     for (int c = 0; c < VT / 32; ++c)
@@ -614,13 +620,13 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
             // Stores of all lanes, the hardware drops those behind the chunk's last row (past the buffer's end): a branch
             // around them would make the next chunk's rows, which were asked for before, wait for them too. (The whole
             // offset is in the lane's part: the scalar part is not held against the buffer's end.)
-            const int eb = BF && !A.y_fp32 ? 2 : 4;
+            constexpr int eb = BF && !YF ? 2 : 4;
             const uint32_t pitch = (uint32_t)A.H * (uint32_t)(A.VD * eb);  // 64 rows: under 2^32
             const auto out = __builtin_amdgcn_make_buffer_rsrc(
                 reinterpret_cast<char *>(A.y) + ((int64_t)tc * A.H + h) * A.VD * eb, 0, (n - 1) * pitch + A.VD * eb,
                 0x00027000);
             const uint32_t lane_off = li * pitch + (uint32_t)(col0 + 4 * g) * eb;
-            if (BF && !A.y_fp32) {
+            if constexpr (eb == 2) {
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
@@ -664,24 +670,31 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     }
 }
 
-template <bool BF, int KD, int VT, bool REV, bool INC, bool DG>
+template <bool BF, int KD, int VT, bool REV, bool INC, bool DG, bool YF = false>
 hipError_t launch_one(const CoreArgs &a, hipStream_t st) {
     constexpr int NW = VT / 16;
     const int64_t groups = (a.slots * a.H + 7) / 8;
     const int64_t blocks = groups * 8 * a.tiles;
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kda_hd_chunk_kernel<BF, KD, VT, NW, REV, INC, DG>), dim3((uint32_t)blocks), dim3(NW * 64), 0, st,
-                       a);
+    hipLaunchKernelGGL((kda_hd_chunk_kernel<BF, KD, VT, NW, REV, INC, DG, YF>), dim3((uint32_t)blocks), dim3(NW * 64), 0,
+                       st, a);
     return hipGetLastError();
 }
 template <bool BF, int KD, int VT>
 hipError_t launch_kind(const CoreArgs &a, Kind k, hipStream_t st) {
+    const bool yf = BF && a.y_fp32;
     switch (k) {
-        case Kind::fwd: return launch_one<BF, KD, VT, false, false, false>(a, st);
-        case Kind::rev: return launch_one<BF, KD, VT, true, false, false>(a, st);
+        case Kind::fwd:
+            return yf ? launch_one<BF, KD, VT, false, false, false, BF>(a, st)
+                      : launch_one<BF, KD, VT, false, false, false>(a, st);
+        case Kind::rev:
+            return yf ? launch_one<BF, KD, VT, true, false, false, BF>(a, st)
+                      : launch_one<BF, KD, VT, true, false, false>(a, st);
         case Kind::fwd_inc: return launch_one<BF, KD, VT, false, true, false>(a, st);
         case Kind::rev_inc: return launch_one<BF, KD, VT, true, true, false>(a, st);
-        case Kind::fwd_dg: return launch_one<BF, KD, VT, false, false, true>(a, st);
+        case Kind::fwd_dg:
+            return yf ? launch_one<BF, KD, VT, false, false, true, BF>(a, st)
+                      : launch_one<BF, KD, VT, false, false, true>(a, st);
         default: return launch_one<BF, KD, VT, true, false, true>(a, st);
     }
 }
