@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     constexpr int NB = BF ? 2 : 1;
     __shared__ __align__(16) char s_b2[NB][SZ_K], s_c2[NB][SZ_V];
     __shared__ __align__(16) char s_a2[NB][INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
-    __shared__ __align__(16) char s_x2[NB][DG && REV ? SZ_V : 16];
+    __shared__ __align__(16) char s_x2[NB][DG ? SZ_V : 16];
     __shared__ __align__(16) float s_wup2[DB][C], s_win2[INC ? 1 : DB][C], s_bh2[INC ? 1 : DB][C], s_bl2[INC ? 1 : DB][C],
         s_f2[INC ? 1 : DB][C];
     __shared__ float s_ec2[DB];
@@ -366,14 +366,14 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         if constexpr (!INC) ra.take(tid, pa + tc * la, la, n);
         rb.take(tid, pb + tc * lb, lb, n);
         rc.take(tid, pc + tc * lc, lc, n);
-        if constexpr (DG && REV) rx.take(tid, px + tc * lx, lx, n);
+        if constexpr (DG) rx.take(tid, px + tc * lx, lx, n);
     };
     auto put_rows = [&](int tid, int i) __attribute__((always_inline)) {
         const int j = i & (NB - 1);
         if constexpr (!INC) ra.put(tid, s_a2[j]);
         rb.put(tid, s_b2[j]);
         rc.put(tid, s_c2[j]);
-        if constexpr (DG && REV) rx.put(tid, s_x2[j]);
+        if constexpr (DG) rx.put(tid, s_x2[j]);
     };
     float gnext = 0.f;
     if (nch > 0) {
@@ -532,14 +532,8 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                     float d = 0.f;
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
-                        if constexpr (REV) {
-                            RV::load_quad(s_x2[rbuf], t, wave * CT * 16 + 16 * ct + 4 * g, x);
-                        } else if (t < n) {
-                            const E *p = reinterpret_cast<const E *>(px + (tc + t) * lx) + wave * CT * 16 + 16 * ct + 4 * g;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[i] = IO<BF>::ld(p, i);
-                        }
+                        float x[4];
+                        RV::load_quad(s_x2[rbuf], t, wave * CT * 16 + 16 * ct + 4 * g, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) d = fmaf(x[i], y[ct][tt][i], d);
                     }
