@@ -8,94 +8,115 @@
 namespace kda {
 namespace {
 
-// A workgroup takes one (sequence, head, tile of W value columns). Thread t owns the float4 column group t % (W/4) of
-// the RPT consecutive key rows from RPT * (t / (W/4)) on: its q and k are one short run each, and a wavefront's
-// accesses to S are whole row pieces of 4W bytes.
-template <bool BF, int K, int W, int NT>
+// e^g of a log-decay: the rounding of g log2(e) is made up for (2^-24 of the exponent is 6e-7 of the result at g = -10).
+__device__ __forceinline__ float exp_decay(float g) {
+    const float x = g * 1.4426950408889634f;
+    const float rest = fmaf(g, 1.4426950408889634f, -x) + g * 1.9259629911266175e-8f;
+    const float e = __builtin_amdgcn_exp2f(x);
+    return x < -150.f ? e : fmaf(e, rest * 0.6931471805599453f, e);  // -inf: 0, and no inf - inf in the rest
+}
+
+// A workgroup of NT threads walks the (sequence, head) pairs blockIdx.x, blockIdx.x + gridDim.x, ...; while it updates
+// one it holds the next one's state and vectors in flight. Thread t owns the float4 column group t % (V/4) of the RPT
+// consecutive key rows from RPT * (t / (V/4)) on: its q and k are one short run each, a wavefront's accesses to S whole
+// rows. The partial read-outs of the wavefronts meet in LDS (two buffers: one barrier per pair).
+template <bool BF, int K, int V, int NT>
 __global__ __launch_bounds__(NT) void kda_hd_decode_kernel(const void *__restrict__ qp, const void *__restrict__ kp,
                                                            const void *__restrict__ vp, const void *__restrict__ gp,
                                                            float *__restrict__ S, void *__restrict__ op, int H,
-                                                           int group, int V, int decay_per_head, float scale) {
-    constexpr int CG = W / 4, RG = NT / CG, RPT = K / RG, NW = NT / 64;
-    static_assert(RPT >= 1 && RG * RPT == K && NT % 64 == 0, "unsupported K, W");
+                                                           int group, int decay_per_head, float scale, int32_t NH) {
+    constexpr int CG = V / 4, RG = NT / CG, RPT = K / RG, NW = NT / 64;
+    static_assert(RPT >= 1 && RG * RPT == K && NT % 64 == 0 && NW > 1, "unsupported K, V");
     using E = typename IO<BF>::T;
-    __shared__ f32x4 s_part[NW][CG];
+    __shared__ f32x4 s_part[2][NW][CG];
     const int t = threadIdx.x, cg = t % CG, rg = t / CG, lane = t & 63, wave = t >> 6;
-    const int tiles = V / W;
-    const int64_t nh = blockIdx.x / tiles;
-    const int c0 = (int)(blockIdx.x % tiles) * W + 4 * cg;
-    const int64_t n = nh / H;
-    const int h = (int)(nh - n * H);
-    const int64_t nk = n * (H / group) + h / group;
-    float *Sp = S + (nh * K + (int64_t)rg * RPT) * V + c0;
-    f32x4 s[RPT];
+    struct Pair {
+        f32x4 s[RPT];
+        float q[RPT], k[RPT], v[4], g;
+    };
+    auto take = [&](int32_t nh, Pair &x) __attribute__((always_inline)) {
+        const float *Sp = S + ((int64_t)nh * K + rg * RPT) * V + 4 * cg;
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(Sp + j * V));
-    const E *q = reinterpret_cast<const E *>(qp) + nk * K + rg * RPT;
-    const E *k = reinterpret_cast<const E *>(kp) + nk * K + rg * RPT;
-    const E *v = reinterpret_cast<const E *>(vp) + nh * V + c0;
-    float qr[RPT], kr[RPT], vv[4];
+        for (int j = 0; j < RPT; ++j) x.s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(Sp + j * V));
+        const int32_t n = nh / H, h = nh - n * H;
+        const int64_t nk = (int64_t)n * (H / group) + h / group;
+        const E *q = reinterpret_cast<const E *>(qp) + nk * K + rg * RPT;
+        const E *k = reinterpret_cast<const E *>(kp) + nk * K + rg * RPT;
+        const E *v = reinterpret_cast<const E *>(vp) + (int64_t)nh * V + 4 * cg;
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-        qr[j] = IO<BF>::ld(q, j);
-        kr[j] = IO<BF>::ld(k, j);
-    }
+        for (int j = 0; j < RPT; ++j) {
+            x.q[j] = IO<BF>::ld(q, j);
+            x.k[j] = IO<BF>::ld(k, j);
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) vv[j] = IO<BF>::ld(v, j);
-    const float g = decay_per_head ? reinterpret_cast<const float *>(gp)[h]
-                                   : IO<BF>::ld(reinterpret_cast<const E *>(gp), nh);
-    const float a = __builtin_amdgcn_exp2f(g * 1.4426950408889634f);
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 4; ++j) x.v[j] = IO<BF>::ld(v, j);
+        x.g = decay_per_head ? reinterpret_cast<const float *>(gp)[h] : IO<BF>::ld(reinterpret_cast<const E *>(gp), nh);
+    };
+    int32_t nh = blockIdx.x;  // gridDim.x <= NH
+    Pair x, next;
+    take(nh, x);
+    for (int buf = 0;; buf ^= 1) {
+        const int32_t nx = nh + gridDim.x;
+        if (nx < NH) take(nx, next);
+        const float a = exp_decay(x.g);
+        float *Sp = S + ((int64_t)nh * K + rg * RPT) * V + 4 * cg;
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-        s[j].x = fmaf(s[j].x, a, kr[j] * vv[0]);
-        s[j].y = fmaf(s[j].y, a, kr[j] * vv[1]);
-        s[j].z = fmaf(s[j].z, a, kr[j] * vv[2]);
-        s[j].w = fmaf(s[j].w, a, kr[j] * vv[3]);
-        __builtin_nontemporal_store(s[j], reinterpret_cast<f32x4 *>(Sp + j * V));
-        y.x = fmaf(s[j].x, qr[j], y.x);
-        y.y = fmaf(s[j].y, qr[j], y.y);
-        y.z = fmaf(s[j].z, qr[j], y.z);
-        y.w = fmaf(s[j].w, qr[j], y.w);
-    }
+        for (int j = 0; j < RPT; ++j) {
+            f32x4 s = x.s[j];
+            s.x = fmaf(s.x, a, x.k[j] * x.v[0]);
+            s.y = fmaf(s.y, a, x.k[j] * x.v[1]);
+            s.z = fmaf(s.z, a, x.k[j] * x.v[2]);
+            s.w = fmaf(s.w, a, x.k[j] * x.v[3]);
+            __builtin_nontemporal_store(s, reinterpret_cast<f32x4 *>(Sp + j * V));
+            y.x = fmaf(s.x, x.q[j], y.x);
+            y.y = fmaf(s.y, x.q[j], y.y);
+            y.z = fmaf(s.z, x.q[j], y.z);
+            y.w = fmaf(s.w, x.q[j], y.w);
+        }
 #pragma unroll
-    for (int d = CG; d < 64; d <<= 1) {  // row groups of a wavefront
-        y.x += __shfl_xor(y.x, d);
-        y.y += __shfl_xor(y.y, d);
-        y.z += __shfl_xor(y.z, d);
-        y.w += __shfl_xor(y.w, d);
-    }
-    if (NW > 1) {
-        if (lane < CG) s_part[wave][cg] = y;
+        for (int d = CG; d < 64; d <<= 1) {  // row groups of a wavefront
+            y.x += __shfl_xor(y.x, d);
+            y.y += __shfl_xor(y.y, d);
+            y.z += __shfl_xor(y.z, d);
+            y.w += __shfl_xor(y.w, d);
+        }
+        if (lane < CG) s_part[buf][wave][cg] = y;
         __syncthreads();
-    }
-    if (t < CG) {
+        if (t < CG) {
+            y = s_part[buf][0][t];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) y += s_part[w][t];
-        const int64_t ob = nh * V + c0;
-        if constexpr (BF)
-            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(op) + ob) =
-                make_uint2(pack_bf16(scale * y.x, scale * y.y), pack_bf16(scale * y.z, scale * y.w));
-        else
-            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(op) + ob) =
-                make_float4(scale * y.x, scale * y.y, scale * y.z, scale * y.w);
+            for (int w = 1; w < NW; ++w) y += s_part[buf][w][t];
+            y *= scale;
+            const int64_t ob = (int64_t)nh * V + 4 * t;
+            if constexpr (BF)
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(op) + ob) =
+                    make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+            else
+                *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(op) + ob) = y;
+        }
+        if (nx >= NH) break;
+        nh = nx;
+        x = next;
     }
 }
 
-template <bool BF, int K, int W>
-hipError_t launch_kw(const HdDecodeArgs &a, hipStream_t st) {
-    constexpr int NT = K * W / 4 < 512 ? K * W / 4 : 512;
-    const uint32_t grid = (uint32_t)((int64_t)a.N * a.H * (a.V / W));
-    hipLaunchKernelGGL((kda_hd_decode_kernel<BF, K, W, NT>), dim3(grid), dim3(NT), 0, st, a.q, a.k, a.v, a.g, a.S, a.o,
-                       a.H, a.H / a.Hk, a.V, (int)a.decay_per_head, a.scale);
+template <bool BF, int K, int V>
+hipError_t launch_kv(const HdDecodeArgs &a, hipStream_t st) {
+    constexpr int NT = K * V / 4 < 512 ? K * V / 4 : 512;
+    const int32_t NH = a.N * a.H;
+    // up to 4096 workgroups take one pair each; above that each walks about 4 pairs
+    const int32_t grid = NH <= 4096 ? NH : (NH + 3) / 4 > 4096 ? (NH + 3) / 4 : 4096;
+    hipLaunchKernelGGL((kda_hd_decode_kernel<BF, K, V, NT>), dim3(grid), dim3(NT), 0, st, a.q, a.k, a.v, a.g, a.S, a.o,
+                       a.H, a.H / a.Hk, (int)a.decay_per_head, a.scale, NH);
     return hipGetLastError();
 }
 template <bool BF, int K>
 hipError_t launch_k(const HdDecodeArgs &a, hipStream_t st) {
     switch (a.V) {
-        case 32: return launch_kw<BF, K, 32>(a, st);
-        case 64: return launch_kw<BF, K, 64>(a, st);
-        default: return launch_kw<BF, K, 128>(a, st);
+        case 32: return launch_kv<BF, K, 32>(a, st);
+        case 64: return launch_kv<BF, K, 64>(a, st);
+        default: return launch_kv<BF, K, 128>(a, st);
     }
 }
 template <bool BF>

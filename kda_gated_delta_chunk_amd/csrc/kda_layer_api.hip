@@ -5,6 +5,7 @@
 #include "../../include/kda.h"
 #include "kda_layer.hpp"
 
+#include <atomic>
 #include <cmath>
 
 namespace {
@@ -40,11 +41,14 @@ bool clash(const Range (&out)[NO], const Range (&in)[NI]) {
 }
 
 kda_status_t check_device() {
+    static std::atomic<bool> found{false};  // a device that was visible stays so
+    if (found.load(std::memory_order_relaxed)) return KDA_SUCCESS;
     int n = 0;
     if (hipGetDeviceCount(&n) != hipSuccess || n < 1) {
         (void)hipGetLastError();
         return KDA_ERROR_NO_DEVICE;
     }
+    found.store(true, std::memory_order_relaxed);
     return KDA_SUCCESS;
 }
 kda_status_t launched(hipError_t e) {

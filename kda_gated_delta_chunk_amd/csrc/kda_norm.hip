@@ -20,28 +20,31 @@
 namespace kda {
 namespace {
 
-constexpr int kMaxWG = 1024;  // row slots of the backward's grid are at most this many workgroups (and G's multiple)
+constexpr int kMaxWG = 512;  // row slots of the backward's grid are at most this many workgroups (and G's multiple)
 
+// Sums of NS values over the TPR threads of a row. Rows of several wavefronts meet in LDS, in one of two buffers in
+// turn: a wavefront that is a call ahead writes the other one, and cannot be two ahead of the barrier.
 template <int TPR, int NT, int NS>
-__device__ __forceinline__ void row_sums(float (&x)[NS], float *lds) {
+__device__ __forceinline__ void row_sums(float (&x)[NS], float (*lds)[4 * (NT / 64)], int &turn) {
 #pragma unroll
     for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1)
 #pragma unroll
         for (int i = 0; i < NS; ++i) x[i] += __shfl_xor(x[i], d);
     if constexpr (TPR > 64) {
+        static_assert(NS <= 4, "the buffers hold four sums");
         constexpr int NW = TPR / 64;
-        const int wave = threadIdx.x >> 6;
-        __syncthreads();  // the last sums have been read
+        const int wave = threadIdx.x >> 6, w0 = wave / NW * NW;
+        float *b = lds[turn];
+        turn ^= 1;
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
-            for (int i = 0; i < NS; ++i) lds[wave * NS + i] = x[i];
+            for (int i = 0; i < NS; ++i) b[wave * NS + i] = x[i];
         __syncthreads();
-        const int w0 = wave / NW * NW;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            float s = lds[w0 * NS + i];
+            float s = b[w0 * NS + i];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) s += lds[(w0 + w) * NS + i];
+            for (int w = 1; w < NW; ++w) s += b[(w0 + w) * NS + i];
             x[i] = s;
         }
     }
@@ -55,22 +58,38 @@ struct Slice {
     static __device__ __forceinline__ int at(int i, int t) {
         return VEC ? ((i / EL) * TPR + t) * EL + i % EL : i * TPR + t;
     }
-    static __device__ __forceinline__ void load(const void *p, int64_t row, int C, int t, float (&x)[EPT]) {
+    // as loaded: a row on its way while another is worked on
+    struct Raw {
+        typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+        u32x4 v[VEC ? EPT / EL : 1];
+        typename IO<BF>::T e[VEC ? 1 : EPT];
+    };
+    static __device__ __forceinline__ void load(const void *p, int64_t row, int C, int t, Raw &x) {
         using E = typename IO<BF>::T;
         const E *r = reinterpret_cast<const E *>(p) + row * C;
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < EPT; i += EL) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (at(i, t) < C) w = *reinterpret_cast<const uint4 *>(r + at(i, t));
-                E e[EL];
-                __builtin_memcpy(e, &w, 16);
+                x.v[i / EL] = typename Raw::u32x4{0, 0, 0, 0};
+                if (at(i, t) < C) x.v[i / EL] = *reinterpret_cast<const typename Raw::u32x4 *>(r + at(i, t));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x.e[i] = at(i, t) < C ? r[at(i, t)] : E(0);
+        }
+    }
+    static __device__ __forceinline__ void widen(const Raw &w, float (&x)[EPT]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += EL) {
+                typename IO<BF>::T e[EL];
+                __builtin_memcpy(e, &w.v[i / EL], 16);
 #pragma unroll
                 for (int j = 0; j < EL; ++j) x[i + j] = IO<BF>::ld(e, j);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) x[i] = at(i, t) < C ? IO<BF>::ld(r, at(i, t)) : 0.f;
+            for (int i = 0; i < EPT; ++i) x[i] = IO<BF>::ld(w.e, i);
         }
     }
     static __device__ __forceinline__ void store(void *p, int64_t row, int C, int t, const float (&x)[EPT]) {
@@ -120,27 +139,13 @@ struct Slice {
     }
 };
 
-// Statistics of a row in registers: x becomes x - mean, the result is r.
-template <bool BF, bool VEC, int TPR, int NT, int EPT>
-__device__ __forceinline__ float normalise(float (&x)[EPT], int C, int t, int center, float eps, float *lds) {
-    using SL = Slice<BF, VEC, TPR, EPT>;
-    const float inv = 1.f / (float)C;
-    if (center) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) s[0] += x[i];  // elements past the row are 0
-        row_sums<TPR, NT>(s, lds);
-        const float mean = s[0] * inv;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) x[i] = SL::at(i, t) < C ? x[i] - mean : 0.f;
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) s[0] = fmaf(x[i], x[i], s[0]);
-    row_sums<TPR, NT>(s, lds);
-    return rsqrtf(s[0] * inv + eps);
-}
+// A workgroup of 1024 threads with 16 elements each has no registers for a second row: no row in flight, one more round.
+template <int NT, int EPT>
+constexpr bool piped = NT * EPT < 1024 * 16;
 
+// A row's reductions go in two rounds, and the second shares one with the next row's first (its values are in flight
+// meanwhile and arrive by then): the sum for the mean, then everything that needs it. d = e w does not depend on the
+// statistics and n = (x - mean) r only through r, so mean(d n) = r mean(d (x - mean)) needs no round of its own.
 template <bool BF, bool VEC, int TPR, int NT, int EPT>
 __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict__ xp, const void *__restrict__ zp,
                                                           const float *__restrict__ wp, const float *__restrict__ bp,
@@ -148,26 +153,66 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
                                                           int center) {
     using SL = Slice<BF, VEC, TPR, EPT>;
     constexpr int RPW = NT / TPR;
-    __shared__ float lds[NT / 64];
+    __shared__ float lds[2][4 * (NT / 64)];
+    int turn = 0;
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t slot = (int64_t)blockIdx.x * RPW + sub, slots = (int64_t)gridDim.x * RPW;
+    const float inv = 1.f / (float)C;
     float w[EPT], b[EPT];
     SL::param(wp, slot % G, C, t, 1.f, w);
     SL::param(bp, slot % G, C, t, 0.f, b);
     const int64_t turns = (rows + slots - 1) / slots;  // the same for all threads: the sums hold barriers
+    auto row_of = [&](int64_t i) { const int64_t r = i * slots + slot; return r < rows ? r : rows - 1; };
+    constexpr bool PIPE = piped<NT, EPT>;
+    typename SL::Raw rx, rz;
+    float x[EPT], z[EPT], mean[1];
+    auto first_round = [&](int64_t i) __attribute__((always_inline)) {
+        SL::load(xp, row_of(i), C, t, rx);
+        if (zp) SL::load(zp, row_of(i), C, t, rz);
+        SL::widen(rx, x);
+        if (zp) SL::widen(rz, z);
+        mean[0] = 0.f;
+        if (!center) return;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) mean[0] += x[e];  // elements past the row are 0
+        row_sums<TPR, NT>(mean, lds, turn);
+    };
+    first_round(0);
     for (int64_t i = 0; i < turns; ++i) {
-        const int64_t row = i * slots + slot;
-        const bool mine = row < rows;
-        float x[EPT], z[EPT];
-        SL::load(xp, mine ? row : 0, C, t, x);
-        if (zp) SL::load(zp, mine ? row : 0, C, t, z);
-        const float r = normalise<BF, VEC, TPR, NT>(x, C, t, center, eps, lds);
+        const bool next = PIPE && i + 1 < turns;
+        if (!PIPE && i > 0) first_round(i);
+        if (next) {
+            SL::load(xp, row_of(i + 1), C, t, rx);
+            if (zp) SL::load(zp, row_of(i + 1), C, t, rz);
+        }
+        const float mu = mean[0] * inv;
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            x[e] = SL::at(e, t) < C ? x[e] - mu : 0.f;
+            s[0] = fmaf(x[e], x[e], s[0]);
+        }
+        float nx[EPT];
+        if (next) {
+            SL::widen(rx, nx);
+            if (center)
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) s[1] += nx[e];
+        }
+        row_sums<TPR, NT>(s, lds, turn);
+        const float r = rsqrtf(s[0] * inv + eps);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             x[e] = fmaf(x[e] * r, w[e], b[e]);
             if (zp) x[e] *= sigmoid_f(z[e]);
         }
-        if (mine) SL::store(yp, row, C, t, x);
+        if (i * slots + slot < rows) SL::store(yp, i * slots + slot, C, t, x);
+        if (next) {
+            mean[0] = s[1];
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) x[e] = nx[e];
+            if (zp) SL::widen(rz, z);
+        }
     }
 }
 
@@ -181,48 +226,93 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
                                                           float eps, int center) {
     using SL = Slice<BF, VEC, TPR, EPT>;
     constexpr int RPW = NT / TPR;
-    __shared__ float lds[2 * (NT / 64)];
+    __shared__ float lds[2][4 * (NT / 64)];
+    int turn = 0;
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t slot = (int64_t)blockIdx.x * RPW + sub, slots = (int64_t)gridDim.x * RPW;
     const float inv = 1.f / (float)C;
-    float w[EPT], b[EPT], dw[EPT], db[EPT];
+    float w[EPT], dw[EPT], db[EPT];
     SL::param(wp, slot % G, C, t, 1.f, w);
-    SL::param(bp, slot % G, C, t, 0.f, b);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) dw[e] = db[e] = 0.f;
     const int64_t turns = (rows + slots - 1) / slots;
+    auto row_of = [&](int64_t i) { const int64_t r = i * slots + slot; return r < rows ? r : rows - 1; };
+    constexpr bool PIPE = piped<NT, EPT>;
+    typename SL::Raw rx, rd, rz;
+    float x[EPT], mean[1];
+    auto first_round = [&](int64_t i) __attribute__((always_inline)) {
+        SL::load(xp, row_of(i), C, t, rx);
+        SL::load(dyp, row_of(i), C, t, rd);
+        if (zp) SL::load(zp, row_of(i), C, t, rz);
+        SL::widen(rx, x);
+        mean[0] = 0.f;
+        if (!center) return;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) mean[0] += x[e];
+        row_sums<TPR, NT>(mean, lds, turn);
+    };
+    first_round(0);
     for (int64_t i = 0; i < turns; ++i) {
-        const int64_t row = i * slots + slot;
-        const bool mine = row < rows;
-        float x[EPT], d[EPT], z[EPT];
-        SL::load(xp, mine ? row : 0, C, t, x);
-        SL::load(dyp, mine ? row : 0, C, t, d);
-        if (zp) SL::load(zp, mine ? row : 0, C, t, z);
-        const float r = normalise<BF, VEC, TPR, NT>(x, C, t, center, eps, lds);
-        float s[2] = {0.f, 0.f};
+        const bool mine = i * slots + slot < rows, next = PIPE && i + 1 < turns;
+        if (!PIPE) {  // the parameters come anew, too
+            if (i > 0) first_round(i);
+            SL::param(wp, slot % G, C, t, 1.f, w);
+        }
+        float d[EPT], a[EPT];
+        SL::widen(rd, d);
+        if (zp) SL::widen(rz, a);
+        if (next) {
+            SL::load(xp, row_of(i + 1), C, t, rx);
+            SL::load(dyp, row_of(i + 1), C, t, rd);
+            if (zp) SL::load(zp, row_of(i + 1), C, t, rz);
+        }
+        const float mu = mean[0] * inv;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            x[e] = SL::at(e, t) < C ? x[e] - mu : 0.f;
+            const float g = zp ? sigmoid_f(a[e]) : 1.f;
+            a[e] = d[e] * (1.f - g);  // what dz has beside y g
+            d[e] *= g;
+            const float dn = d[e] * w[e];
+            s[0] = fmaf(x[e], x[e], s[0]);
+            s[1] = fmaf(dn, x[e], s[1]);
+            s[2] += dn;
+            if (zp) a[e] *= g;
+        }
+        float nx[EPT];
+        if (next) {
+            SL::widen(rx, nx);
+            if (center)
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) s[3] += nx[e];
+        }
+        row_sums<TPR, NT>(s, lds, turn);
+        const float r = rsqrtf(s[0] * inv + eps);
+        const float m1 = r * s[1] * inv, m2 = center ? s[2] * inv : 0.f;
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             x[e] *= r;  // n
-            if (zp) {
-                const float a = sigmoid_f(z[e]);
-                z[e] = d[e] * fmaf(x[e], w[e], b[e]) * a * (1.f - a);
-                d[e] *= a;
-            }
             if (mine) {
                 dw[e] = fmaf(d[e], x[e], dw[e]);
                 db[e] += d[e];
             }
-            d[e] *= w[e];
-            s[0] = fmaf(d[e], x[e], s[0]);
-            s[1] += d[e];
+            d[e] = r * (d[e] * w[e] - fmaf(x[e], m1, m2));
         }
-        row_sums<TPR, NT>(s, lds);
-        const float m1 = s[0] * inv, m2 = center ? s[1] * inv : 0.f;
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) x[e] = r * (d[e] - fmaf(x[e], m1, m2));
         if (mine) {
-            SL::store(dxp, row, C, t, x);
-            if (zp) SL::store(dzp, row, C, t, z);
+            SL::store(dxp, i * slots + slot, C, t, d);
+            if (zp) {
+                float bb[EPT];
+                SL::param(bp, slot % G, C, t, 0.f, bb);
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) a[e] *= fmaf(x[e], w[e], bb[e]);
+                SL::store(dzp, i * slots + slot, C, t, a);
+            }
+        }
+        if (next) {
+            mean[0] = s[3];
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) x[e] = nx[e];
         }
     }
     if (want_dw) SL::store_param(part, slot, C, t, dw);
@@ -294,8 +384,8 @@ hipError_t by_width(const NormArgs &a, bool bwd, hipStream_t st) {
     if (C <= 16 * 8) return run_norm<BF, VEC, 16, 256, 8>(a, bwd, st);
     if (C <= 64 * 8) return run_norm<BF, VEC, 64, 256, 8>(a, bwd, st);
     if (C <= 256 * 8) return run_norm<BF, VEC, 256, 256, 8>(a, bwd, st);
-    if (C <= 256 * 16) return run_norm<BF, VEC, 256, 256, 16>(a, bwd, st);
-    if (C <= 512 * 16) return run_norm<BF, VEC, 512, 512, 16>(a, bwd, st);
+    if (C <= 512 * 8) return run_norm<BF, VEC, 512, 512, 8>(a, bwd, st);
+    if (C <= 1024 * 8) return run_norm<BF, VEC, 1024, 1024, 8>(a, bwd, st);
     return run_norm<BF, VEC, 1024, 1024, 16>(a, bwd, st);
 }
 hipError_t by_type(const NormArgs &a, bool bwd, hipStream_t st) {

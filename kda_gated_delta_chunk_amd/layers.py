@@ -10,21 +10,33 @@ import math
 
 import torch
 
-from . import KDAError, _io_code, _lib, _need, _ptr
+from . import KDAError, _io_code, _lib, _ptr
+from . import _need as _explain
 
 __all__ = ["hd_chunk_fwd", "hd_chunk_bwd", "hd_decode_step", "hd_workspace_bytes", "hd_bwd_workspace_bytes", "rotary",
            "rotary_freqs", "layer_norm_fwd", "layer_norm_bwd"]
 
 
+# the current stream's handle by device index, without making a Stream object of it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(dev, fn, *args) -> None:
     """fn(*args, stream) on dev's current stream, with dev current while the kernels are enqueued."""
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(i))
     if status:
         raise KDAError(status, fn.__name__)
+
+
+def _need(t, name, shape, dtype, dev):
+    """The package's check of an argument; what is right passes on one line (small calls cost little else)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _explain(t, name, shape, dtype, dev)
 
 
 def _cuda(t):
