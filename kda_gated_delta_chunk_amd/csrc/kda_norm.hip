@@ -40,13 +40,14 @@ __device__ __forceinline__ void row_sums(float (&x)[NS], float (*lds)[4 * (NT / 
 #pragma unroll
             for (int i = 0; i < NS; ++i) b[wave * NS + i] = x[i];
         __syncthreads();
+        // a lane per (wavefront, sum): NS values a wavefront, at most 64
+        static_assert(NW * NS <= 64 && (NS & (NS - 1)) == 0, "one value per lane");
+        const int lane = threadIdx.x & 63;
+        float v = b[w0 * NS + (lane & (NW * NS - 1))];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            float s = b[w0 * NS + i];
+        for (int d = NS; d < NW * NS; d <<= 1) v += __shfl_xor(v, d);
 #pragma unroll
-            for (int w = 1; w < NW; ++w) s += b[(w0 + w) * NS + i];
-            x[i] = s;
-        }
+        for (int i = 0; i < NS; ++i) x[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), i));
     }
 }
 
@@ -146,7 +147,7 @@ constexpr bool piped = NT * EPT < 1024 * 16;
 // A row's reductions go in two rounds, and the second shares one with the next row's first (its values are in flight
 // meanwhile and arrive by then): the sum for the mean, then everything that needs it. d = e w does not depend on the
 // statistics and n = (x - mean) r only through r, so mean(d n) = r mean(d (x - mean)) needs no round of its own.
-template <bool BF, bool VEC, int TPR, int NT, int EPT>
+template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
 __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict__ xp, const void *__restrict__ zp,
                                                           const float *__restrict__ wp, const float *__restrict__ bp,
                                                           void *__restrict__ yp, int64_t rows, int G, int C, float eps,
@@ -168,9 +169,9 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
     float x[EPT], z[EPT], mean[1];
     auto first_round = [&](int64_t i) __attribute__((always_inline)) {
         SL::load(xp, row_of(i), C, t, rx);
-        if (zp) SL::load(zp, row_of(i), C, t, rz);
+        if (GATE) SL::load(zp, row_of(i), C, t, rz);
         SL::widen(rx, x);
-        if (zp) SL::widen(rz, z);
+        if (GATE) SL::widen(rz, z);
         mean[0] = 0.f;
         if (!center) return;
 #pragma unroll
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
         if (!PIPE && i > 0) first_round(i);
         if (next) {
             SL::load(xp, row_of(i + 1), C, t, rx);
-            if (zp) SL::load(zp, row_of(i + 1), C, t, rz);
+            if (GATE) SL::load(zp, row_of(i + 1), C, t, rz);
         }
         const float mu = mean[0] * inv;
         float s[2] = {0.f, 0.f};
@@ -204,21 +205,21 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             x[e] = fmaf(x[e] * r, w[e], b[e]);
-            if (zp) x[e] *= sigmoid_f(z[e]);
+            if (GATE) x[e] *= sigmoid_f(z[e]);
         }
         if (i * slots + slot < rows) SL::store(yp, i * slots + slot, C, t, x);
         if (next) {
             mean[0] = s[1];
 #pragma unroll
             for (int e = 0; e < EPT; ++e) x[e] = nx[e];
-            if (zp) SL::widen(rz, z);
+            if (GATE) SL::widen(rz, z);
         }
     }
 }
 
 // part: [2][slots][C] fp32, the sums of e n and of e over the rows of each slot
-template <bool BF, bool VEC, int TPR, int NT, int EPT>
-__global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict__ dyp, const void *__restrict__ xp,
+template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
+__global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void kda_norm_bwd_kernel(const void *__restrict__ dyp, const void *__restrict__ xp,
                                                           const void *__restrict__ zp, const float *__restrict__ wp,
                                                           const float *__restrict__ bp, void *__restrict__ dxp,
                                                           void *__restrict__ dzp, float *__restrict__ part,
@@ -231,10 +232,16 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t slot = (int64_t)blockIdx.x * RPW + sub, slots = (int64_t)gridDim.x * RPW;
     const float inv = 1.f / (float)C;
+    // the parameters' sums: registers, or LDS where 1024 threads of 16 elements leave none
+    constexpr bool LACC = !piped<NT, EPT>;
+    __shared__ float s_acc[LACC ? 2 * EPT : 1][LACC ? NT : 1];
     float w[EPT], dw[EPT], db[EPT];
     SL::param(wp, slot % G, C, t, 1.f, w);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) dw[e] = db[e] = 0.f;
+    for (int e = 0; e < EPT; ++e) {
+        dw[e] = db[e] = 0.f;
+        if constexpr (LACC) s_acc[e][threadIdx.x] = s_acc[EPT + e][threadIdx.x] = 0.f;
+    }
     const int64_t turns = (rows + slots - 1) / slots;
     auto row_of = [&](int64_t i) { const int64_t r = i * slots + slot; return r < rows ? r : rows - 1; };
     constexpr bool PIPE = piped<NT, EPT>;
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
     auto first_round = [&](int64_t i) __attribute__((always_inline)) {
         SL::load(xp, row_of(i), C, t, rx);
         SL::load(dyp, row_of(i), C, t, rd);
-        if (zp) SL::load(zp, row_of(i), C, t, rz);
+        if (GATE) SL::load(zp, row_of(i), C, t, rz);
         SL::widen(rx, x);
         mean[0] = 0.f;
         if (!center) return;
@@ -260,25 +267,25 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
         }
         float d[EPT], a[EPT];
         SL::widen(rd, d);
-        if (zp) SL::widen(rz, a);
+        if (GATE) SL::widen(rz, a);
         if (next) {
             SL::load(xp, row_of(i + 1), C, t, rx);
             SL::load(dyp, row_of(i + 1), C, t, rd);
-            if (zp) SL::load(zp, row_of(i + 1), C, t, rz);
+            if (GATE) SL::load(zp, row_of(i + 1), C, t, rz);
         }
         const float mu = mean[0] * inv;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             x[e] = SL::at(e, t) < C ? x[e] - mu : 0.f;
-            const float g = zp ? sigmoid_f(a[e]) : 1.f;
+            const float g = GATE ? sigmoid_f(a[e]) : 1.f;
             a[e] = d[e] * (1.f - g);  // what dz has beside y g
             d[e] *= g;
             const float dn = d[e] * w[e];
             s[0] = fmaf(x[e], x[e], s[0]);
             s[1] = fmaf(dn, x[e], s[1]);
             s[2] += dn;
-            if (zp) a[e] *= g;
+            if (GATE) a[e] *= g;
         }
         float nx[EPT];
         if (next) {
@@ -294,14 +301,19 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
         for (int e = 0; e < EPT; ++e) {
             x[e] *= r;  // n
             if (mine) {
-                dw[e] = fmaf(d[e], x[e], dw[e]);
-                db[e] += d[e];
+                if constexpr (LACC) {
+                    s_acc[e][threadIdx.x] = fmaf(d[e], x[e], s_acc[e][threadIdx.x]);
+                    s_acc[EPT + e][threadIdx.x] += d[e];
+                } else {
+                    dw[e] = fmaf(d[e], x[e], dw[e]);
+                    db[e] += d[e];
+                }
             }
             d[e] = r * (d[e] * w[e] - fmaf(x[e], m1, m2));
         }
         if (mine) {
             SL::store(dxp, i * slots + slot, C, t, d);
-            if (zp) {
+            if (GATE) {
                 float bb[EPT];
                 SL::param(bp, slot % G, C, t, 0.f, bb);
 #pragma unroll
@@ -315,6 +327,12 @@ __global__ __launch_bounds__(NT) void kda_norm_bwd_kernel(const void *__restrict
             for (int e = 0; e < EPT; ++e) x[e] = nx[e];
         }
     }
+    if constexpr (LACC)
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            dw[e] = s_acc[e][threadIdx.x];
+            db[e] = s_acc[EPT + e][threadIdx.x];
+        }
     if (want_dw) SL::store_param(part, slot, C, t, dw);
     if (want_db) SL::store_param(part + slots * C, slot, C, t, db);
 }
@@ -355,19 +373,19 @@ int64_t grid_for(int64_t rows, int G, int rpw, int64_t most) {
     return wgs;
 }
 
-template <bool BF, bool VEC, int TPR, int NT, int EPT>
-hipError_t run_norm(const NormArgs &a, bool bwd, hipStream_t st) {
+template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
+hipError_t run_gate(const NormArgs &a, bool bwd, hipStream_t st) {
     constexpr int RPW = NT / TPR;
     if (!bwd) {
         const int64_t wgs = grid_for(a.rows, a.G, RPW, 2048);
-        hipLaunchKernelGGL((kda_norm_fwd_kernel<BF, VEC, TPR, NT, EPT>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.x,
-                           a.gate, a.weight, a.bias, a.y, a.rows, a.G, a.C, a.eps, (int)a.center);
+        hipLaunchKernelGGL((kda_norm_fwd_kernel<BF, VEC, TPR, NT, EPT, GATE>), dim3((uint32_t)wgs), dim3(NT), 0, st,
+                           a.x, a.gate, a.weight, a.bias, a.y, a.rows, a.G, a.C, a.eps, (int)a.center);
         return hipGetLastError();
     }
     const int64_t wgs = grid_for(a.rows, a.G, RPW, kMaxWG);
     float *part = reinterpret_cast<float *>(a.workspace);
-    hipLaunchKernelGGL((kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.dy, a.x,
-                       a.gate, a.weight, a.bias, a.dx, a.dgate, part, (int)(a.dweight != nullptr),
+    hipLaunchKernelGGL((kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT, GATE>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.dy,
+                       a.x, a.gate, a.weight, a.bias, a.dx, a.dgate, part, (int)(a.dweight != nullptr),
                        (int)(a.dbias != nullptr), a.rows, a.G, a.C, a.eps, (int)a.center);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
@@ -375,6 +393,10 @@ hipError_t run_norm(const NormArgs &a, bool bwd, hipStream_t st) {
     hipLaunchKernelGGL(kda_norm_param_kernel, dim3((uint32_t)((cols + 63) / 64), 2), dim3(1024), 0, st, part,
                        a.dweight, a.dbias, wgs * RPW, a.G, a.C);
     return hipGetLastError();
+}
+template <bool BF, bool VEC, int TPR, int NT, int EPT>
+hipError_t run_norm(const NormArgs &a, bool bwd, hipStream_t st) {
+    return a.gate ? run_gate<BF, VEC, TPR, NT, EPT, true>(a, bwd, st) : run_gate<BF, VEC, TPR, NT, EPT, false>(a, bwd, st);
 }
 
 template <bool BF, bool VEC>

@@ -74,6 +74,26 @@ __device__ __forceinline__ void store_run(void *p, const float (&x)[E]) {
     *reinterpret_cast<W *>(p) = w;
 }
 
+// E pairs of a unit: (x[i], y[i]), or adjacent channels of x followed by y.
+template <int E, bool INTER>
+__device__ __forceinline__ void turn_run(float (&x)[E], float (&y)[E], const float (&cs)[E], const float (&sn)[E]) {
+    auto turn = [](float &a, float &b, float c, float s) __attribute__((always_inline)) {
+        const float r = a * c - b * s;
+        b = a * s + b * c;
+        a = r;
+    };
+    if constexpr (!INTER || E == 1) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) turn(x[i], y[i], cs[i], sn[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+            turn(y[2 * i], y[2 * i + 1], cs[E / 2 + i], sn[E / 2 + i]);
+        }
+    }
+}
+
 // A unit is a run of E pairs or, behind them, a run of 2E copied channels; an interleaved unit that straddles R turns
 // its pairs from R on by nothing. Threads of a workgroup: `units` consecutive ones per head, heads_par heads at a
 // time, tok_par tokens at a time. q_out and k_out may be q and k: a thread reads its channels before it writes them.
@@ -87,8 +107,8 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     const int per_tok = units * heads_par;
     const int tsub = threadIdx.x / per_tok;
     if (tsub >= tok_par) return;
-    const int r = threadIdx.x - tsub * per_tok;
-    const int hsub = r / units, u = r - hsub * units;
+    const int in_tok = threadIdx.x - tsub * per_tok;
+    const int hsub = in_tok / units, u = in_tok - hsub * units;
     const int np = (R / 2 + E - 1) / E;  // units with pairs to turn
     const bool pairs = u < np;
     uint64_t fr[E];
@@ -98,10 +118,32 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     const int c0 = INTER ? 2 * E * u : pairs ? E * u : R + 2 * E * (u - np);
     const int c1 = pairs && !INTER ? c0 + R / 2 : c0 + E;
     const bool two = c1 + E <= D;  // a last copied run may be half as long
-    for (int64_t t = (int64_t)blockIdx.x * tok_par + tsub; t < tokens; t += (int64_t)gridDim.x * tok_par) {
+    // A row (token, head) in flight: the next one's loads go out before this one is turned.
+    struct Row {
+        float x[E], y[E];
+        char *d;
+        bool live;
+    };
+    auto take = [&](int64_t t, int h, Row &r) __attribute__((always_inline)) {
+        const bool isq = h < Hq;
+        const char *src = isq ? (const char *)qp : (const char *)kp;
+        char *dst = isq ? (char *)qo : (char *)ko;
+        const int64_t row = (isq ? t * Hq + h : t * Hk + (h - Hq)) * D * ES;
+        r.d = dst + row;
+        r.live = t < tokens && (pairs || src != dst);  // in place there is nothing to copy
+        if (!r.live) return;
+        load_run<BF, E>(src + row + c0 * ES, r.x);
+        if (two) load_run<BF, E>(src + row + c1 * ES, r.y);
+    };
+    const int64_t step = (int64_t)gridDim.x * tok_par;
+    Row r = {};
+    int64_t t = (int64_t)blockIdx.x * tok_par + tsub;
+    take(t, hsub, r);
+    for (; t < tokens; t += step) {
         float cs[E], sn[E];
         if (pairs) {
-            const int64_t pos = positions ? (int64_t)positions[t] : t % T;
+            const int64_t pos = positions ? (int64_t)positions[t]
+                              : tokens <= 0xffffffffll ? (int64_t)((uint32_t)t % (uint32_t)T) : t % T;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 sincos_turn(fr[i] * (uint64_t)pos, sn[i], cs[i]);
@@ -111,45 +153,15 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
             }
         }
         for (int h = hsub; h < Hq + Hk; h += heads_par) {
-            const bool isq = h < Hq;
-            const char *src = isq ? (const char *)qp : (const char *)kp;
-            char *dst = isq ? (char *)qo : (char *)ko;
-            if (!pairs && src == dst) continue;  // in place: nothing to copy
-            const int64_t row = isq ? t * Hq + h : t * Hk + (h - Hq);
-            const char *s = src + row * D * ES;
-            char *d = dst + row * D * ES;
-            float x[E], y[E] = {};
-            load_run<BF, E>(s + c0 * ES, x);
-            if (two) load_run<BF, E>(s + c1 * ES, y);
-            if (pairs) {
-                float v[E], w[E];
-                if constexpr (INTER) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float p1 = 2 * i < E ? x[(2 * i) % E] : y[(2 * i) % E];
-                        const float p2 = 2 * i < E ? x[(2 * i + 1) % E] : y[(2 * i + 1) % E];
-                        if constexpr (E == 1) {  // one pair: x[0] and y[0]
-                            v[0] = x[0] * cs[0] - y[0] * sn[0];
-                            w[0] = x[0] * sn[0] + y[0] * cs[0];
-                        } else {
-                            const float r1 = p1 * cs[i] - p2 * sn[i], r2 = p1 * sn[i] + p2 * cs[i];
-                            if (2 * i < E) { v[(2 * i) % E] = r1; v[(2 * i + 1) % E] = r2; }
-                            else { w[(2 * i) % E] = r1; w[(2 * i + 1) % E] = r2; }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        v[i] = x[i] * cs[i] - y[i] * sn[i];
-                        w[i] = x[i] * sn[i] + y[i] * cs[i];
-                    }
-                }
-                store_run<BF, E>(d + c0 * ES, v);
-                if (two) store_run<BF, E>(d + c1 * ES, w);
-            } else {
-                store_run<BF, E>(d + c0 * ES, x);
-                if (two) store_run<BF, E>(d + c1 * ES, y);
+            Row next = {};
+            const bool more = h + heads_par < Hq + Hk;
+            take(more ? t : t + step, more ? h + heads_par : hsub, next);
+            if (r.live) {
+                if (pairs) turn_run<E, INTER>(r.x, r.y, cs, sn);
+                store_run<BF, E>(r.d + c0 * ES, r.x);
+                if (two) store_run<BF, E>(r.d + c1 * ES, r.y);
             }
+            r = next;
         }
     }
 }
@@ -165,7 +177,7 @@ hipError_t launch_e(const RotaryArgs &a, hipStream_t st) {
     int tok_par = 256 / (units * heads_par);
     if (tok_par < 1) tok_par = 1;
     int64_t wgs = (a.tokens + tok_par - 1) / tok_par;
-    if (wgs > 16384) wgs = 16384;
+    if (wgs > 4096) wgs = 4096;  // a thread's frequencies serve several tokens
     const float sgn = a.inverse ? -1.f : 1.f;
     if (a.interleaved)
         hipLaunchKernelGGL((kda_rotary_kernel<BF, E, true>), dim3((uint32_t)wgs), dim3(256), 0, st, a.q, a.k, a.q_out,
