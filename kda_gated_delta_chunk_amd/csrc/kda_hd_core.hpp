@@ -36,47 +36,62 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 constexpr int kChunk = 32;  // tokens per chunk
 
 // ------------------------------------------------------------------ rows in LDS
-// NCOL elements a row. bf16: the 8-byte units of a row are permuted by an exclusive or with bits of the row's index,
-// chosen (r0..r3: the index's low bits) so that 16 rows at one unit (a row read's 16 lanes), those at two adjacent ones
-// (32 lanes), 4 rows at 4 adjacent units (a transposing read's 16 lanes) and 8 rows at 4 (32 lanes) all fall on
-// different banks, whatever the row's length adds. fp32: rows padded by 16 bytes to the same end.
+// NCOL elements a row. bf16: the 16-byte slots of a row are permuted by an exclusive or with bits of the row's index,
+// chosen so that 8 rows at one slot (a row read's eight lanes) and 4 rows at two adjacent slots (a transposing read's
+// sixteen) fall on different banks. fp32: rows padded by 16 bytes to the same end.
+//
+// Which index an operand's slot or a state tile's row stands for is free as long as both operands of a product agree:
+//   bf16: channel slots 0-7 of a 32-deep product <-> channels 32c + 8g + j (one 16-byte read of a row), so row 4g + i of
+//         the state's tile kt is channel 32 (kt / 2) + 8g + 4 (kt % 2) + i; token slots <-> tokens 8g + j;
+//   fp32: slots 0-3 <-> 4g + i, slots 4-7 <-> 16 + 4g + i, tile rows in order.
 template <bool BF, int NCOL> struct Rows;
 template <int NCOL> struct Rows<true, NCOL> {
     static constexpr int NS = NCOL / 8, RB = NCOL * 2;
     static constexpr int bytes(int rows) { return rows * RB; }
     static __device__ __forceinline__ int swz(int row) {
-        const int r0 = row & 1, r1 = (row >> 1) & 1, r2 = (row >> 2) & 1, r3 = (row >> 3) & 1;
-        if (NCOL == 128) return (r2 << 4) | (r1 << 3) | (r0 << 2) | (r3 << 1) | r2;
-        if (NCOL == 64) return (r1 << 3) | ((r0 ^ r2) << 2) | (r3 << 1) | r2;
-        return ((r1 ^ r2) << 2) | (r3 << 1) | r2;
+        if (NCOL == 32) return (row & 2) | ((row >> 2) & 1);
+        return ((row & 3) << 1) | ((row >> 2) & 1) | (NCOL == 128 ? row & 8 : 0);
     }
-    static __device__ __forceinline__ int quad(int row, int col) { return row * RB + (((col >> 2) ^ swz(row)) << 3); }
-    // 16 bytes from column 8s on: two units that stay neighbours, in either order
+    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + ((s ^ swz(row)) << 4); }
+    static __device__ __forceinline__ int quad(int row, int col) { return slot(row, col >> 3) + ((col & 4) << 1); }
     static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
-        const int at = quad(row, 8 * s);
-        *reinterpret_cast<u32x2 *>(t + at) = u32x2{w.x, w.y};
-        *reinterpret_cast<u32x2 *>(t + (at ^ 8)) = u32x2{w.z, w.w};
+        *reinterpret_cast<u32x4 *>(t + slot(row, s)) = w;
     }
-    // Operand with slots 0-3 <-> columns 32c + 4g + i, 4-7 <-> 32c + 16 + 4g + i of row l%16 (+ what is added to t).
-    // at: row_at(lane), the lane's address for c = 0; the others differ from it in the bits of c alone.
-    static __device__ __forceinline__ int row_at(int lane) { return quad(lane & 15, 4 * (lane >> 4)); }
+    static __device__ __forceinline__ int state_row(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
+    static __device__ __forceinline__ int token(int half, int g) { return 8 * g + 4 * half; }  // of slots 4 half + i
+    // Channels 32c .. 32c+31 of row l%16 (+ what is added to t). at: row_at(lane), the lane's address for c = 0; the
+    // others differ from it in the bits of c alone.
+    static __device__ __forceinline__ int row_at(int lane) { return slot(lane & 15, lane >> 4); }
     static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int at, int c) {
-        const u32x2 u = *reinterpret_cast<const u32x2 *>(t + (at ^ (c << 6)));
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(t + (at ^ (c << 6 | 32)));
+        const u32x4 u = *reinterpret_cast<const u32x4 *>(t + (at ^ (c << 6)));
         Frag8<true> f;
-        f.p[0] = u.x; f.p[1] = u.y; f.p[2] = w.x; f.p[3] = w.y;
+        f.p[0] = u.x; f.p[1] = u.y; f.p[2] = u.z; f.p[3] = u.w;
         return f;
     }
-    // Operand with the same slot map along 32 rows, column 16c + l%16; at: col_at(lane).
-    static __device__ __forceinline__ int col_at(int lane) { return quad(4 * (lane >> 4) + ((lane >> 2) & 3), 4 * (lane & 3)); }
-    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int at, int c) {
+    // 32 tokens at the column of lane l%16. The transposing read gives lane i of sixteen column i of a 4 x 16 block, of
+    // which its lane j holds the four elements j % 4 of row j / 4. ats: the addresses for the first and second four
+    // tokens of the lanes' groups (the row's bit 2 moves its slots by one).
+    static __device__ __forceinline__ Frag8<true> tr_frag(const char *t, int at, int at4) {
         typedef __attribute__((address_space(3))) s16x4 *lds4;
-        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + (at ^ (c << 5))));
-        const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + (at ^ (c << 5)) + 16 * RB));
+        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + at));
+        const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + at4));
         const uint2 a = __builtin_bit_cast(uint2, u), b = __builtin_bit_cast(uint2, w);
         Frag8<true> f;
         f.p[0] = a.x; f.p[1] = a.y; f.p[2] = b.x; f.p[3] = b.y;
         return f;
+    }
+    static __device__ __forceinline__ int col_row(int lane) { return 8 * (lane >> 4) + ((lane >> 2) & 3); }
+    // plain columns 16c + l%16
+    static __device__ __forceinline__ int col_at(int lane) { return slot(col_row(lane), (lane >> 1) & 1) + (lane & 1) * 8; }
+    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int at, int c) {
+        const int x = at ^ (c << 5);
+        return tr_frag(t, x, (x ^ 16) + 4 * RB);
+    }
+    // the channels of the state tile kt
+    static __device__ __forceinline__ int tile_at(int lane) { return slot(col_row(lane), lane & 3); }
+    static __device__ __forceinline__ Frag8<true> tile_frag(const char *t, int at, int kt) {
+        const int x = at ^ (kt >> 1 << 6);
+        return tr_frag(t, x + 8 * (kt & 1), (x ^ 16) + 4 * RB + 8 * (kt & 1));
     }
     static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
         *reinterpret_cast<uint2 *>(t + quad(row, col)) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
@@ -93,6 +108,8 @@ template <int NCOL> struct Rows<false, NCOL> {
     static __device__ __forceinline__ void put16(char *t, int row, int s, u32x4 w) {
         *reinterpret_cast<u32x4 *>(t + row * RB + (s << 4)) = w;
     }
+    static __device__ __forceinline__ int state_row(int kt, int g) { return 16 * kt + 4 * g; }
+    static __device__ __forceinline__ int token(int half, int g) { return 16 * half + 4 * g; }
     static __device__ __forceinline__ int row_at(int lane) { return quad(lane & 15, 4 * (lane >> 4)); }
     static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int at, int c) {
         const f32x4 u = *reinterpret_cast<const f32x4 *>(t + at + 128 * c);
@@ -109,6 +126,8 @@ template <int NCOL> struct Rows<false, NCOL> {
         }
         return f;
     }
+    static __device__ __forceinline__ int tile_at(int lane) { return col_at(lane); }
+    static __device__ __forceinline__ Frag8<false> tile_frag(const char *t, int at, int kt) { return col_frag(t, at, kt); }
     static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
         *reinterpret_cast<float4 *>(t + quad(row, col)) = make_float4(a, b, c, d);
     }
@@ -173,14 +192,20 @@ __device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8
     hi = Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
     lo = hi;
 }
+// The pair as it was packed: the compiler would convert each half again to take it from its value.
+__device__ __forceinline__ uint32_t seen(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
+}
 // w c as three bf16 operands whose sum has all 24 bits (fp32: as it is)
 __device__ __forceinline__ void scaled_frags(const Frag8<true> &c, const float (&w)[8], Frag8<true> (&f)[3]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float x = bf_lo(c.p[i]) * w[2 * i], y = bf_hi(c.p[i]) * w[2 * i + 1];
-        f[0].p[i] = pack_bf16(x, y);
+        f[0].p[i] = seen(pack_bf16(x, y));
         const float x1 = x - bf_lo(f[0].p[i]), y1 = y - bf_hi(f[0].p[i]);
-        split_bf16(x1, y1, f[1].p[i], f[2].p[i]);
+        f[1].p[i] = seen(pack_bf16(x1, y1));
+        f[2].p[i] = pack_bf16(x1 - bf_lo(f[1].p[i]), y1 - bf_hi(f[1].p[i]));
     }
 }
 __device__ __forceinline__ void scaled_frags(const Frag8<false> &c, const float (&w)[8], Frag8<false> (&f)[1]) {
@@ -266,7 +291,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        st[kt][ct][i] = s0[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc];
+                        st[kt][ct][i] = s0[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc];
         }
     }
     mfma_fence_state(st);  // the loads end here: a wait for them inside the loop would hold up the rows under way
@@ -283,7 +308,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        carry += st[kt][ct][i] * se[(int64_t)(16 * kt + 4 * g + i) * A.sr +
+                        carry += st[kt][ct][i] * se[(int64_t)(RK::state_row(kt, g) + i) * A.sr +
                                                     (int64_t)(col0 + 16 * ct + li) * A.sc];
         }
 #pragma unroll
@@ -311,6 +336,9 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         }
     }
     float btot = 0.f;
+    const int lane0 = lane, rowk0 = RK::row_at(lane), tilek0 = RK::tile_at(lane), rowv0 = RV::row_at(lane);
+    const int rowp0 = RP::row_at(lane);
+    const int colv0 = BF ? RV::col_at(lane) ^ (wave * CT << 5) : RV::col_at(lane) + 64 * wave * CT;
     auto chunk_at = [&](int i, int64_t &tc, int &n) __attribute__((always_inline)) {  // its first token and how many
         tc = sg.t0 + (int64_t)(REV ? nch - 1 - i : i) * C;
         n = (int)(sg.t1 - tc < C ? sg.t1 - tc : C);
@@ -343,18 +371,25 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         const float l0 = lane < 32 ? lane_value(d.lo, 15) : lane_value(d.lo, 47);
         d.hi += lane & 16 ? h0 : 0.f;
         d.lo += lane & 16 ? l0 : 0.f;
-        const float hc = lane < 32 ? lane_value(d.hi, 31) : lane_value(d.hi, 63);
-        const float lc2 = lane < 32 ? lane_value(d.lo, 31) : lane_value(d.lo, 63);
-        const float ein = __builtin_amdgcn_exp2f(d.hi + d.lo);
-        const float eout = __builtin_amdgcn_exp2f((hc - d.hi) + (lc2 - d.lo));
-        s_wup2[at][t] = live ? (REV ? ein : eout) * A.s_up : 0.f;
+        const float h31 = lane_value(d.hi, 31), l31 = lane_value(d.lo, 31);
+        const float h63 = lane_value(d.hi, 63), l63 = lane_value(d.lo, 63);
+        // Of a pair of chunks that decays mildly the first leaves the state undecayed (what it adds is scaled up
+        // instead, by less than 2^24) and the second decays it for both.
+        const bool both = first + 2 * wave + 1 < nch && h31 + l31 > -24.f;
+        const float hc = lane < 32 ? h31 : h63, lc2 = lane < 32 ? l31 : l63;
+        const float uh = both && lane < 32 ? h31 : 0.f, ul = both && lane < 32 ? l31 : 0.f;    // added to the state
+        const float rh = both && lane >= 32 ? h31 : 0.f, rl = both && lane >= 32 ? l31 : 0.f;  // read from it
+        const float dh = REV ? d.hi : hc - d.hi, dl = REV ? d.lo : lc2 - d.lo;  // from a token to the state behind it
+        const float eh = REV ? hc - d.hi : d.hi, el = REV ? lc2 - d.lo : d.lo;  // from the state before it to a token
+        const float wup = __builtin_amdgcn_exp2f((dh - uh) + (dl - ul)), win = __builtin_amdgcn_exp2f((eh + rh) + (el + rl));
+        s_wup2[at][t] = live ? wup * A.s_up : 0.f;
         if constexpr (!INC) {
             s_bh2[at][t] = d.hi;
             s_bl2[at][t] = d.lo;
             s_f2[at][t] = live ? f * A.s_intra : 0.f;
-            s_win2[at][t] = live ? (REV ? eout : ein) * A.s_inter : 0.f;
+            s_win2[at][t] = live ? win * A.s_inter : 0.f;
         }
-        if (t == 0) s_ec2[at] = __builtin_amdgcn_exp2f(hc + lc2);
+        if (t == 0) s_ec2[at] = __builtin_amdgcn_exp2f(((hc - uh) + rh) + ((lc2 - ul) + rl));
         if constexpr (INC) btot += hc + lc2;  // lanes 0 and 32: this wavefront's chunks
     };
     Stage<BF, KD, C, NT> ra, rb;
@@ -392,15 +427,14 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         const int buf = cc & (DB - 1), rbuf = cc & (NB - 1);
         const float *s_wup = s_wup2[buf], *s_win = s_win2[INC ? 0 : buf], *s_bh = s_bh2[INC ? 0 : buf],
                     *s_bl = s_bl2[INC ? 0 : buf], *s_f = s_f2[INC ? 0 : buf];
-        // The lanes' addresses are made anew each chunk, from the lane's number that the compiler cannot see through:
-        // kept over the loop, the some forty of them would take the registers the products need. The rows' buffer
-        // enters them too (its size is above all their bits).
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63, g = lane >> 4, li = lane & 15;
-        const int rowk = RK::row_at(lane) + rbuf * SZ_K, colk = RK::col_at(lane) + rbuf * SZ_K;
-        const int rowv = RV::row_at(lane) + rbuf * SZ_V, rowp = RP::row_at(lane);
-        const int colv = (BF ? RV::col_at(lane) ^ (wave * CT << 5) : RV::col_at(lane) + 64 * wave * CT) + rbuf * SZ_V;
+        // The rows' buffer enters the lanes' addresses (its size is above all their bits). What is derived from them is
+        // made anew each chunk, from values that the compiler cannot see through: kept over the loop, the some forty
+        // addresses would take the registers the products need.
+        int rowk = rowk0 + rbuf * SZ_K, tilek = tilek0 + rbuf * SZ_K, rowv = rowv0 + rbuf * SZ_V;
+        int colv = colv0 + rbuf * SZ_V, rowp = rowp0, lane = lane0;
+        asm volatile("" : "+v"(rowk), "+v"(tilek), "+v"(rowv), "+v"(colv), "+v"(rowp), "+v"(lane));
+        const int g = lane >> 4, li = lane & 15;
+        (void)rowk; (void)rowv; (void)rowp;
         const char *s_a = s_a2[0], *s_b = s_b2[0], *s_c = s_c2[0], *s_x = s_x2[0];
         (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
@@ -409,13 +443,13 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
             if (cc + DB < nch) gnext = take_decay(lane, cc + DB);
         }
         if constexpr (NB == 1) {
-            put_rows(tid, cc);
-            if (cc + 1 < nch) take_rows(tid, cc + 1);
+            put_rows(threadIdx.x, cc);
+            if (cc + 1 < nch) take_rows(threadIdx.x, cc + 1);
         }
         if (NB == 1 || buf == 0) __syncthreads();
         if (NB == 2 && cc + 1 < nch) {
-            put_rows(tid, cc + 1);
-            if (cc + 2 < nch) take_rows(tid, cc + 2);
+            put_rows(threadIdx.x, cc + 1);
+            if (cc + 2 < nch) take_rows(threadIdx.x, cc + 2);
         }
 
         // ---- weighted products D (a.b), tile by tile, transposed: lane holds sources 16ts+4g+i of token 16tt+l%16
@@ -571,17 +605,18 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
             }
         }
         // ---- the chunk's own products, and the state's update
-        const float ec = s_ec2[buf];
+        const float ec = lane_value(s_ec2[buf], 0);
+        if (ec != 1.f)
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) st[kt][ct] *= ec;
+                for (int ct = 0; ct < CT; ++ct) st[kt][ct] *= ec;
 #pragma unroll
         for (int s = 0; s < SC; ++s) {
             Frag8<BF> cw[CT][NPART];
             float w[8];
-            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + 4 * g);
-            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + 16 + 4 * g);
+            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + RV::token(0, g));
+            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(s_wup + 32 * s + RV::token(1, g));
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 const Frag8<BF> cf = RV::col_frag(s_c + 32 * s * RV::RB, colv, ct);
@@ -600,7 +635,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
             for (int k0 = 0; k0 < KT; k0 += KG) {
                 Frag8<BF> bf[KG];
 #pragma unroll
-                for (int j = 0; j < KG; ++j) bf[j] = RK::col_frag(s_b + 32 * s * RK::RB, colk, k0 + j);
+                for (int j = 0; j < KG; ++j) bf[j] = RK::tile_frag(s_b + 32 * s * RK::RB, tilek, k0 + j);
 #pragma unroll
                 for (int q = 0; q < NPART; ++q)
 #pragma unroll
@@ -650,7 +685,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    so[(int64_t)(16 * kt + 4 * g + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
+                    so[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
     }
     if constexpr (INC) {  // the segment's whole decay: the wavefronts' sums
         btot = lane_value(btot, 0) + lane_value(btot, 32);
