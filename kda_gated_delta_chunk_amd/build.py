@@ -15,8 +15,8 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libkda.so"
-SOURCES = ["kda_prefill.hip", "kda_decode.hip", "kda_backward.hip", "kda_api.hip", "kda_hd_bf16.hip",
-           "kda_hd_fp32.hip", "kda_hd.hip", "kda_hd_decode.hip", "kda_rotary.hip", "kda_norm.hip",
+SOURCES = ["kda_prefill.hip", "kda_decode.hip", "kda_backward.hip", "kda_api.hip", "kda_hd_fwd.hip",
+           "kda_hd_grad_bf16.hip", "kda_hd_grad_fp32.hip", "kda_hd.hip", "kda_hd_decode.hip", "kda_rotary.hip", "kda_norm.hip",
            "kda_layer_api.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -13,7 +13,6 @@ namespace kda {
 namespace hd {
 namespace {
 
-constexpr int64_t kResident = 512;  // workgroups of the chunk kernel that run at a time: two per CU
 constexpr int64_t kLeastSegment = 256;
 
 struct Plan {
@@ -21,36 +20,34 @@ struct Plan {
     int32_t nseg;       // segments per row (not packed)
     int64_t slots;      // workgroups' slots: an upper bound when packed
     bool several;       // some sequence may have more than one segment
-    int vk, vv;         // column tile over K and over V columns
 };
-
-int tile_of(int cols, bool bf16) { return bf16 || cols < 64 ? cols : 64; }
-
-// The increment passes have no weighted products to share, only the rows b: narrower tiles, more workgroups.
-int inc_tile_of(int cols) { return cols < 64 ? cols : 64; }
 
 int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
 
-// How long a call with n segments per row takes, in tokens of one workgroup: its rounds over the chip's resident
-// workgroups; with several segments also the increments' rounds (about a third of the work), two more launches and the
-// states' traffic.
-int64_t cost(int64_t rows, int64_t T, int64_t n) {
-    const int64_t seg = round64((T + n - 1) / n);
-    int64_t c = (rows * n + kResident - 1) / kResident * seg;
-    if (n > 1) c += (rows * (n - 1) + kResident - 1) / kResident * seg / 3 + 100 + rows * n / 3;
+// How long a call with n segments per row takes, in ns as measured at K = V = 128 in bf16: the main pass's rounds over
+// the workgroups that the chip holds (a token of the forward pass takes 110 ns, of the gradients 160; three quarters of
+// that where no two share a CU); with several segments also the increments' rounds (80 ns), the states' traffic (50 ns
+// per head and segment, twice for the gradients) and two more launches.
+int64_t cost(int64_t rows, int64_t inc_rows, int64_t heads, int64_t resident, int64_t T, int64_t n, bool bwd) {
+    const int64_t seg = round64((T + n - 1) / n), groups = rows * n;
+    int64_t c = (groups + resident - 1) / resident * seg * (bwd ? 160 : 110);
+    if (groups <= 256) c = c * 3 / 4;
+    if (n > 1) c += (inc_rows * (n - 1) + 1023) / 1024 * seg * 80 + heads * n * (bwd ? 100 : 50) + 12000;
     return c;
 }
 
-Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool packed, bool bf16) {
+Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool packed, bool bf16, bool bwd) {
     Plan p;
-    p.vk = tile_of(K, bf16);
-    p.vv = tile_of(V, bf16);
     const int64_t whole = round64(T > 0 ? T : 1);
     // workgroups of one segment per row (packed: one sequence may be nearly all of the batch)
-    const int64_t rows = (packed ? 1 : B) * H * (V / p.vv);
-    int64_t best = 1;
-    for (int64_t n = 2; n <= whole / kLeastSegment && rows * (n - 1) < 2 * kResident; ++n)
-        if (cost(rows, whole, n) < cost(rows, whole, best)) best = n;
+    const int vt = bwd ? grad_tile(K, V, bf16) : fwd_tile(V, bf16);
+    const int64_t heads = (packed ? 1 : B) * H, rows = heads * (bwd ? 2 * (K / vt) + V / vt : V / vt);
+    const int64_t inc_rows = heads * (V / inc_tile(V)) * (bwd ? 2 : 1), resident = vt == 128 || bwd ? 512 : 768;
+    int64_t best = 1, least = cost(rows, inc_rows, heads, resident, whole, 1, bwd);
+    for (int64_t n = 2; n <= whole / kLeastSegment && rows * (n - 1) < 4 * resident; ++n) {
+        const int64_t c = cost(rows, inc_rows, heads, resident, whole, n, bwd);
+        if (c < least) best = n, least = c;
+    }
     p.seg = round64((whole + best - 1) / best);
     p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
     p.slots = packed ? T / p.seg + N : B * p.nseg;
@@ -114,11 +111,18 @@ __global__ __launch_bounds__(1024) void kda_hd_table_kernel(const int32_t *__res
 }
 
 // ------------------------------------------------------------------ states over the segments
+struct CarryArgs {
+    float *seg;
+    const float *decay, *init;
+};
 // In place: what each segment adds becomes the state it starts from (rev: the state gradient it ends with). A thread
 // carries four adjacent state entries over the segments of its sequence.
-__global__ __launch_bounds__(256) void kda_hd_carry_kernel(float *__restrict__ seg, const float *__restrict__ decay,
-                                                           const float *__restrict__ init, const SeqSlots *__restrict__ seqs,
-                                                           int32_t nseg, int32_t H, int64_t kv4, int rev) {
+__global__ __launch_bounds__(256) void kda_hd_carry_kernel(const CarryArgs F, const CarryArgs R,
+                                                           const SeqSlots *__restrict__ seqs, int32_t nseg, int32_t H,
+                                                           int64_t kv4) {
+    const int rev = blockIdx.y;
+    float *seg = rev ? R.seg : F.seg;
+    const float *decay = rev ? R.decay : F.decay, *init = rev ? R.init : F.init;
     const int64_t runs = (kv4 + 255) / 256, nh = blockIdx.x / runs, n = nh / H;
     const int64_t e = (blockIdx.x - nh * runs) * 256 + threadIdx.x;
     if (e >= kv4) return;
@@ -141,46 +145,86 @@ __global__ __launch_bounds__(256) void kda_hd_carry_kernel(float *__restrict__ s
     }
 }
 
-hipError_t launch_carry(float *seg, const float *decay, const float *init, const SeqSlots *seqs, const Plan &p,
-                        const HdArgs &a, bool rev, hipStream_t st) {
+hipError_t launch_carry(const CarryArgs &f, const CarryArgs *r, const SeqSlots *seqs, const Plan &p, const HdArgs &a,
+                        hipStream_t st) {
     const int64_t kv4 = (int64_t)a.K * a.V / 4, nh = (int64_t)a.num_seqs * a.H;
-    // heads of all sequences times runs of 256 state entries: num_seqs * H < 2^28, K * V / 1024 <= 16
+    // heads of all sequences times runs of 256 state entries: num_seqs * H < 2^26, K * V / 1024 <= 16
     const int64_t x = (kv4 + 255) / 256;
     if (nh * x >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kda_hd_carry_kernel, dim3((uint32_t)(nh * x)), dim3(256), 0, st, seg, decay, init, seqs, p.nseg,
-                       a.H, kv4, (int)rev);
+    hipLaunchKernelGGL(kda_hd_carry_kernel, dim3((uint32_t)(nh * x), r ? 2 : 1), dim3(256), 0, st, f, r ? *r : f, seqs,
+                       p.nseg, a.H, kv4);
     return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ the gradients' last steps
-// dg[t][h] = sum of the column tiles' parts [tiles][H][ntok], for the tokens of the sequences.
+// dg_t = what passes the border behind t's segment + sum over the tokens from t to there of their parts (rows' sums
+// less columns' sums of the pairs, and the states' shares). A workgroup takes two heads of a segment, from its end in
+// steps of 512 tokens: a wavefront sums 64 of them, then the totals of the wavefronts behind it are added.
 template <bool BF>
-__global__ __launch_bounds__(256) void kda_hd_dg_kernel(const float *__restrict__ part, int tiles, int32_t H,
-                                                        int64_t ntok, const int64_t *__restrict__ covered,
-                                                        void *__restrict__ dg) {
-    __shared__ float s[64][65];
-    const int64_t t0 = (int64_t)blockIdx.x * 64;
-    const int h0 = blockIdx.y * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t lo = covered ? covered[0] : 0, hi = covered ? covered[1] : ntok;
-    for (int i = wave; i < 64; i += 4) {
-        float x = 0.f;
-        if (h0 + i < H && t0 + lane >= lo && t0 + lane < hi)
-            for (int w = 0; w < tiles; ++w) x += part[((int64_t)w * H + h0 + i) * ntok + t0 + lane];
-        s[i][lane] = x;
+__global__ __launch_bounds__(1024) void kda_hd_dg_kernel(const CoreArgs A, const float *__restrict__ part_q, int tiles_q,
+                                                         int K, const float *__restrict__ dS, const float *__restrict__ s_end,
+                                                         void *__restrict__ dg) {
+    __shared__ float s_total[2][2][8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hsub = wave >> 3, blk = wave & 7;
+    const int h = blockIdx.y * 2 + hsub;
+    const Segment sg = segment_of(A, blockIdx.x);
+    if (sg.seq < 0 || sg.t1 <= sg.t0) return;
+    const bool live = h < A.H;
+    double behind = 0.0;
+    if (live) {
+        for (int w = 0; w < A.tiles; ++w) behind += A.border[((int64_t)w * A.slots + blockIdx.x) * A.H + h];
+        if (sg.j == sg.nseg - 1 && dS) {
+            const int64_t kv4 = (int64_t)K * A.VD / 4, at = ((int64_t)sg.seq * A.H + h) * kv4;
+            const f32x4 *x = reinterpret_cast<const f32x4 *>(dS) + at, *y = reinterpret_cast<const f32x4 *>(s_end) + at;
+            float dot = 0.f;
+            for (int64_t i = lane; i < kv4; i += 64) {
+                const f32x4 z = x[i] * y[i];
+                dot += (z.x + z.y) + (z.z + z.w);
+            }
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+            behind += dot;
+        }
     }
-    __syncthreads();
-    for (int i = wave; i < 64; i += 4) {
-        const int64_t t = t0 + i;
-        if (t >= lo && t < hi && h0 + lane < H)
-            IO<BF>::st(reinterpret_cast<typename IO<BF>::T *>(dg), t * H + h0 + lane, s[lane][i]);
+    const int64_t plane = (int64_t)A.H * A.ntok, steps = (sg.t1 - sg.t0 + 511) / 512;
+    auto take = [&](int64_t b) {
+        const int64_t t = sg.t0 + b * 512 + blk * 64 + lane, at = (int64_t)h * A.ntok + t;
+        float x = 0.f;
+        if (b >= 0 && live && t < sg.t1) {
+            for (int w = 0; w < A.tiles; ++w) x += A.part[w * plane + at];
+            for (int w = 0; w < tiles_q; ++w) x += part_q[w * plane + at];
+        }
+        return x;
+    };
+    float next = take(steps - 1);
+    for (int64_t b = steps - 1; b >= 0; --b) {
+        float x = next;
+        next = take(b - 1);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const float y = __shfl_down(x, d);
+            if (lane + d < 64) x += y;
+        }
+        float(*const total)[8] = s_total[b & 1];
+        if (lane == 0) total[hsub][blk] = x;
+        __syncthreads();
+        double later = behind;
+        for (int w = 7; w > blk; --w) later += total[hsub][w];
+        const int64_t t = sg.t0 + b * 512 + blk * 64 + lane;
+        if (live && t < sg.t1)
+            IO<BF>::st(reinterpret_cast<typename IO<BF>::T *>(dg), t * A.H + h, (float)(later + x));
+        for (int w = 0; w < 8; ++w) behind += total[hsub][w];
     }
 }
 
 // out[t][hk][d] = sum over the group's heads of in[t][h][d] (fp32), for the tokens of the sequences; four d a thread.
 template <bool BF>
-__global__ __launch_bounds__(256) void kda_hd_group_kernel(const float *__restrict__ in, void *__restrict__ out,
+__global__ __launch_bounds__(256) void kda_hd_group_kernel(const float *__restrict__ in0, void *__restrict__ out0,
+                                                           const float *__restrict__ in1, void *__restrict__ out1,
                                                            int64_t ntok, int64_t per_token, int64_t D4, int group,
                                                            const int64_t *__restrict__ covered) {
+    const float *in = blockIdx.y ? in1 : in0;
+    void *out = blockIdx.y ? out1 : out0;
     const int64_t lo = covered ? covered[0] : 0, hi = covered ? covered[1] : ntok;
     const int64_t n = ntok * per_token;  // per_token: Hk * D / 4
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
@@ -198,10 +242,10 @@ __global__ __launch_bounds__(256) void kda_hd_group_kernel(const float *__restri
 
 // ------------------------------------------------------------------ workspace
 struct Layout {
-    size_t table, seqs, covered, seg, decay, dseg, ddecay, s_end, share, dg_part, dq, dk, total;
+    size_t table, seqs, covered, seg, decay, dseg, ddecay, s_end, part_q, part_v, border, dq, dk, total;
 };
 Layout layout(const Plan &p, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t N, bool packed,
-              bool bwd) {
+              bool bf16, bool bwd) {
     Layout l{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -225,8 +269,10 @@ Layout layout(const Plan &p, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int
     }
     if (bwd) {
         l.s_end = take((size_t)N * states);
-        l.share = take((size_t)(K / p.vk) * ntok * H * sizeof(float));
-        l.dg_part = take((size_t)(V / p.vv) * ntok * H * sizeof(float));
+        const int gt = grad_tile(K, V, bf16);
+        l.part_q = take((size_t)(K / gt) * ntok * H * sizeof(float));
+        l.part_v = take((size_t)(V / gt) * ntok * H * sizeof(float));
+        l.border = take((size_t)(V / gt) * p.slots * H * sizeof(float));
         if (Hk != H) {
             l.dq = take((size_t)ntok * H * K * sizeof(float));
             l.dk = take((size_t)ntok * H * K * sizeof(float));
@@ -234,10 +280,6 @@ Layout layout(const Plan &p, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int
     }
     l.total = at ? at : 256;
     return l;
-}
-
-hipError_t core(const HdArgs &a, const CoreArgs &c, int kd, int vt, Kind k, hipStream_t st) {
-    return a.io_bf16 ? core_bf16(c, kd, vt, k, st) : core_fp32(c, kd, vt, k, st);
 }
 
 #define KDA_TRY(x)                            \
@@ -258,8 +300,8 @@ struct Call {
 Call prepare(const HdArgs &a, bool bwd) {
     Call c;
     const bool packed = a.cu_seqlens != nullptr;
-    c.p = plan(a.B, a.T, a.H, a.K, a.V, a.num_seqs, packed, a.io_bf16);
-    c.l = layout(c.p, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd);
+    c.p = plan(a.B, a.T, a.H, a.K, a.V, a.num_seqs, packed, a.io_bf16, bwd);
+    c.l = layout(c.p, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, a.io_bf16, bwd);
     c.ws = reinterpret_cast<char *>(a.workspace);
     c.table = packed ? reinterpret_cast<const Segment *>(c.ws + c.l.table) : nullptr;
     c.seqs = packed ? reinterpret_cast<const SeqSlots *>(c.ws + c.l.seqs) : nullptr;
@@ -289,21 +331,32 @@ CoreArgs base(const HdArgs &a, const Call &c) {
     x.sr = a.V;
     x.sc = 1;
     x.VD = a.V;
-    x.tiles = a.V / c.p.vv;
     return x;
 }
-// the states that the segments start from
-hipError_t forward_states(const HdArgs &a, const Call &c, hipStream_t st) {
-    if (!c.p.several) return hipSuccess;
+// What the segments add to the states (to their gradients).
+CoreArgs increments(const HdArgs &a, const Call &c, bool rev) {
     CoreArgs x = base(a, c);
-    x.b = a.k;
+    x.tiles = a.V / inc_tile(a.V);
+    x.b = rev ? a.q : a.k;
     x.gb = a.H / a.Hk;
-    x.c = a.v;
-    x.s_inc = reinterpret_cast<float *>(c.ws + c.l.seg);
-    x.seg_decay = reinterpret_cast<float *>(c.ws + c.l.decay);
-    x.tiles = a.V / inc_tile_of(a.V);
-    KDA_TRY(core(a, x, a.K, inc_tile_of(a.V), Kind::fwd_inc, st));
-    return launch_carry(x.s_inc, x.seg_decay, a.S0, c.seqs, c.p, a, false, st);
+    x.c = rev ? a.dout : a.v;
+    x.s_up = rev ? a.scale : 1.f;
+    x.s_inc = reinterpret_cast<float *>(c.ws + (rev ? c.l.dseg : c.l.seg));
+    x.seg_decay = reinterpret_cast<float *>(c.ws + (rev ? c.l.ddecay : c.l.decay));
+    return x;
+}
+hipError_t segment_states(const HdArgs &a, const Call &c, bool bwd, hipStream_t st) {
+    if (!c.p.several) return hipSuccess;
+    const CoreArgs f = increments(a, c, false);
+    const CarryArgs cf{f.s_inc, f.seg_decay, a.S0};
+    if (!bwd) {
+        KDA_TRY(inc_pass(a.io_bf16, f, nullptr, a.K, inc_tile(a.V), st));
+        return launch_carry(cf, nullptr, c.seqs, c.p, a, st);
+    }
+    const CoreArgs r = increments(a, c, true);
+    const CarryArgs cr{r.s_inc, r.seg_decay, a.dS_final};
+    KDA_TRY(inc_pass(a.io_bf16, f, &r, a.K, inc_tile(a.V), st));
+    return launch_carry(cf, &cr, c.seqs, c.p, a, st);
 }
 
 }  // namespace
@@ -311,21 +364,23 @@ hipError_t forward_states(const HdArgs &a, const Call &c, hipStream_t st) {
 
 size_t hd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool io_bf16) {
-    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16);
-    return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, false).total;
+    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16, false);
+    return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, io_bf16, false).total;
 }
 size_t hd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool io_bf16) {
-    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16);
-    return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, true).total;
+    const hd::Plan p = hd::plan(B, T, H, K, V, num_seqs, packed, io_bf16, true);
+    return hd::layout(p, B * T, H, Hk, K, V, num_seqs, packed, io_bf16, true).total;
 }
 
 hipError_t launch_hd_fwd(const HdArgs &a, hipStream_t st) {
     using namespace hd;
     const Call c = prepare(a, false);
     KDA_TRY(make_table(a, c, st));
-    KDA_TRY(forward_states(a, c, st));
+    KDA_TRY(segment_states(a, c, false, st));
     CoreArgs x = base(a, c);
+    const int vt = fwd_tile(a.V, a.io_bf16);
+    x.tiles = a.V / vt;
     x.a = a.q;
     x.b = a.k;
     x.ga = x.gb = a.H / a.Hk;
@@ -335,113 +390,94 @@ hipError_t launch_hd_fwd(const HdArgs &a, hipStream_t st) {
     x.s_seg = reinterpret_cast<const float *>(c.ws + c.l.seg);
     x.s_out = a.S_final;
     x.s_intra = x.s_inter = a.scale;
-    return core(a, x, a.K, c.p.vv, Kind::fwd, st);
+    return fwd_pass(a.io_bf16, x, a.K, vt, st);
 }
 
 hipError_t launch_hd_bwd(const HdArgs &a, hipStream_t st) {
     using namespace hd;
     const Call c = prepare(a, true);
-    const int group = a.H / a.Hk;
+    const int group = a.H / a.Hk, gt = grad_tile(a.K, a.V, a.io_bf16);
     const int64_t ntok = a.B * a.T;
-    KDA_TRY(make_table(a, c, st));
-    KDA_TRY(forward_states(a, c, st));
-    float *dseg = reinterpret_cast<float *>(c.ws + c.l.dseg), *s_end = reinterpret_cast<float *>(c.ws + c.l.s_end);
-    if (c.p.several) {  // the state gradients that the segments end with
-        CoreArgs x = base(a, c);
-        x.b = a.q;
-        x.gb = group;
-        x.c = a.dout;
-        x.s_up = a.scale;
-        x.s_inc = dseg;
-        x.seg_decay = reinterpret_cast<float *>(c.ws + c.l.ddecay);
-        x.tiles = a.V / inc_tile_of(a.V);
-        KDA_TRY(core(a, x, a.K, inc_tile_of(a.V), Kind::rev_inc, st));
-        KDA_TRY(launch_carry(dseg, x.seg_decay, a.dS_final, c.seqs, c.p, a, true, st));
-    }
     const bool grouped = group > 1;
+    KDA_TRY(make_table(a, c, st));
+    KDA_TRY(segment_states(a, c, true, st));
+    const float *seg = reinterpret_cast<const float *>(c.ws + c.l.seg);
+    const float *dseg = reinterpret_cast<const float *>(c.ws + c.l.dseg);
+    float *s_end = reinterpret_cast<float *>(c.ws + c.l.s_end);
     void *dq = grouped ? c.ws + c.l.dq : a.dq, *dk = grouped ? c.ws + c.l.dk : a.dk;
-    {  // dq: forward in time, rows do against v, summing k; the state transposed
-        CoreArgs x = base(a, c);
-        x.a = a.dout;
-        x.b = a.v;
-        x.c = a.k;
-        x.gc = group;
-        x.VD = a.K;
-        x.tiles = a.K / c.p.vk;
-        x.sr = 1;
-        x.sc = a.V;
-        x.y = dq;
-        x.y_fp32 = grouped;
-        x.s_init = a.S0;
-        x.s_seg = reinterpret_cast<const float *>(c.ws + c.l.seg);
-        x.s_intra = x.s_inter = a.scale;
-        x.x = a.q;
-        x.gx = group;
-        x.share = reinterpret_cast<float *>(c.ws + c.l.share);
-        x.s_out = a.dg && a.dS_final ? s_end : nullptr;
-        KDA_TRY(core(a, x, a.V, c.p.vk, a.dg ? Kind::fwd_dg : Kind::fwd, st));
-    }
-    {  // dv: backward in time, rows k against q, summing do
-        CoreArgs x = base(a, c);
-        x.a = a.k;
-        x.b = a.q;
-        x.ga = x.gb = group;
-        x.c = a.dout;
-        x.y = a.dv;
-        x.s_init = a.dS_final;
-        x.s_seg = dseg;
-        x.s_out = a.dS0;
-        x.s_intra = x.s_up = a.scale;
-        x.x = a.v;
-        x.share = reinterpret_cast<float *>(c.ws + c.l.share);
-        x.share_tiles = a.K / c.p.vk;
-        x.dg_part = reinterpret_cast<float *>(c.ws + c.l.dg_part);
-        x.s_end = s_end;
-        x.s_seg_fwd = reinterpret_cast<const float *>(c.ws + c.l.seg);
-        KDA_TRY(core(a, x, a.K, c.p.vv, a.dg ? Kind::rev_dg : Kind::rev, st));
-    }
-    {  // dk: backward in time, rows v against do, summing q; the state gradient transposed
-        CoreArgs x = base(a, c);
-        x.a = a.v;
-        x.b = a.dout;
-        x.c = a.q;
-        x.gc = group;
-        x.VD = a.K;
-        x.tiles = a.K / c.p.vk;
-        x.sr = 1;
-        x.sc = a.V;
-        x.y = dk;
-        x.y_fp32 = grouped;
-        x.s_init = a.dS_final;
-        x.s_seg = dseg;
-        x.s_intra = x.s_up = a.scale;
-        KDA_TRY(core(a, x, a.V, c.p.vk, Kind::rev, st));
-    }
+    GradArgs g;
+    // dv: backward in time, rows k against q, summing do
+    g.dv = base(a, c);
+    g.dv.tiles = a.V / gt;
+    g.dv.a = a.k;
+    g.dv.b = a.q;
+    g.dv.ga = g.dv.gb = group;
+    g.dv.c = a.dout;
+    g.dv.y = a.dv;
+    g.dv.s_init = a.dS_final;
+    g.dv.s_seg = dseg;
+    g.dv.s_out = a.dS0;
+    g.dv.s_intra = g.dv.s_up = a.scale;
+    g.dv.x = a.v;
+    g.dv.part = reinterpret_cast<float *>(c.ws + c.l.part_v);
+    g.dv.border = reinterpret_cast<float *>(c.ws + c.l.border);
+    g.dv.s_seg_fwd = seg;
+    // dk: backward in time, rows v against do, summing q; the state gradient transposed
+    g.dk = base(a, c);
+    g.dk.a = a.v;
+    g.dk.b = a.dout;
+    g.dk.c = a.q;
+    g.dk.gc = group;
+    g.dk.VD = a.K;
+    g.dk.tiles = a.K / gt;
+    g.dk.sr = 1;
+    g.dk.sc = a.V;
+    g.dk.y = dk;
+    g.dk.s_init = a.dS_final;
+    g.dk.s_seg = dseg;
+    g.dk.s_intra = g.dk.s_up = a.scale;
+    // dq: forward in time, rows do against v, summing k; the state transposed
+    g.dq = base(a, c);
+    g.dq.a = a.dout;
+    g.dq.b = a.v;
+    g.dq.c = a.k;
+    g.dq.gc = group;
+    g.dq.VD = a.K;
+    g.dq.tiles = a.K / gt;
+    g.dq.sr = 1;
+    g.dq.sc = a.V;
+    g.dq.y = dq;
+    g.dq.s_init = a.S0;
+    g.dq.s_seg = seg;
+    g.dq.s_out = a.dg && a.dS_final ? s_end : nullptr;
+    g.dq.s_intra = g.dq.s_inter = a.scale;
+    g.dq.x = a.q;
+    g.dq.gx = group;
+    g.dq.part = reinterpret_cast<float *>(c.ws + c.l.part_q);
+    KDA_TRY(a.io_bf16 ? grad_pass_bf16(g, a.K, a.V, a.dg != nullptr, grouped, st)
+                      : grad_pass_fp32(g, a.K, a.V, a.dg != nullptr, st));
     if (ntok == 0) return hipSuccess;
     if (a.dg) {
-        const dim3 grid((uint32_t)((ntok + 63) / 64), (uint32_t)((a.H + 63) / 64));
-        const float *part = reinterpret_cast<const float *>(c.ws + c.l.dg_part);
-        const int tiles = a.V / c.p.vv;
+        const dim3 grid((uint32_t)c.p.slots, (uint32_t)((a.H + 1) / 2));
         if (a.io_bf16)
-            hipLaunchKernelGGL(kda_hd_dg_kernel<true>, grid, dim3(256), 0, st, part, tiles, a.H, ntok, c.covered, a.dg);
+            hipLaunchKernelGGL(kda_hd_dg_kernel<true>, grid, dim3(1024), 0, st, g.dv, g.dq.part, g.dq.tiles, a.K,
+                               a.dS_final, s_end, a.dg);
         else
-            hipLaunchKernelGGL(kda_hd_dg_kernel<false>, grid, dim3(256), 0, st, part, tiles, a.H, ntok, c.covered, a.dg);
+            hipLaunchKernelGGL(kda_hd_dg_kernel<false>, grid, dim3(1024), 0, st, g.dv, g.dq.part, g.dq.tiles, a.K,
+                               a.dS_final, s_end, a.dg);
         KDA_TRY(hipGetLastError());
     }
     if (grouped) {
         const int64_t per = (int64_t)a.Hk * a.K / 4, n = ntok * per;
-        const uint32_t wgs = (uint32_t)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
-        for (int i = 0; i < 2; ++i) {
-            const float *in = reinterpret_cast<const float *>(i ? dk : dq);
-            void *out = i ? a.dk : a.dq;
-            if (a.io_bf16)
-                hipLaunchKernelGGL(kda_hd_group_kernel<true>, dim3(wgs), dim3(256), 0, st, in, out, ntok, per,
-                                   (int64_t)a.K / 4, group, c.covered);
-            else
-                hipLaunchKernelGGL(kda_hd_group_kernel<false>, dim3(wgs), dim3(256), 0, st, in, out, ntok, per,
-                                   (int64_t)a.K / 4, group, c.covered);
-            KDA_TRY(hipGetLastError());
-        }
+        const dim3 grid((uint32_t)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192), 2);
+        const float *iq = reinterpret_cast<const float *>(dq), *ik = reinterpret_cast<const float *>(dk);
+        if (a.io_bf16)
+            hipLaunchKernelGGL(kda_hd_group_kernel<true>, grid, dim3(256), 0, st, iq, a.dq, ik, a.dk, ntok, per,
+                               (int64_t)a.K / 4, group, c.covered);
+        else
+            hipLaunchKernelGGL(kda_hd_group_kernel<false>, grid, dim3(256), 0, st, iq, a.dq, ik, a.dk, ntok, per,
+                               (int64_t)a.K / 4, group, c.covered);
+        KDA_TRY(hipGetLastError());
     }
     return hipSuccess;
 }

@@ -17,14 +17,11 @@ struct Segment {
     int64_t t0, t1;  // tokens of the flattened [B * T]
 };
 
-enum class Kind { fwd, rev, fwd_inc, rev_inc, fwd_dg, rev_dg };
-
 struct CoreArgs {
     const void *a, *b, *c;      // rows [B*T, H / g?, KD | KD | VD]
     int32_t ga, gb, gc;         // heads that share a row of a, b, c
     int32_t H, VD, tiles;       // heads; columns of c and y; tiles of VT columns
     void *y;                    // [B*T, H, VD]
-    bool y_fp32;                // y in fp32 whatever the I/O type
     bool g_head;
     const void *g;              // [B*T, H] I/O type, or [H] fp32 (g_head)
     const float *s_init;        // state before the first segment (REV: after the last), or null
@@ -39,11 +36,13 @@ struct CoreArgs {
     float s_intra, s_inter, s_up;
     // the log-decays' gradient
     const void *x;              // rows [B*T, H / gx, VD] that y is multiplied with
-    int32_t gx, share_tiles;
-    float *share;               // [tiles][H][B*T]: x.y of the state's part, from the pass over dq
-    float *dg_part;             // [tiles][H][B*T]
-    const float *s_end;         // the sequences' last states (read where s_init is not null)
+    int32_t gx;
+    float *part;                // [tiles][H][B*T]: a token's part, from these columns
+    float *border;              // [tiles][slots][H]: <state gradient, state> behind a segment, from these columns
     const float *s_seg_fwd;     // the forward states the segments start from
+};
+struct GradArgs {
+    CoreArgs dv, dk, dq;
 };
 
 #ifdef __HIPCC__
@@ -61,8 +60,17 @@ __device__ __forceinline__ Segment segment_of(const CoreArgs &A, int64_t slot) {
 }
 #endif
 
-hipError_t core_bf16(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st);
-hipError_t core_fp32(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st);
+// Columns of a tile: of the forward pass and the gradients (whose three workgroups have one size), of the increments
+// (no weighted products to share, only the rows b: narrower tiles, more workgroups).
+constexpr int fwd_tile(int V, bool bf16) { return bf16 || V < 64 ? V : 64; }
+constexpr int grad_tile(int K, int V, bool bf16) { return fwd_tile(K < V ? K : V, bf16); }
+constexpr int inc_tile(int V) { return V < 64 ? V : 64; }
+
+// The passes. inc_pass: the increments of the states, and with r those of their gradients.
+hipError_t fwd_pass(bool bf16, const CoreArgs &a, int K, int vt, hipStream_t st);
+hipError_t inc_pass(bool bf16, const CoreArgs &f, const CoreArgs *r, int K, int vt, hipStream_t st);
+hipError_t grad_pass_bf16(const GradArgs &g, int K, int V, bool dg, bool y_fp32, hipStream_t st);
+hipError_t grad_pass_fp32(const GradArgs &g, int K, int V, bool dg, hipStream_t st);
 
 }  // namespace hd
 }  // namespace kda

@@ -230,39 +230,48 @@ __device__ __forceinline__ void mfma_fence_state(f32x4 (&x)[M][N]) {
     }
 }
 
+// Where a pass keeps what in LDS. bf16 holds rows twice, the next chunk's arrive while this one's are read (fp32's would
+// leave one workgroup per CU).
+template <bool BF, int KD, int VT, int NW, bool INC, bool DG>
+struct Lds {
+    static constexpr int C = kChunk, NB = BF ? 2 : 1, DB = 2 * NW;  // DB: chunks whose decays are made at a time
+    static constexpr bool PLO = BF && DG;
+    static constexpr int K = Rows<BF, KD>::bytes(C), V = Rows<BF, VT>::bytes(C), P = Rows<BF, C>::bytes(C);
+    static constexpr int b = 0, c = b + NB * K, a = c + NB * V, x = a + (INC ? 0 : NB * K), p = x + (DG ? NB * V : 0);
+    static constexpr int pl = p + (INC ? 0 : P), wup = pl + (PLO ? P : 0), win = wup + DB * C * 4;
+    static constexpr int bh = win + (INC ? 0 : DB * C * 4), bl = bh + (INC ? 0 : DB * C * 4);
+    static constexpr int f = bl + (INC ? 0 : DB * C * 4), ec = f + (INC ? 0 : DB * C * 4), u = ec + DB * 4;
+    static constexpr int red = u + (DG ? NW * C * 4 : 0), bytes = red + NW * 4;
+};
+
+// One (segment, head), column tile vt; NW * 64 threads, Lds::bytes of LDS.
 template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG, bool YF>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(const CoreArgs A) {
+__device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int vt, char *smem) {
+    using L = Lds<BF, KD, VT, NW, INC, DG>;
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
-    constexpr int DB = 2 * NW;                            // chunks whose decays are made at a time
+    constexpr int DB = L::DB, NB = L::NB;
     constexpr int NPART = BF ? 3 : 1;
-    constexpr bool PLO = BF && DG, SLO = BF && DG;
+    constexpr bool PLO = L::PLO, SLO = BF && DG;
     static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
     using E = typename IO<BF>::T;
     using RK = Rows<BF, KD>;
     using RV = Rows<BF, VT>;
     using RP = Rows<BF, C>;
-    constexpr int SZ_K = RK::bytes(C), SZ_V = RV::bytes(C), SZ_P = RP::bytes(C);
-    // bf16: rows twice, the next chunk's arrive while this one's are read (fp32's would leave one workgroup per CU)
-    constexpr int NB = BF ? 2 : 1;
-    __shared__ __align__(16) char s_b2[NB][SZ_K], s_c2[NB][SZ_V];
-    __shared__ __align__(16) char s_a2[NB][INC ? 16 : SZ_K], s_p[INC ? 16 : SZ_P], s_pl[INC || !PLO ? 16 : SZ_P];
-    __shared__ __align__(16) char s_x2[NB][DG ? SZ_V : 16];
-    __shared__ __align__(16) float s_wup2[DB][C], s_win2[INC ? 1 : DB][C], s_bh2[INC ? 1 : DB][C], s_bl2[INC ? 1 : DB][C],
-        s_f2[INC ? 1 : DB][C];
-    __shared__ float s_ec2[DB];
-    __shared__ float s_u[DG ? NW : 1][C], s_red[NW];
-    (void)s_pl; (void)s_x2; (void)s_u; (void)s_red;
+    constexpr int SZ_K = L::K, SZ_V = L::V, SZ_P = L::P;
+    char *const s_a = smem + L::a, *const s_b = smem + L::b, *const s_c = smem + L::c, *const s_x = smem + L::x;
+    char *const s_p = smem + L::p, *const s_pl = smem + L::pl;
+    float(*const s_wup2)[C] = reinterpret_cast<float(*)[C]>(smem + L::wup);
+    float(*const s_win2)[C] = reinterpret_cast<float(*)[C]>(smem + L::win);
+    float(*const s_bh2)[C] = reinterpret_cast<float(*)[C]>(smem + L::bh);
+    float(*const s_bl2)[C] = reinterpret_cast<float(*)[C]>(smem + L::bl);
+    float(*const s_f2)[C] = reinterpret_cast<float(*)[C]>(smem + L::f);
+    float(*const s_u)[C] = reinterpret_cast<float(*)[C]>(smem + L::u);
+    float *const s_ec2 = reinterpret_cast<float *>(smem + L::ec), *const s_red = reinterpret_cast<float *>(smem + L::red);
+    (void)s_a; (void)s_x; (void)s_p; (void)s_pl; (void)s_u; (void)s_red;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4,
               li = lane & 15;
-    // tiles of one (segment, head) sit 8 workgroups apart: the same XCD, whose L2 then holds their common rows
-    const int64_t items = A.slots * A.H;
-    const int64_t blk = blockIdx.x, grp = blk / (8 * A.tiles);
-    const int in = (int)(blk - grp * 8 * A.tiles);
-    const int64_t item = grp * 8 + (in & 7);
-    const int vt = in >> 3;
-    if (item >= items) return;
     const int64_t slot = item / A.H;
     const int h = (int)(item - slot * A.H);
     const Segment sg = segment_of(A, slot);
@@ -295,29 +304,30 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         }
     }
     mfma_fence_state(st);  // the loads end here: a wait for them inside the loop would hold up the rows under way
-    // ---- what the borders behind the segment pass on to its log-decays: <state gradient, state> at its end
-    float carry = 0.f;
+    // ---- what the border behind the segment passes on to its log-decays: <state gradient, state> there. (Behind the
+    // last one the state is not known yet: the last kernel adds its part.)
     if constexpr (DG && REV) {
-        const bool last = sg.j == sg.nseg - 1;
-        const float *se = last ? (A.s_init ? A.s_end + nh * sstate : nullptr)
-                               : A.s_seg_fwd + ((slot + 1) * A.H + h) * sstate;
-        if (se) {
+        float dot = 0.f;
+        if (sg.j < sg.nseg - 1) {
+            const float *se = A.s_seg_fwd + ((slot + 1) * A.H + h) * sstate;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        carry += st[kt][ct][i] * se[(int64_t)(RK::state_row(kt, g) + i) * A.sr +
-                                                    (int64_t)(col0 + 16 * ct + li) * A.sc];
+                        dot += st[kt][ct][i] * se[(int64_t)(RK::state_row(kt, g) + i) * A.sr +
+                                                  (int64_t)(col0 + 16 * ct + li) * A.sc];
         }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) carry += __shfl_xor(carry, d);
-        if (lane == 0) s_red[wave] = carry;
+        for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+        if (lane == 0) s_red[wave] = dot;
         __syncthreads();
-        carry = 0.f;
+        if (threadIdx.x == 0) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) carry += s_red[w];
+            for (int w = 1; w < NW; ++w) dot += s_red[w];
+            A.border[((int64_t)vt * A.slots + slot) * A.H + h] = dot;
+        }
     }
 
     // the head's rows and the bytes from one token's to the next
@@ -405,10 +415,10 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     };
     auto put_rows = [&](int tid, int i) __attribute__((always_inline)) {
         const int j = i & (NB - 1);
-        if constexpr (!INC) ra.put(tid, s_a2[j]);
-        rb.put(tid, s_b2[j]);
-        rc.put(tid, s_c2[j]);
-        if constexpr (DG) rx.put(tid, s_x2[j]);
+        if constexpr (!INC) ra.put(tid, s_a + j * SZ_K);
+        rb.put(tid, s_b + j * SZ_K);
+        rc.put(tid, s_c + j * SZ_V);
+        if constexpr (DG) rx.put(tid, s_x + j * SZ_V);
     };
     float gnext = 0.f;
     if (nch > 0) {
@@ -435,7 +445,6 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         asm volatile("" : "+v"(rowk), "+v"(tilek), "+v"(rowv), "+v"(colv), "+v"(rowp), "+v"(lane));
         const int g = lane >> 4, li = lane & 15;
         (void)rowk; (void)rowv; (void)rowp;
-        const char *s_a = s_a2[0], *s_b = s_b2[0], *s_c = s_c2[0], *s_x = s_x2[0];
         (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
         if (buf == 0) {
@@ -567,7 +576,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         float x[4];
-                        RV::load_quad(s_x2[rbuf], t, wave * CT * 16 + 16 * ct + 4 * g, x);
+                        RV::load_quad(s_x + rbuf * SZ_V, t, wave * CT * 16 + 16 * ct + 4 * g, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) d = fmaf(x[i], y[ct][tt][i], d);
                     }
@@ -583,25 +592,13 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
         if constexpr (!INC) __syncthreads();  // the weighted products (and the shares) of every wavefront are there
 
         if constexpr (DG) {
-            if (wave == 0 && lane < C) {
+            if (wave == 0) {  // a token's part of the log-decays' gradient; stores as for y below
                 float u = 0.f;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) u += s_u[w][lane];
-                const int64_t at = (int64_t)h * A.ntok + tc + lane;
-                if constexpr (!REV) {
-                    if (lane < n) A.share[vt * A.ntok * A.H + at] = u;
-                } else {
-                    if (vt == 0 && lane < n)  // the forward states' shares, from the pass before
-                        for (int w = 0; w < A.share_tiles; ++w) u += A.share[w * A.ntok * A.H + at];
-                    // sum over the tokens from this one to the segment's end
-#pragma unroll
-                    for (int d = 1; d < C; d <<= 1) {
-                        const float v = __shfl_down(u, d);
-                        if (lane + d < C) u += v;
-                    }
-                    if (lane < n) A.dg_part[vt * A.ntok * A.H + at] = u + carry;
-                }
-                if constexpr (REV) carry += __shfl(u, 0);
+                for (int w = 0; w < NW; ++w) u += s_u[w][lane & (C - 1)];
+                const auto out = __builtin_amdgcn_make_buffer_rsrc(
+                    A.part + ((int64_t)vt * A.H + h) * A.ntok + tc, 0, n * 4, 0x00027000);
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, u), out, lane * 4, 0, 0);
             }
         }
         // ---- the chunk's own products, and the state's update
@@ -699,49 +696,62 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 4 : 2) void kda_hd_chunk_kernel(
     }
 }
 
-template <bool BF, int KD, int VT, bool REV, bool INC, bool DG, bool YF = false>
-hipError_t launch_one(const CoreArgs &a, hipStream_t st) {
-    constexpr int NW = VT / 16;
-    const int64_t groups = (a.slots * a.H + 7) / 8;
-    const int64_t blocks = groups * 8 * a.tiles;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kda_hd_chunk_kernel<BF, KD, VT, NW, REV, INC, DG, YF>), dim3((uint32_t)blocks), dim3(NW * 64), 0,
-                       st, a);
-    return hipGetLastError();
+// Workgroups of one (segment, head) sit 8 apart: the same XCD, whose L2 then holds the rows they share.
+__device__ __forceinline__ bool item_of(const CoreArgs &A, int per_item, int64_t &item, int &r) {
+    const int64_t blk = blockIdx.x, grp = blk / (8 * per_item);
+    const int in = (int)(blk - grp * 8 * per_item);
+    item = grp * 8 + (in & 7);
+    r = in >> 3;
+    return item < A.slots * A.H;
 }
+template <int NW> constexpr int kWavesPerSimd = NW == 8 ? 4 : 2;  // two workgroups of 8 or 4 wavefronts per CU
+
 template <bool BF, int KD, int VT>
-hipError_t launch_kind(const CoreArgs &a, Kind k, hipStream_t st) {
-    const bool yf = BF && a.y_fp32;
-    switch (k) {
-        case Kind::fwd:
-            return yf ? launch_one<BF, KD, VT, false, false, false, BF>(a, st)
-                      : launch_one<BF, KD, VT, false, false, false>(a, st);
-        case Kind::rev:
-            return yf ? launch_one<BF, KD, VT, true, false, false, BF>(a, st)
-                      : launch_one<BF, KD, VT, true, false, false>(a, st);
-        case Kind::fwd_inc: return launch_one<BF, KD, VT, false, true, false>(a, st);
-        case Kind::rev_inc: return launch_one<BF, KD, VT, true, true, false>(a, st);
-        case Kind::fwd_dg:
-            return yf ? launch_one<BF, KD, VT, false, false, true, BF>(a, st)
-                      : launch_one<BF, KD, VT, false, false, true>(a, st);
-        default: return launch_one<BF, KD, VT, true, false, true>(a, st);
-    }
+__global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_fwd_kernel(const CoreArgs A) {
+    __shared__ __align__(16) char smem[Lds<BF, KD, VT, VT / 16, false, false>::bytes];
+    int64_t item;
+    int r;
+    if (!item_of(A, A.tiles, item, r)) return;
+    chunk_pass<BF, KD, VT, VT / 16, false, false, false, false>(A, item, r, smem);
 }
-template <bool BF, int KD>
-hipError_t launch_vt(const CoreArgs &a, int vt, Kind k, hipStream_t st) {
-    switch (vt) {
-        case 32: return launch_kind<BF, KD, 32>(a, k, st);
-        case 64: return launch_kind<BF, KD, 64>(a, k, st);
-        default: return launch_kind<BF, KD, 128>(a, k, st);
-    }
+// The increments of the states (and, from workgroup tiles on, of their gradients).
+template <bool BF, int KD, int VT>
+__global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_inc_kernel(const CoreArgs F, const CoreArgs R, int both) {
+    __shared__ __align__(16) char smem[Lds<BF, KD, VT, VT / 16, true, false>::bytes];
+    int64_t item;
+    int r;
+    if (!item_of(F, both ? 2 * F.tiles : F.tiles, item, r)) return;
+    if (r < F.tiles)
+        chunk_pass<BF, KD, VT, VT / 16, false, true, false, false>(F, item, r, smem);
+    else
+        chunk_pass<BF, KD, VT, VT / 16, true, true, false, false>(R, item, r - F.tiles, smem);
 }
-template <bool BF>
-hipError_t launch_core(const CoreArgs &a, int kd, int vt, Kind k, hipStream_t st) {
-    switch (kd) {
-        case 32: return launch_vt<BF, 32>(a, vt, k, st);
-        case 64: return launch_vt<BF, 64>(a, vt, k, st);
-        default: return launch_vt<BF, 128>(a, vt, k, st);
+// The three gradients of a (segment, head) as workgroups of one launch: dv and dk walk back through the same rows side
+// by side (what one fetches the other finds in L2), dq walks forward.
+template <bool BF, int K, int V, int VT, bool DG, bool YF>
+__global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_grad_kernel(const GradArgs G) {
+    constexpr int NW = VT / 16;
+    constexpr int L1 = Lds<BF, V, VT, NW, false, DG>::bytes, L2 = Lds<BF, K, VT, NW, false, DG>::bytes;
+    __shared__ __align__(16) char smem[L1 > L2 ? L1 : L2];
+    int64_t item;
+    int r;
+    if (!item_of(G.dv, G.dv.tiles + 2 * G.dk.tiles, item, r)) return;
+    if (r < G.dv.tiles) {
+        chunk_pass<BF, K, VT, NW, true, false, DG, false>(G.dv, item, r, smem);
+        return;
     }
+    r -= G.dv.tiles;
+    if (r < G.dk.tiles)
+        chunk_pass<BF, V, VT, NW, true, false, false, YF>(G.dk, item, r, smem);
+    else
+        chunk_pass<BF, V, VT, NW, false, false, DG, YF>(G.dq, item, r - G.dk.tiles, smem);
+}
+
+inline hipError_t grid_of(const CoreArgs &a, int64_t per_item, dim3 &grid) {
+    const int64_t blocks = (a.slots * a.H + 7) / 8 * 8 * per_item;
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    grid = dim3((uint32_t)blocks);
+    return hipSuccess;
 }
 
 }  // namespace hd
