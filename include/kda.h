@@ -469,8 +469,8 @@ typedef enum {
 
 /*
  * Workspace bytes of kda_hd_chunk_fwd and kda_hd_chunk_bwd (arguments as
- * there; packed: whether cu_seqlens is given, 0 or 1). Never 0 for sizes that
- * are supported; 0 otherwise.
+ * there; packed: whether cu_seqlens is given, 0 or 1). 0 for sizes that are
+ * not supported, else at least 256; at 256 the call keeps nothing there.
  */
 size_t kda_hd_chunk_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
                                         int32_t num_seqs, int32_t packed, kda_dtype_t io);

@@ -97,8 +97,10 @@ __global__ __launch_bounds__(1024) void kda_hd_table_kernel(const int32_t *__res
         if (n < N) {
             const int64_t at = first + s_sum[t] - count;
             seqs[n] = SeqSlots{(int32_t)at, count};
+            // equal parts (at most `seg`, so none is empty): workgroups of one length
+            const int64_t part = ((end - before + count - 1) / count + 63) / 64 * 64;
             for (int32_t j = 0; j < count; ++j) {
-                const int64_t a = before + j * seg, e = a + seg;
+                const int64_t a = before + j * part, e = a + part;
                 table[at + j] = Segment{(int32_t)n, j, count, 0, a, e < end ? e : end};
             }
         }

@@ -54,6 +54,16 @@ def _workspace(workspace, need: int, what: str, dev):
     return workspace
 
 
+_untouched = {}
+
+
+def _no_workspace(dev):
+    """What a call that keeps nothing in its workspace is given: any calls may name the same bytes."""
+    if dev not in _untouched:
+        _untouched[dev] = torch.empty(256, dtype=torch.uint8, device=dev)
+    return _untouched[dev]
+
+
 def _result(out, name, shape, dtype, dev):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
@@ -125,6 +135,8 @@ def hd_chunk_fwd(q, k, v, g, S0=None, cu_seqlens=None, scale: float = 1.0, outpu
     if S0 is not None:
         _need(S0, "S0", (N, H, K, V), torch.float32, dev)
     need = lib.kda_hd_chunk_fwd_workspace_bytes(B, T, H, Hk, K, V, N, int(cu_seqlens is not None), io)
+    if workspace is None and need == 256:
+        workspace = _no_workspace(dev)
     workspace = _workspace(workspace, need, "hd_chunk_fwd(B=%d, T=%d, H=%d, Hk=%d, K=%d, V=%d, num_seqs=%d)"
                            % (B, T, H, Hk, K, V, N), dev)
     out = _result(out, "out", (B, T, H, V), dt, dev)
