@@ -429,6 +429,14 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
             if (nch > 1) take_rows(threadIdx.x, 1);
         }
     }
+    if constexpr (!INC) {
+        // As many stores as a chunk ends with, into a buffer of no bytes (nothing is written): rows are waited for by
+        // how many memory operations came after them, and the loop's first chunk has to look like the others, or all of
+        // them would wait for the last chunk's stores as well.
+        const auto none = __builtin_amdgcn_make_buffer_rsrc(A.y, 0, 0, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < CT * TT; ++i) __builtin_amdgcn_raw_buffer_store_b64(u32x2{0, 0}, none, 16 * i, 0, 0);
+    }
 
     for (int cc = 0; cc < nch; ++cc) {
         int64_t tc;
