@@ -490,8 +490,9 @@ size_t kda_hd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t
  *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
  * The state is fp32 throughout; for bf16 I/O what is added to it is exact to
  * fp32. A non-finite q, k, v or g spoils its own head and sequence, from the
- * first token of its 64-token chunk on. Errors as for kda_chunk_fwd
- * (INVALID_VALUE also for H % Hk != 0 and a scale that is not finite).
+ * first token of its 32-token chunk on. Errors as for kda_chunk_fwd
+ * (INVALID_VALUE also for H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a
+ * scale that is not finite).
  */
 kda_status_t kda_hd_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
                               const int32_t *cu_seqlens, int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K,

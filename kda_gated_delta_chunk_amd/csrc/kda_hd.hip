@@ -120,14 +120,15 @@ struct CarryArgs {
 // In place: what each segment adds becomes the state it starts from (rev: the state gradient it ends with). A thread
 // carries four adjacent state entries over the segments of its sequence.
 __global__ __launch_bounds__(256) void kda_hd_carry_kernel(const CarryArgs F, const CarryArgs R,
-                                                           const SeqSlots *__restrict__ seqs, int32_t nseg, int32_t H,
-                                                           int64_t kv4) {
-    const int rev = blockIdx.y;
+                                                           const SeqSlots *__restrict__ seqs, int32_t N, int32_t nseg,
+                                                           int32_t H, int64_t kv4) {
+    const int rev = blockIdx.z;
     float *seg = rev ? R.seg : F.seg;
     const float *decay = rev ? R.decay : F.decay, *init = rev ? R.init : F.init;
-    const int64_t runs = (kv4 + 255) / 256, nh = blockIdx.x / runs, n = nh / H;
-    const int64_t e = (blockIdx.x - nh * runs) * 256 + threadIdx.x;
-    if (e >= kv4) return;
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    const int64_t runs = (kv4 + 255) / 256, nh = blk / runs, n = nh / H;
+    const int64_t e = (blk - nh * runs) * 256 + threadIdx.x;
+    if (e >= kv4 || n >= N) return;
     const int h = (int)(nh - n * H);
     const int32_t first = seqs ? seqs[n].first : (int32_t)(n * nseg), count = seqs ? seqs[n].count : nseg;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
@@ -150,11 +151,9 @@ __global__ __launch_bounds__(256) void kda_hd_carry_kernel(const CarryArgs F, co
 hipError_t launch_carry(const CarryArgs &f, const CarryArgs *r, const SeqSlots *seqs, const Plan &p, const HdArgs &a,
                         hipStream_t st) {
     const int64_t kv4 = (int64_t)a.K * a.V / 4, nh = (int64_t)a.num_seqs * a.H;
-    // heads of all sequences times runs of 256 state entries: num_seqs * H < 2^26, K * V / 1024 <= 16
-    const int64_t x = (kv4 + 255) / 256;
-    if (nh * x >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kda_hd_carry_kernel, dim3((uint32_t)(nh * x), r ? 2 : 1), dim3(256), 0, st, f, r ? *r : f, seqs,
-                       p.nseg, a.H, kv4);
+    dim3 grid = wide_grid(nh * ((kv4 + 255) / 256));
+    if (r) grid.z = 2;
+    hipLaunchKernelGGL(kda_hd_carry_kernel, grid, dim3(256), 0, st, f, r ? *r : f, seqs, a.num_seqs, p.nseg, a.H, kv4);
     return hipGetLastError();
 }
 
@@ -168,13 +167,15 @@ __global__ __launch_bounds__(1024) void kda_hd_dg_kernel(const CoreArgs A, const
                                                          void *__restrict__ dg) {
     __shared__ float s_total[2][2][8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hsub = wave >> 3, blk = wave & 7;
-    const int h = blockIdx.y * 2 + hsub;
-    const Segment sg = segment_of(A, blockIdx.x);
+    const int h = blockIdx.z * 2 + hsub;
+    const int64_t slot = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    if (slot >= A.slots) return;
+    const Segment sg = segment_of(A, slot);
     if (sg.seq < 0 || sg.t1 <= sg.t0) return;
     const bool live = h < A.H;
     double behind = 0.0;
     if (live) {
-        for (int w = 0; w < A.tiles; ++w) behind += A.border[((int64_t)w * A.slots + blockIdx.x) * A.H + h];
+        for (int w = 0; w < A.tiles; ++w) behind += A.border[((int64_t)w * A.slots + slot) * A.H + h];
         if (sg.j == sg.nseg - 1 && dS) {
             const int64_t kv4 = (int64_t)K * A.VD / 4, at = ((int64_t)sg.seq * A.H + h) * kv4;
             const f32x4 *x = reinterpret_cast<const f32x4 *>(dS) + at, *y = reinterpret_cast<const f32x4 *>(s_end) + at;
@@ -460,7 +461,8 @@ hipError_t launch_hd_bwd(const HdArgs &a, hipStream_t st) {
                       : grad_pass_fp32(g, a.K, a.V, a.dg != nullptr, st));
     if (ntok == 0) return hipSuccess;
     if (a.dg) {
-        const dim3 grid((uint32_t)c.p.slots, (uint32_t)((a.H + 1) / 2));
+        dim3 grid = wide_grid(c.p.slots);
+        grid.z = (uint32_t)((a.H + 1) / 2);
         if (a.io_bf16)
             hipLaunchKernelGGL(kda_hd_dg_kernel<true>, grid, dim3(1024), 0, st, g.dv, g.dq.part, g.dq.tiles, a.K,
                                a.dS_final, s_end, a.dg);

@@ -66,6 +66,12 @@ constexpr int fwd_tile(int V, bool bf16) { return bf16 || V < 64 ? V : 64; }
 constexpr int grad_tile(int K, int V, bool bf16) { return fwd_tile(K < V ? K : V, bf16); }
 constexpr int inc_tile(int V) { return V < 64 ? V : 64; }
 
+// A grid of n workgroups (at least; under 2^32): a dimension's threads are 32-bit, and 2^20 workgroups of 1024 are within.
+inline dim3 wide_grid(int64_t n) {
+    const int64_t x = (int64_t)1 << 20;
+    return n <= x ? dim3((uint32_t)n) : dim3((uint32_t)x, (uint32_t)((n + x - 1) / x));
+}
+
 // The passes. inc_pass: the increments of the states, and with r those of their gradients.
 hipError_t fwd_pass(bool bf16, const CoreArgs &a, int K, int vt, hipStream_t st);
 hipError_t inc_pass(bool bf16, const CoreArgs &f, const CoreArgs *r, int K, int vt, hipStream_t st);

@@ -8,8 +8,8 @@
 //   y_t = s_intra sum_s D_ts (a_t.b_s) c_s + s_inter win_t St^T a_t,    St <- e^{b_C} St + s_up sum_s wup_s b_s c_s^T
 // chunk by chunk: forward in time (s <= t, win = e^{b_t}, wup = e^{b_C - b_s}) or backward (REV: s >= t,
 // win = e^{b_C - b_t}, wup = e^{b_s}). The differences of b are at most 0 wherever they are used, so no weight
-// overflows however strong the decay; b is kept as a whole part and a rest in [0, 1) (base 2), whose differences are
-// exact, so a token that decays everything (down to -inf, held at e^-104 = 0) does not cost its neighbours precision.
+// overflows however strong the decay; b is kept (base 2) as a multiple of 2^-8, whose sums and differences are exact, and
+// a rest, so a token that decays everything (down to -inf, held at e^-104 = 0) does not cost its neighbours precision.
 //
 // Layout (16x16 matrix-core tiles, see kda_common.hpp). A workgroup owns one (segment of a sequence, head, tile of VT
 // columns); each wavefront owns CT 16-column tiles of the state, all KD rows, as fp32 accumulators. An accumulator
@@ -19,9 +19,15 @@
 // products D (a.b) go through LDS once, shared by all wavefronts.
 //
 // Precision (bf16 I/O). Products of inputs are exact in the matrix cores' fp32 sums. Three operands are computed
-// values: the weighted products D (a.b) and the state as an operand are rounded to bf16 pairs or singles (PLO, SLO:
-// whether the rounding's rest is multiplied too), and wup c, which everything later in the sequence is summed from,
-// goes in as three bf16 parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
+// values. The weighted products D (a.b) go in as two bf16 parts (16 bits: with one, a result's error is 1.4 times its own
+// rounding, with two 1.05 times, for 1% of the time). The state as an operand is one bf16 part, two (SLO) where the
+// log-decays' gradient is summed from what it gives, for its terms cancel. wup c, which everything later in the sequence
+// is summed from, goes in as three parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
+//
+// What bounds it. Per token and head of K = V = 128 in bf16 the forward pass moves 1 KB and multiplies 0.36 MFLOP, of
+// which 0.2 MFLOP are the three parts of wup c: at the card's rates the bytes take longer, but a chunk's steps (weighted
+// products, one barrier, the state's products) follow each other, so what bounds it is their latency and the vector
+// instructions that convert, scale and address, with two workgroups of 8 wavefronts a CU to hide behind one another.
 #pragma once
 
 #include "kda_common.hpp"
@@ -139,7 +145,7 @@ template <int NCOL> struct Rows<false, NCOL> {
 
 // C rows of a chunk on their way to LDS: from p, `pitch` bytes apart; rows behind the last of `n` repeat it (their
 // weights are zero). take() issues the loads, put() waits for them: a chunk's rows travel while the one before it is
-// worked on. A lane's offsets (under 2^32: 64 rows) grow with the row, so holding them to the last row's is a minimum;
+// worked on. A lane's offsets (32 rows: under 2^31) grow with the row, so holding them to the last row's is a minimum;
 // the base is the same for all lanes.
 template <bool BF, int NCOL, int C, int NT>
 struct Stage {
@@ -164,8 +170,8 @@ struct Stage {
     }
 };
 
-// Sums of a chunk's log-decays (base 2) over the lanes 0 .. C-1 of a wavefront: exact whole multiples of 2^-8 (at most
-// 64 * 151 in size: 22 bits) and a rest of at most 2^-3, each summed in fp32.
+// A log-decay in base 2: a multiple of 2^-8 (a chunk's sum is at most 32 * 151 in size: 21 bits, exact in fp32) and a
+// rest of at most 2^-9 (2^-4 in a chunk's sum).
 struct Decay { float hi, lo; };
 __device__ __forceinline__ Decay decay_base2(float g) {
     g = g < -104.f ? -104.f : g;  // e^-104 is 0 in fp32; NaN stays
@@ -177,9 +183,6 @@ __device__ __forceinline__ Decay decay_base2(float g) {
 __device__ __forceinline__ float lane_value(float x, int lane) {  // the same for all lanes
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
-
-// Sum over the 16 lanes of a row, in its last lane.
-__device__ __forceinline__ float row_sum_last(float x) { return row_scan16(x); }
 
 // Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
 __device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<true> &hi, Frag8<true> &lo) {
@@ -235,10 +238,9 @@ __device__ __forceinline__ void mfma_fence_state(f32x4 (&x)[M][N]) {
 template <bool BF, int KD, int VT, int NW, bool INC, bool DG>
 struct Lds {
     static constexpr int C = kChunk, NB = BF ? 2 : 1, DB = 2 * NW;  // DB: chunks whose decays are made at a time
-    static constexpr bool PLO = BF && DG;
     static constexpr int K = Rows<BF, KD>::bytes(C), V = Rows<BF, VT>::bytes(C), P = Rows<BF, C>::bytes(C);
     static constexpr int b = 0, c = b + NB * K, a = c + NB * V, x = a + (INC ? 0 : NB * K), p = x + (DG ? NB * V : 0);
-    static constexpr int pl = p + (INC ? 0 : P), wup = pl + (PLO ? P : 0), win = wup + DB * C * 4;
+    static constexpr int pl = p + (INC ? 0 : P), wup = pl + (BF && !INC ? P : 0), win = wup + DB * C * 4;
     static constexpr int bh = win + (INC ? 0 : DB * C * 4), bl = bh + (INC ? 0 : DB * C * 4);
     static constexpr int f = bl + (INC ? 0 : DB * C * 4), ec = f + (INC ? 0 : DB * C * 4), u = ec + DB * 4;
     static constexpr int red = u + (DG ? NW * C * 4 : 0), bytes = red + NW * 4;
@@ -252,7 +254,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
     constexpr int DB = L::DB, NB = L::NB;
     constexpr int NPART = BF ? 3 : 1;
-    constexpr bool PLO = L::PLO, SLO = BF && DG;
+    constexpr bool SLO = BF && DG;
     static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
     using E = typename IO<BF>::T;
     using RK = Rows<BF, KD>;
@@ -342,7 +344,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     if constexpr (!INC) {  // tiles across the diagonal that are read but never computed
         for (int i = threadIdx.x; i < SZ_P / 16; i += NT) {
             reinterpret_cast<uint4 *>(s_p)[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (PLO) reinterpret_cast<uint4 *>(s_pl)[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (BF) reinterpret_cast<uint4 *>(s_pl)[i] = make_uint4(0, 0, 0, 0);
         }
     }
     float btot = 0.f;
@@ -452,7 +454,6 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
         int colv = colv0 + rbuf * SZ_V, rowp = rowp0, lane = lane0;
         asm volatile("" : "+v"(rowk), "+v"(tilek), "+v"(rowv), "+v"(colv), "+v"(rowp), "+v"(lane));
         const int g = lane >> 4, li = lane & 15;
-        (void)rowk; (void)rowv; (void)rowp;
         (void)rowk; (void)rowv; (void)rowp; (void)s_a; (void)s_x; (void)s_win; (void)s_bh; (void)s_bl; (void)s_f;
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
         if (buf == 0) {
@@ -525,7 +526,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
                     for (int i = 0; i < 4; ++i) {
                         const float X = w[i] * acd[i];
                         csum += X;
-                        const float r = row_sum_last(X);
+                        const float r = row_scan16(X);  // the row's sum, in its last lane
                         if (li == 15) s_u[wave][16 * ts + 4 * g + i] += r;
                     }
                     csum += __shfl_xor(csum, 16);
@@ -534,7 +535,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
                     if (g == 0) s_u[wave][t] -= csum;
                     __builtin_amdgcn_wave_barrier();
                 }
-                if constexpr (PLO) {
+                if constexpr (BF) {
                     uint2 hi, lo;
                     split_bf16(w[0], w[1], hi.x, lo.x);
                     split_bf16(w[2], w[3], hi.y, lo.y);
@@ -630,7 +631,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
                     for (int tt = 0; tt < TT; ++tt) {
                         if (REV ? 2 * s + 1 < tt : 2 * s > tt) continue;
                         y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p + 16 * tt * RP::RB, rowp, s));
-                        if constexpr (PLO) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl + 16 * tt * RP::RB, rowp, s));
+                        if constexpr (BF) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl + 16 * tt * RP::RB, rowp, s));
                     }
                 }
                 scaled_frags(cf, w, cw[ct]);
@@ -655,7 +656,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
             // around them would make the next chunk's rows, which were asked for before, wait for them too. (The whole
             // offset is in the lane's part: the scalar part is not held against the buffer's end.)
             constexpr int eb = BF && !YF ? 2 : 4;
-            const uint32_t pitch = (uint32_t)A.H * (uint32_t)(A.VD * eb);  // 64 rows: under 2^32
+            const uint32_t pitch = (uint32_t)A.H * (uint32_t)(A.VD * eb);  // 32 rows: under 2^31
             const auto out = __builtin_amdgcn_make_buffer_rsrc(
                 reinterpret_cast<char *>(A.y) + ((int64_t)tc * A.H + h) * A.VD * eb, 0, (n - 1) * pitch + A.VD * eb,
                 0x00027000);
@@ -706,7 +707,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
 
 // Workgroups of one (segment, head) sit 8 apart: the same XCD, whose L2 then holds the rows they share.
 __device__ __forceinline__ bool item_of(const CoreArgs &A, int per_item, int64_t &item, int &r) {
-    const int64_t blk = blockIdx.x, grp = blk / (8 * per_item);
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, grp = blk / (8 * per_item);
     const int in = (int)(blk - grp * 8 * per_item);
     item = grp * 8 + (in & 7);
     r = in >> 3;
@@ -755,11 +756,8 @@ __global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_grad_ke
         chunk_pass<BF, V, VT, NW, false, false, DG, YF>(G.dq, item, r - G.dk.tiles, smem);
 }
 
-inline hipError_t grid_of(const CoreArgs &a, int64_t per_item, dim3 &grid) {
-    const int64_t blocks = (a.slots * a.H + 7) / 8 * 8 * per_item;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    grid = dim3((uint32_t)blocks);
-    return hipSuccess;
+inline dim3 grid_of(const CoreArgs &a, int64_t per_item) {
+    return wide_grid((a.slots * a.H + 7) / 8 * 8 * per_item);
 }
 
 }  // namespace hd

@@ -113,8 +113,11 @@ template <bool BF, int K, int V>
 hipError_t launch_kv(const HdDecodeArgs &a, hipStream_t st) {
     constexpr int NT = K * V / 4 < 1024 ? K * V / 4 : 1024;
     const int32_t NH = a.N * a.H;
-    // up to 4096 workgroups take one pair each; above that each walks about 4 pairs
-    const int32_t grid = NH <= 4096 ? NH : (NH + 3) / 4 > 4096 ? (NH + 3) / 4 : 4096;
+    // up to 4096 workgroups take one pair each; above that each walks about 4 pairs (more where the grid's threads would
+    // pass 32 bits)
+    constexpr int32_t most = 1 << 21;
+    const int32_t quarter = (NH + 3) / 4;
+    const int32_t grid = NH <= 4096 ? NH : quarter < 4096 ? 4096 : quarter < most ? quarter : most;
     hipLaunchKernelGGL((kda_hd_decode_kernel<BF, K, V, NT>), dim3(grid), dim3(NT), 0, st, a.q, a.k, a.v, a.g, a.S, a.o,
                        a.H, a.H / a.Hk, (int)a.decay_per_head, a.scale, NH);
     return hipGetLastError();

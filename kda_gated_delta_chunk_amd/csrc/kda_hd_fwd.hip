@@ -6,8 +6,7 @@ namespace hd {
 namespace {
 template <bool BF, int KD, int VT>
 hipError_t fwd_kv(const CoreArgs &a, hipStream_t st) {
-    dim3 grid;
-    if (hipError_t e = grid_of(a, a.tiles, grid)) return e;
+    const dim3 grid = grid_of(a, a.tiles);
     hipLaunchKernelGGL((kda_hd_fwd_kernel<BF, KD, VT>), grid, dim3(VT * 4), 0, st, a);
     return hipGetLastError();
 }
@@ -24,8 +23,7 @@ hipError_t fwd_b(const CoreArgs &a, int K, int vt, hipStream_t st) {
 }
 template <bool BF, int KD, int VT>
 hipError_t inc_kv(const CoreArgs &f, const CoreArgs *r, hipStream_t st) {
-    dim3 grid;
-    if (hipError_t e = grid_of(f, r ? 2 * f.tiles : f.tiles, grid)) return e;
+    const dim3 grid = grid_of(f, r ? 2 * f.tiles : f.tiles);
     hipLaunchKernelGGL((kda_hd_inc_kernel<BF, KD, VT>), grid, dim3(VT * 4), 0, st, f, r ? *r : f, (int)(r != nullptr));
     return hipGetLastError();
 }

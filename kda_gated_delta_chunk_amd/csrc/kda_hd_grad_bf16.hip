@@ -6,8 +6,7 @@ namespace hd {
 namespace {
 template <int K, int V, int VT, bool DG, bool YF>
 hipError_t launch(const GradArgs &g, hipStream_t st) {
-    dim3 grid;
-    if (hipError_t e = grid_of(g.dv, g.dv.tiles + 2 * g.dk.tiles, grid)) return e;
+    const dim3 grid = grid_of(g.dv, g.dv.tiles + 2 * g.dk.tiles);
     hipLaunchKernelGGL((kda_hd_grad_kernel<true, K, V, VT, DG, YF>), grid, dim3(VT * 4), 0, st, g);
     return hipGetLastError();
 }

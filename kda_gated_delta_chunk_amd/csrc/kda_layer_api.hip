@@ -63,12 +63,13 @@ kda_status_t check_hd_sizes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t
     if (H % Hk != 0) return KDA_ERROR_INVALID_VALUE;
     if (packed ? (B != 1) : (num_seqs != B)) return KDA_ERROR_INVALID_VALUE;
     if (!supported_dim(K) || !supported_dim(V)) return KDA_ERROR_NOT_SUPPORTED;
-    // element counts; cu_seqlens and a sequence's chunks are 32-bit; workgroups of a pass (at most one per 256 tokens
-    // of a sequence, head and 32 columns) stay launchable
+    // element counts; cu_seqlens and a sequence's chunks are 32-bit
     if (T >= ((int64_t)1 << 31) || T > kMaxElems / B || B * T > kMaxElems / H / 512) return KDA_ERROR_INVALID_VALUE;
-    // 64 tokens of all heads stay below 2^32 bytes (the kernels' offsets within a chunk)
+    // a chunk's rows of all heads (32 tokens) stay below 2^31 bytes, the kernels' offsets within it; heads and states
+    // are 32-bit
     if (H >= (1 << 16) || (int64_t)num_seqs * H >= ((int64_t)1 << 26)) return KDA_ERROR_INVALID_VALUE;
-    if ((B * ((T + 255) / 256) + num_seqs) > ((int64_t)1 << 28) / H) return KDA_ERROR_INVALID_VALUE;
+    // workgroups of a pass (at most 9 for each head of a segment, at least 256 tokens or a sequence) stay below 2^32
+    if ((B * ((T + 255) / 256) + num_seqs) > ((int64_t)1 << 27) / H) return KDA_ERROR_INVALID_VALUE;
     return KDA_SUCCESS;
 }
 
@@ -226,7 +227,8 @@ kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const
 static kda_status_t check_norm_sizes(int64_t rows, int32_t groups, int32_t C) {
     if (rows < 0 || groups < 1 || C < 1 || rows % groups != 0) return KDA_ERROR_INVALID_VALUE;
     if (C > 16384) return KDA_ERROR_NOT_SUPPORTED;
-    if (rows > kMaxElems / C || groups > (1 << 20)) return KDA_ERROR_INVALID_VALUE;
+    // a workgroup of 1024 threads for 64 parameters: a grid's threads are 32-bit
+    if (rows > kMaxElems / C || (int64_t)groups * C > (1 << 27)) return KDA_ERROR_INVALID_VALUE;
     return KDA_SUCCESS;
 }
 

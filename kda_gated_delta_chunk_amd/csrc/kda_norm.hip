@@ -11,9 +11,9 @@
 // the statistics, so nothing is kept from the forward. All arithmetic is fp32.
 //
 // Row r has the parameters of group r % G. A row is handled by TPR threads; a thread's rows are a whole multiple of G
-// apart, so its parameters, and its sums for their gradients, stay in registers over all of its rows. The sums leave
-// as one partial row per row slot of the grid and a second kernel adds those in a fixed order (no atomics: the same
-// inputs give the same bits).
+// apart, so its parameters, and its sums for their gradients, stay in registers over all of its rows. At the end a
+// workgroup adds up its row slots of one group where G divides their number, the sums leave as partial rows, and a
+// second kernel adds those in a fixed order (no atomics: the same inputs give the same bits).
 #include "kda_common.hpp"
 #include "kda_layer.hpp"
 
@@ -217,7 +217,10 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
     }
 }
 
-// part: [2][slots][C] fp32, the sums of e n and of e over the rows of each slot
+// Partial rows that a workgroup of rpw row slots leaves: one per group where that is possible.
+__host__ __device__ constexpr int parts_of(int rpw, int G) { return rpw % G == 0 ? G : rpw; }
+
+// part: [2][partial rows][C] fp32, the sums of e n and of e over the rows of each
 template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
 __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void kda_norm_bwd_kernel(const void *__restrict__ dyp, const void *__restrict__ xp,
                                                           const void *__restrict__ zp, const float *__restrict__ wp,
@@ -333,24 +336,43 @@ __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void 
             dw[e] = s_acc[e][threadIdx.x];
             db[e] = s_acc[EPT + e][threadIdx.x];
         }
-    if (want_dw) SL::store_param(part, slot, C, t, dw);
-    if (want_db) SL::store_param(part + slots * C, slot, C, t, db);
+    const int per = parts_of(RPW, G);
+    if constexpr (RPW > 1) {
+        __shared__ float s_sum[RPW][EPT][TPR];
+        if (per < RPW) {  // uniform: slots sub, sub + G, ... of the workgroup are of one group
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                if (p == 1) __syncthreads();
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) s_sum[sub][e][t] = p ? db[e] : dw[e];
+                __syncthreads();
+                if (sub < per)
+                    for (int j = sub + per; j < RPW; j += per)
+#pragma unroll
+                        for (int e = 0; e < EPT; ++e) (p ? db : dw)[e] += s_sum[j][e][t];
+            }
+        }
+    }
+    if (sub >= per) return;
+    const int64_t row = (int64_t)blockIdx.x * per + sub, all = (int64_t)gridDim.x * per;
+    if (want_dw) SL::store_param(part, row, C, t, dw);
+    if (want_db) SL::store_param(part + all * C, row, C, t, db);
 }
 
-// dw[g][c], db[g][c] = sum over the slots s with s % G == g, in order: 16 wavefronts take every 16th of them, then
-// one adds the wavefronts.
+// dw[g][c], db[g][c] = sum over the partial rows s with s % G == g, in order: 16 wavefronts take every 16th of them,
+// 8 loads at a time, then one adds the wavefronts.
 __global__ __launch_bounds__(1024) void kda_norm_param_kernel(const float *__restrict__ part, float *__restrict__ dw,
-                                                              float *__restrict__ db, int64_t slots, int G, int C) {
+                                                              float *__restrict__ db, int64_t parts, int G, int C) {
     __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)G * C;
     float *out = blockIdx.y ? db : dw;
     if (!out) return;  // uniform
-    const float *p = part + (blockIdx.y ? slots * C : 0);
+    const float *p = part + (blockIdx.y ? parts * C : 0);
     float a = 0.f;
     if (col < cols) {
-        const int64_t n = slots / G;
-#pragma unroll 4
+        const int64_t n = parts / G;
+#pragma unroll 8
         for (int64_t i = wave; i < n; i += 16) a += p[i * cols + col];
     }
     s[wave][lane] = a;
@@ -391,7 +413,7 @@ hipError_t run_gate(const NormArgs &a, bool bwd, hipStream_t st) {
     if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
     const int64_t cols = (int64_t)a.G * a.C;
     hipLaunchKernelGGL(kda_norm_param_kernel, dim3((uint32_t)((cols + 63) / 64), 2), dim3(1024), 0, st, part,
-                       a.dweight, a.dbias, wgs * RPW, a.G, a.C);
+                       a.dweight, a.dbias, wgs * parts_of(RPW, a.G), a.G, a.C);
     return hipGetLastError();
 }
 template <bool BF, bool VEC, int TPR, int NT, int EPT>
@@ -419,7 +441,7 @@ hipError_t by_type(const NormArgs &a, bool bwd, hipStream_t st) {
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t G, int32_t C) {
     const int rpw = C <= 64 ? 32 : C <= 128 ? 16 : C <= 512 ? 4 : 1;  // NT / TPR of by_width
-    return (size_t)(grid_for(rows, G, rpw, kMaxWG) * rpw) * C * 2 * sizeof(float);
+    return (size_t)(grid_for(rows, G, rpw, kMaxWG) * parts_of(rpw, G)) * C * 2 * sizeof(float);
 }
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
     return a.rows == 0 ? hipSuccess : by_type(a, false, st);

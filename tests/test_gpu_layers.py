@@ -148,6 +148,63 @@ def test_hd_segments(io, T):
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H,Hk,K,V", [(2100, 2, 1, 128, 128), (1500, 3, 1, 128, 32), (1501, 1, 1, 32, 128),
+                                        (1100, 5, 5, 32, 32)])
+def test_hd_segments_of_shared_heads(io, T, H, Hk, K, V):
+    x = hd_inputs(1, T, H, Hk, K, V, io, 12)
+    o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"])
+    check_fwd(x, o, S)
+    r = kda.hd_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_final=x["dS"])
+    check_bwd(x, r)
+    cu = [5, 1, T - 700, T - 699, T - 3]  # falls once: read as 5
+    x = hd_inputs(1, T, H, Hk, K, V, io, 13, N=4)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"], cu_seqlens=c)
+    r = kda.hd_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=c)
+    for res in (o, r["dq"], r["dk"], r["dv"], r["dg"]):  # rows of no sequence are as they were: anything
+        res[:, :5], res[:, T - 3:] = 0.0, 0.0
+    check_fwd(x, o, S, cu=c.cpu())
+    check_bwd(x, r, cu=c.cpu())
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("strength", [-20.0, -1.0, 0.0, 1.5])
+@pytest.mark.parametrize("T", [31, 32, 95, 96, 97, 161])
+def test_hd_lengths_about_whole_chunks(io, strength, T):
+    """One to six chunks, full and ragged, with decays from none to e^-200 a chunk, so that two chunks' decays are
+    within one scaling, or only one's, or neither's."""
+    x = hd_inputs(1, T, 2, 1, 64, 64, io, 14, strength=strength)
+    x["g"][:, : T // 2, 1] *= 0.25
+    o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"])
+    check_fwd(x, o, S)
+    r = kda.hd_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_final=x["dS"])
+    check_bwd(x, r)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_hd_nan_stays_in_its_sequence_and_head(io):
+    """A NaN reaches its own head of its own sequence, and no token before its chunk of 32."""
+    cu = torch.tensor([0, 40, 150, 190], dtype=torch.int32, device="cuda")
+    x = hd_inputs(1, 190, 3, 3, 64, 64, io, 15, N=3)
+    args = [x[n] for n in ("q", "k", "v", "g")]
+    o, S = kda.hd_chunk_fwd(*args, S0=x["S0"], cu_seqlens=cu)
+    r = kda.hd_chunk_bwd(*args, x["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=cu)
+    x["v"][:, 40 + 50, 1, 3] = float("nan")
+    x["k"][:, 40 + 51, 1, 5] = float("inf")
+    on, Sn = kda.hd_chunk_fwd(*args, S0=x["S0"], cu_seqlens=cu)
+    rn = kda.hd_chunk_bwd(*args, x["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=cu)
+    assert bool(on[0, 90:150, 1].isnan().any()) and bool(Sn[1, 1].isnan().any())
+    on[0, 40 + 32:150, 1] = o[0, 40 + 32:150, 1]
+    Sn[1, 1] = S[1, 1]
+    assert torch.equal(on, o) and torch.equal(Sn, S)
+    for n in ("dq", "dk", "dv", "dg"):
+        rn[n][0, 40:150, 1] = r[n][0, 40:150, 1]
+        assert torch.equal(rn[n], r[n]), n
+    rn["dS0"][1, 1] = r["dS0"][1, 1]
+    assert torch.equal(rn["dS0"], r["dS0"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
 @pytest.mark.parametrize("cu", [[0, 0, 1, 64, 64, 191, 400], [3, 700, 700, 1180], [0, 1180], [1180, 1180], [0, 0]])
 def test_hd_packed(io, cu):
     """Empty sequences, one token, borders inside a chunk, segments; rows outside the sequences stay as they were and
@@ -310,6 +367,9 @@ def test_hd_refusals():
         kda.hd_chunk_fwd(*[torch.zeros(1, 8, 4, 48, device="cuda") for _ in range(3)], torch.zeros(1, 8, 4, device="cuda"))
     with pytest.raises(kda.KDAError):
         kda.hd_chunk_fwd(q, k, v, g, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    many = [torch.zeros(1, 1, 1 << 16, 32, device="cuda") for _ in range(3)]
+    with pytest.raises(kda.KDAError):
+        kda.hd_chunk_fwd(*many, torch.zeros(1, 1, 1 << 16, device="cuda"))
     S = torch.zeros(8, 4, 32, 32, device="cuda")
     with pytest.raises(ValueError):
         kda.hd_decode_step(q[0], k[0], v[0], g[0], S[:7])
@@ -395,7 +455,10 @@ def norm_inputs(shape, wdim, io, gate, seed):
 
 NORMS = [((1, 1), 1), ((7, 3), 1), ((5, 16), 0), ((33, 64), 1), ((9, 100), 1), ((3, 5, 128), 2), ((11, 6, 96), 2),
          ((40, 257), 1), ((6, 512), 1), ((4, 1000), 1), ((3, 2049), 1), ((5, 4096), 1), ((2, 7, 700), 2), ((3, 5001), 1),
-         ((2, 8192), 1), ((2, 16384), 1), ((3, 9999), 1), ((300, 3, 24), 2), ((1500, 128), 1)]
+         ((2, 8192), 1), ((2, 16384), 1), ((3, 9999), 1), ((300, 3, 24), 2), ((1500, 128), 1),
+         # more rows than the backward's grid takes at a time: groups that divide a workgroup's rows and that do not
+         ((20000, 17), 1), ((9000, 4, 40), 2), ((9000, 3, 128), 2), ((700, 64, 32), 2), ((5000, 2, 300), 2),
+         ((1030, 5, 300), 2), ((1100, 2500), 1), ((650, 5001), 1), ((520, 8200), 1), ((515, 9001), 1)]
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])

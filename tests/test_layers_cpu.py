@@ -258,8 +258,8 @@ def test_layer_abi_under_address_sanitizer(tmp_path):
     point with rejected arguments, sweeps the workspace queries and, without a GPU, stops valid calls at the device
     check."""
     csrc = ROOT / "kda_gated_delta_chunk_amd" / "csrc"
-    sources = ["kda_layer_api.hip", "kda_hd.hip", "kda_hd_bf16.hip", "kda_hd_fp32.hip", "kda_hd_decode.hip",
-               "kda_rotary.hip", "kda_norm.hip"]
+    sources = ["kda_layer_api.hip", "kda_hd.hip", "kda_hd_fwd.hip", "kda_hd_grad_bf16.hip", "kda_hd_grad_fp32.hip",
+               "kda_hd_decode.hip", "kda_rotary.hip", "kda_norm.hip"]
     flags = ["-O1", "-g", "-std=c++17", "--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang",
              "-packed-fp32-ops", "-Wno-unused-command-line-argument",
              "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fno-omit-frame-pointer"]
