@@ -59,56 +59,68 @@ Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool
 struct SeqSlots { int32_t first, count; };
 
 // One workgroup: clamps cu_seqlens into [0, T] and makes it non-decreasing (a running maximum), numbers the segments.
-__global__ __launch_bounds__(1024) void kda_hd_table_kernel(const int32_t *__restrict__ cu, int32_t N, int64_t T,
-                                                            int64_t seg, int64_t slots, Segment *__restrict__ table,
+// Both are scans over the sequences, 1024 at a time: within a wavefront by lanes, over its 16 wavefronts through LDS.
+// T < 2^31, so tokens are 32-bit here.
+__global__ __launch_bounds__(1024) void kda_hd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T,
+                                                            uint32_t seg, int64_t slots, Segment *__restrict__ table,
                                                             SeqSlots *__restrict__ seqs, int64_t *__restrict__ covered) {
-    __shared__ int64_t s_max[1024];
-    __shared__ int32_t s_sum[1024];
-    const int t = threadIdx.x;
-    auto entry = [&](int64_t i) {
-        const int64_t x = cu[i];
-        return x < 0 ? 0 : x > T ? T : x;
+    __shared__ uint32_t s_max[2][16], s_sum[2][16];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    auto entry = [&](int64_t i) -> uint32_t {
+        const int32_t x = cu[i];
+        return x < 0 ? 0 : (uint32_t)x > T ? T : (uint32_t)x;
     };
-    int64_t top = entry(0);
-    int64_t first = 0;
+    uint32_t top = entry(0), first = 0;
     if (t == 0) covered[0] = top;
-    for (int64_t base = 0; base < N; base += 1024) {
+    int turn = 0;
+    for (int64_t base = 0; base < N; base += 1024, turn ^= 1) {
         const int64_t n = base + t;
-        s_max[t] = n < N ? entry(n + 1) : 0;
-        __syncthreads();
-        for (int d = 1; d < 1024; d <<= 1) {
-            const int64_t x = t >= d ? s_max[t - d] : 0;
-            __syncthreads();
-            if (x > s_max[t]) s_max[t] = x;
-            __syncthreads();
+        uint32_t end = n < N ? entry(n + 1) : 0;
+        if (end < top) end = top;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t x = __shfl_up(end, d);
+            if (lane >= d && x > end) end = x;
         }
-        const int64_t before = t > 0 && s_max[t - 1] > top ? s_max[t - 1] : top;
-        const int64_t end = s_max[t] > top ? s_max[t] : top;
-        const int64_t segs = (end - before + seg - 1) / seg;
-        const int32_t count = n < N ? (int32_t)(segs > 1 ? segs : 1) : 0;
-        s_sum[t] = count;
+        uint32_t before = __shfl_up(end, 1);
+        if (lane == 0) before = top;
+        if (lane == 63) s_max[turn][wave] = end;
         __syncthreads();
-        for (int d = 1; d < 1024; d <<= 1) {
-            const int32_t x = t >= d ? s_sum[t - d] : 0;
-            __syncthreads();
-            s_sum[t] += x;
-            __syncthreads();
+        for (int w = 0; w < 16; ++w) {
+            const uint32_t x = s_max[turn][w];
+            if (w < wave && x > end) end = x;
+            if (w < wave && x > before) before = x;
+            if (x > top) top = x;
+        }
+        const uint32_t segs = (end - before + (seg - 1)) / seg;  // under 2^32: seg <= 2^31
+        const uint32_t count = n < N ? (segs > 1 ? segs : 1) : 0;
+        uint32_t upto = count;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t x = __shfl_up(upto, d);
+            if (lane >= d) upto += x;
+        }
+        if (lane == 63) s_sum[turn][wave] = upto;
+        __syncthreads();
+        uint32_t all = 0;
+        for (int w = 0; w < 16; ++w) {
+            const uint32_t x = s_sum[turn][w];
+            if (w < wave) upto += x;
+            all += x;
         }
         if (n < N) {
-            const int64_t at = first + s_sum[t] - count;
-            seqs[n] = SeqSlots{(int32_t)at, count};
+            const uint32_t at = first + upto - count;
+            seqs[n] = SeqSlots{(int32_t)at, (int32_t)count};
             // equal parts (at most `seg`, so none is empty): workgroups of one length
-            const int64_t part = ((end - before + count - 1) / count + 63) / 64 * 64;
-            for (int32_t j = 0; j < count; ++j) {
+            const int64_t part = (int64_t)(((end - before + (count - 1)) / count + 63) / 64) * 64;
+            for (uint32_t j = 0; j < count; ++j) {
                 const int64_t a = before + j * part, e = a + part;
-                table[at + j] = Segment{(int32_t)n, j, count, 0, a, e < end ? e : end};
+                table[at + j] = Segment{(int32_t)n, (int32_t)j, (int32_t)count, 0, a, e < end ? e : (int64_t)end};
             }
         }
-        first += s_sum[1023];
-        if (s_max[1023] > top) top = s_max[1023];
-        __syncthreads();
+        first += all;
     }
-    for (int64_t i = first + t; i < slots; i += 1024) table[i] = Segment{-1, 0, 0, 0, 0, 0};
+    for (int64_t i = (int64_t)first + t; i < slots; i += 1024) table[i] = Segment{-1, 0, 0, 0, 0, 0};
     if (t == 0) covered[1] = top;
 }
 
@@ -174,21 +186,26 @@ __global__ __launch_bounds__(1024) void kda_hd_dg_kernel(const CoreArgs A, const
     if (sg.seq < 0 || sg.t1 <= sg.t0) return;
     const bool live = h < A.H;
     double behind = 0.0;
-    if (live) {
-        for (int w = 0; w < A.tiles; ++w) behind += A.border[((int64_t)w * A.slots + slot) * A.H + h];
-        if (sg.j == sg.nseg - 1 && dS) {
+    if (sg.j == sg.nseg - 1 && dS) {  // uniform: behind the last segment the final state's
+        float dot = 0.f;
+        if (live) {
             const int64_t kv4 = (int64_t)K * A.VD / 4, at = ((int64_t)sg.seq * A.H + h) * kv4;
             const f32x4 *x = reinterpret_cast<const f32x4 *>(dS) + at, *y = reinterpret_cast<const f32x4 *>(s_end) + at;
-            float dot = 0.f;
-            for (int64_t i = lane; i < kv4; i += 64) {
+#pragma unroll 4
+            for (int64_t i = blk * 64 + lane; i < kv4; i += 512) {
                 const f32x4 z = x[i] * y[i];
                 dot += (z.x + z.y) + (z.z + z.w);
             }
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
-            behind += dot;
         }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+        if (lane == 0) s_total[0][hsub][blk] = dot;
+        __syncthreads();
+        for (int w = 0; w < 8; ++w) behind += s_total[0][hsub][w];
+        __syncthreads();
     }
+    if (live)
+        for (int w = 0; w < A.tiles; ++w) behind += A.border[((int64_t)w * A.slots + slot) * A.H + h];
     const int64_t plane = (int64_t)A.H * A.ntok, steps = (sg.t1 - sg.t0 + 511) / 512;
     auto take = [&](int64_t b) {
         const int64_t t = sg.t0 + b * 512 + blk * 64 + lane, at = (int64_t)h * A.ntok + t;
@@ -313,7 +330,8 @@ Call prepare(const HdArgs &a, bool bwd) {
 }
 hipError_t make_table(const HdArgs &a, const Call &c, hipStream_t st) {
     if (!c.table) return hipSuccess;
-    hipLaunchKernelGGL(kda_hd_table_kernel, dim3(1), dim3(1024), 0, st, a.cu_seqlens, a.num_seqs, a.T, c.p.seg,
+    hipLaunchKernelGGL(kda_hd_table_kernel, dim3(1), dim3(1024), 0, st, a.cu_seqlens, a.num_seqs, (uint32_t)a.T,
+                       (uint32_t)c.p.seg,
                        c.p.slots, const_cast<Segment *>(c.table), const_cast<SeqSlots *>(c.seqs),
                        const_cast<int64_t *>(c.covered));
     return hipGetLastError();
@@ -322,6 +340,10 @@ CoreArgs base(const HdArgs &a, const Call &c) {
     CoreArgs x{};
     x.ga = x.gb = x.gc = x.gx = 1;
     x.H = a.H;
+    // Heads that share q and k go to one XCD where there are enough of them for all eight (17011 tokens of 32 heads, 4 to
+    // a row of q and k: the forward
+    // pass fetches 171 MB instead of 380, the increments 58 instead of 115).
+    x.share = c.p.slots * a.Hk >= 128 ? a.H / a.Hk : 1;
     x.g_head = a.decay_per_head;
     x.g = a.g;
     x.table = c.table;

@@ -21,6 +21,7 @@ struct CoreArgs {
     const void *a, *b, *c;      // rows [B*T, H / g?, KD | KD | VD]
     int32_t ga, gb, gc;         // heads that share a row of a, b, c
     int32_t H, VD, tiles;       // heads; columns of c and y; tiles of VT columns
+    int32_t share;              // adjacent heads whose workgroups are placed together
     void *y;                    // [B*T, H, VD]
     bool g_head;
     const void *g;              // [B*T, H] I/O type, or [H] fp32 (g_head)

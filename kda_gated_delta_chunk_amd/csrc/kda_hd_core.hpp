@@ -705,12 +705,13 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     }
 }
 
-// Workgroups of one (segment, head) sit 8 apart: the same XCD, whose L2 then holds the rows they share.
+// Workgroups of one (segment, head) sit 8 apart: the same XCD, whose L2 then holds the rows they share. So do those of
+// the heads that share rows of q and k (A.share).
 __device__ __forceinline__ bool item_of(const CoreArgs &A, int per_item, int64_t &item, int &r) {
-    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, grp = blk / (8 * per_item);
-    const int in = (int)(blk - grp * 8 * per_item);
-    item = grp * 8 + (in & 7);
-    r = in >> 3;
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, grp = blk / (8 * per_item * A.share);
+    const int in = (int)(blk - grp * 8 * per_item * A.share), head = (in >> 3) / per_item;
+    r = (in >> 3) - head * per_item;
+    item = (grp * 8 + (in & 7)) * A.share + head;
     return item < A.slots * A.H;
 }
 template <int NW> constexpr int kWavesPerSimd = NW == 8 ? 4 : 2;  // two workgroups of 8 or 4 wavefronts per CU
@@ -757,7 +758,7 @@ __global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_grad_ke
 }
 
 inline dim3 grid_of(const CoreArgs &a, int64_t per_item) {
-    return wide_grid((a.slots * a.H + 7) / 8 * 8 * per_item);
+    return wide_grid((a.slots * (a.H / a.share) + 7) / 8 * 8 * a.share * per_item);
 }
 
 }  // namespace hd
