@@ -45,9 +45,9 @@ def _cuda(t):
     return t.device
 
 
-def _workspace(workspace, need: int, what: str, dev):
+def _workspace(workspace, need: int, dev, what: str, *sizes):
     if need == 0:
-        raise KDAError(2, what)
+        raise KDAError(2, what % sizes)
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
@@ -64,10 +64,19 @@ def _no_workspace(dev):
     return _untouched[dev]
 
 
-def _result(out, name, shape, dtype, dev):
+def _result(out, name, like):
+    """The caller's tensor for a result of ``like``'s shape, dtype and device, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(out, name, shape, dtype, dev)
+        return torch.empty_like(like)
+    _need(out, name, like.shape, like.dtype, like.device)
+    return out
+
+
+def _states(out, name, S, shape, dev):
+    """The same for the states [num_seqs, H, K, V], like S where there is one."""
+    if out is None:
+        return torch.empty(shape, dtype=torch.float32, device=dev) if S is None else torch.empty_like(S)
+    _need(out, name, shape, torch.float32, dev)
     return out
 
 
@@ -137,12 +146,12 @@ def hd_chunk_fwd(q, k, v, g, S0=None, cu_seqlens=None, scale: float = 1.0, outpu
     need = lib.kda_hd_chunk_fwd_workspace_bytes(B, T, H, Hk, K, V, N, int(cu_seqlens is not None), io)
     if workspace is None and need == 256:
         workspace = _no_workspace(dev)
-    workspace = _workspace(workspace, need, "hd_chunk_fwd(B=%d, T=%d, H=%d, Hk=%d, K=%d, V=%d, num_seqs=%d)"
-                           % (B, T, H, Hk, K, V, N), dev)
-    out = _result(out, "out", (B, T, H, V), dt, dev)
+    workspace = _workspace(workspace, need, dev, "hd_chunk_fwd(B=%d, T=%d, H=%d, Hk=%d, K=%d, V=%d, num_seqs=%d)",
+                           B, T, H, Hk, K, V, N)
+    out = _result(out, "out", v)
     S = None
     if final_state_out is not None or output_final_state:
-        S = _result(final_state_out, "final_state_out", (N, H, K, V), torch.float32, dev)
+        S = _states(final_state_out, "final_state_out", S0, (N, H, K, V), dev)
     _call(dev, lib.kda_hd_chunk_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens), B, T, H, Hk, K, V,
           N, io, decay, scale, _ptr(out), _ptr(S), _ptr(workspace), workspace.numel())
     return out, S
@@ -166,19 +175,19 @@ def hd_chunk_bwd(q, k, v, g, do, S0=None, dS_final=None, cu_seqlens=None, scale:
     for name, t in (("S0", S0), ("dS_final", dS_final)):
         if t is not None:
             _need(t, name, (N, H, K, V), torch.float32, dev)
-    shapes = {"dq": (q.shape, dt), "dk": (k.shape, dt), "dv": (v.shape, dt)}
+    like = {"dq": q, "dk": k, "dv": v}
     if want_dg and decay == _lib.KDA_DECAY_PER_TOKEN:
-        shapes["dg"] = (g.shape, dt)
-    if want_dS0:
-        shapes["dS0"] = ((N, H, K, V), torch.float32)
+        like["dg"] = g
     given = out or {}
     for name in given:
-        if name not in shapes:
+        if name not in like and not (name == "dS0" and want_dS0):
             raise ValueError("out[%r]: not a result of this call" % (name,))
     need = lib.kda_hd_chunk_bwd_workspace_bytes(B, T, H, Hk, K, V, N, int(cu_seqlens is not None), io)
-    workspace = _workspace(workspace, need, "hd_chunk_bwd(B=%d, T=%d, H=%d, Hk=%d, K=%d, V=%d, num_seqs=%d)"
-                           % (B, T, H, Hk, K, V, N), dev)
-    res = {n: _result(given.get(n), "out[%r]" % n, s, d, dev) for n, (s, d) in shapes.items()}
+    workspace = _workspace(workspace, need, dev, "hd_chunk_bwd(B=%d, T=%d, H=%d, Hk=%d, K=%d, V=%d, num_seqs=%d)",
+                           B, T, H, Hk, K, V, N)
+    res = {n: _result(given.get(n), n, t) for n, t in like.items()}
+    if want_dS0:
+        res["dS0"] = _states(given.get("dS0"), "dS0", S0 if S0 is not None else dS_final, (N, H, K, V), dev)
     _call(dev, lib.kda_hd_chunk_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens), _ptr(do),
           _ptr(dS_final), B, T, H, Hk, K, V, N, io, decay, scale, _ptr(res["dq"]), _ptr(res["dk"]), _ptr(res["dv"]),
           _ptr(res.get("dg")), _ptr(res.get("dS0")), _ptr(workspace), workspace.numel())
@@ -196,7 +205,7 @@ def hd_decode_step(q, k, v, g, S, scale: float = 1.0, out=None):
     H, Hk, K, V, dt, decay = _hd_inputs(q, k, v, g, (N,))
     io = _io_code(dt)
     _need(S, "S", (N, H, K, V), torch.float32, dev)
-    out = _result(out, "out", (N, H, V), dt, dev)
+    out = _result(out, "out", v)
     _call(dev, lib.kda_hd_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(out), N, H, Hk, K, V, io,
           decay, scale)
     return out
@@ -255,12 +264,12 @@ def rotary(q, freqs, k=None, positions=None, layout: str = "half", inverse: bool
     if k is not None:
         Hk = k.shape[-2] if k.dim() == q.dim() else -1
         _need(k, "k", lead + (Hk, D), dt, dev)
-        k_out = _result(k_out, "k_out", k.shape, dt, dev)
+        k_out = _result(k_out, "k_out", k)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if positions is not None:
         _need(positions, "positions", lead, torch.int32, dev)
-    out = _result(out, "out", q.shape, dt, dev)
+    out = _result(out, "out", q)
     _call(dev, lib.kda_rotary, _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), _ptr(out), _ptr(k_out),
           math.prod(lead), lead[-1], Hq, Hk, D, 2 * freqs.numel(), io, _lib.ROTARY_LAYOUTS[layout], int(bool(inverse)),
           scale)
@@ -299,7 +308,7 @@ def layer_norm_fwd(x, weight=None, bias=None, o_gate=None, eps: float = 1e-5, ce
     io = _io_code(x.dtype)
     rows, groups, C = _norm_args(x, weight, bias, o_gate)
     dev = x.device
-    out = _result(out, "out", x.shape, x.dtype, dev)
+    out = _result(out, "out", x)
     _call(dev, lib.kda_layer_norm_fwd, _ptr(x), _ptr(weight), _ptr(bias), _ptr(o_gate), _ptr(out), rows, groups, C, eps,
           int(bool(center)), io)
     return out
@@ -315,20 +324,20 @@ def layer_norm_bwd(dy, x, weight=None, bias=None, o_gate=None, eps: float = 1e-5
     rows, groups, C = _norm_args(x, weight, bias, o_gate)
     dev, dt = x.device, x.dtype
     _need(dy, "dy", x.shape, dt, dev)
-    shapes = {"dx": (x.shape, dt)}
+    like = {"dx": x}
     if weight is not None:
-        shapes["dweight"] = (weight.shape, torch.float32)
+        like["dweight"] = weight
     if bias is not None:
-        shapes["dbias"] = (bias.shape, torch.float32)
+        like["dbias"] = bias
     if o_gate is not None:
-        shapes["do_gate"] = (x.shape, dt)
+        like["do_gate"] = o_gate
     given = out or {}
     for name in given:
-        if name not in shapes:
+        if name not in like:
             raise ValueError("out[%r]: not a result of this call" % (name,))
-    workspace = _workspace(workspace, lib.kda_layer_norm_bwd_workspace_bytes(rows, groups, C),
-                           "layer_norm_bwd(rows=%d, groups=%d, C=%d)" % (rows, groups, C), dev)
-    res = {n: _result(given.get(n), "out[%r]" % n, s, d, dev) for n, (s, d) in shapes.items()}
+    workspace = _workspace(workspace, lib.kda_layer_norm_bwd_workspace_bytes(rows, groups, C), dev,
+                           "layer_norm_bwd(rows=%d, groups=%d, C=%d)", rows, groups, C)
+    res = {n: _result(given.get(n), n, t) for n, t in like.items()}
     _call(dev, lib.kda_layer_norm_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(o_gate), _ptr(res["dx"]),
           _ptr(res.get("dweight")), _ptr(res.get("dbias")), _ptr(res.get("do_gate")), rows, groups, C, eps,
           int(bool(center)), io, _ptr(workspace), workspace.numel())
