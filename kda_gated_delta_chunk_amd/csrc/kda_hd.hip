@@ -14,12 +14,18 @@ namespace hd {
 namespace {
 
 constexpr int64_t kLeastSegment = 256;
+// Up to this many segments a sequence, a workgroup of the forward pass reads what the segments before its own add and
+// forms the state that it starts from (4096 tokens of 96 heads, 5 segments: 157 -> 150 us). With more that would be too
+// many reads, half the segments' states on average, and a pass of its own carries the states over them first. So it
+// does for the gradients: two of the three read a state transposed, in pieces of 4 bytes, and took 370 -> 424 us.
+constexpr int32_t kFold = 8;
 
 struct Plan {
     int64_t seg;        // tokens per segment
     int32_t nseg;       // segments per row (not packed)
     int64_t slots;      // workgroups' slots: an upper bound when packed
     bool several;       // some sequence may have more than one segment
+    bool fold;          // workgroups form the states they start from themselves
 };
 
 int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
@@ -52,6 +58,7 @@ Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool
     p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
     p.slots = packed ? T / p.seg + N : B * p.nseg;
     p.several = p.nseg > 1;
+    p.fold = !bwd && p.nseg <= kFold;
     return p;
 }
 
@@ -352,6 +359,7 @@ CoreArgs base(const HdArgs &a, const Call &c) {
     x.seg = c.p.seg;
     x.ntok = a.B * a.T;
     x.nseg = c.p.nseg;
+    x.fold = c.p.fold;
     x.s_intra = x.s_inter = x.s_up = 1.f;
     x.sr = a.V;
     x.sc = 1;
@@ -376,6 +384,7 @@ hipError_t segment_states(const HdArgs &a, const Call &c, bool bwd, hipStream_t 
     const CarryArgs cf{f.s_inc, f.seg_decay, a.S0};
     if (!bwd) {
         KDA_TRY(inc_pass(a.io_bf16, f, nullptr, a.K, inc_tile(a.V), st));
+        if (c.p.fold) return hipSuccess;
         return launch_carry(cf, nullptr, c.seqs, c.p, a, st);
     }
     const CoreArgs r = increments(a, c, true);
@@ -413,6 +422,7 @@ hipError_t launch_hd_fwd(const HdArgs &a, hipStream_t st) {
     x.y = a.o;
     x.s_init = a.S0;
     x.s_seg = reinterpret_cast<const float *>(c.ws + c.l.seg);
+    x.seg_decay = reinterpret_cast<float *>(c.ws + c.l.decay);
     x.s_out = a.S_final;
     x.s_intra = x.s_inter = a.scale;
     return fwd_pass(a.io_bf16, x, a.K, vt, st);

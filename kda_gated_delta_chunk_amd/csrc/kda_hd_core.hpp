@@ -296,19 +296,23 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) st[kt][ct] = zero4();
-    if (!INC) {
-        const bool first = REV ? sg.j == sg.nseg - 1 : sg.j == 0;
-        const float *s0 = first ? (A.s_init ? A.s_init + nh * sstate : nullptr)
-                                : A.s_seg + (slot * A.H + h) * sstate;
-        if (s0) {
+    if constexpr (!INC) {
+        auto add_state = [&](float d, const float *p) __attribute__((always_inline)) {  // st <- d st + the state at p
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        st[kt][ct][i] = s0[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc];
-        }
+                        st[kt][ct][i] = fmaf(st[kt][ct][i], d,
+                                             p[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc]);
+        };
+        const bool first = REV ? sg.j == sg.nseg - 1 : sg.j == 0;
+        if (!first && !A.fold) add_state(0.f, A.s_seg + (slot * A.H + h) * sstate);
+        else if (A.s_init) add_state(0.f, A.s_init + nh * sstate);
+        if (A.fold)  // forward in time only
+            for (int64_t at = (slot - sg.j) * A.H + h; at < slot * A.H; at += A.H)
+                add_state(__builtin_amdgcn_exp2f(A.seg_decay[at]), A.s_seg + at * sstate);
     }
     mfma_fence_state(st);  // the loads end here: a wait for them inside the loop would hold up the rows under way
     // ---- what the border behind the segment passes on to its log-decays: <state gradient, state> there. (Behind the

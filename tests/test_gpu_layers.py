@@ -137,9 +137,9 @@ def test_hd_without_states(io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
-@pytest.mark.parametrize("T", [600, 1537])
+@pytest.mark.parametrize("T", [600, 1537, 4100, 9000])
 def test_hd_segments(io, T):
-    """One head over many tokens runs as segments: the same results."""
+    """One head over many tokens runs as segments, few or many: the same results."""
     x = hd_inputs(1, T, 1, 1, 64, 64, io, 11)
     o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"])
     check_fwd(x, o, S)
