@@ -361,8 +361,6 @@ CoreArgs base(const HdArgs &a, const Call &c) {
     x.nseg = c.p.nseg;
     x.fold = c.p.fold;
     x.s_intra = x.s_inter = x.s_up = 1.f;
-    x.sr = a.V;
-    x.sc = 1;
     x.VD = a.V;
     return x;
 }
@@ -465,8 +463,6 @@ hipError_t launch_hd_bwd(const HdArgs &a, hipStream_t st) {
     g.dk.gc = group;
     g.dk.VD = a.K;
     g.dk.tiles = a.K / gt;
-    g.dk.sr = 1;
-    g.dk.sc = a.V;
     g.dk.y = dk;
     g.dk.s_init = a.dS_final;
     g.dk.s_seg = dseg;
@@ -479,8 +475,6 @@ hipError_t launch_hd_bwd(const HdArgs &a, hipStream_t st) {
     g.dq.gc = group;
     g.dq.VD = a.K;
     g.dq.tiles = a.K / gt;
-    g.dq.sr = 1;
-    g.dq.sc = a.V;
     g.dq.y = dq;
     g.dq.s_init = a.S0;
     g.dq.s_seg = seg;

@@ -31,7 +31,6 @@ struct CoreArgs {
     float *s_out;               // state after the last segment (REV: before the first), or null
     float *s_inc;               // what a segment adds (the increment passes), per slot and head
     float *seg_decay;           // log2 of a segment's decay, per slot and head
-    int64_t sr, sc;             // strides of a state's rows and columns
     const Segment *table;       // or null: rows of T tokens
     int64_t slots, T, seg, ntok;
     int32_t nseg;

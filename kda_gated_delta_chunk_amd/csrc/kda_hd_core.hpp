@@ -251,8 +251,9 @@ struct Lds {
     static constexpr int red = u + (DG ? NW * C * 4 : 0), bytes = red + NW * 4;
 };
 
-// One (segment, head), column tile vt; NW * 64 threads, Lds::bytes of LDS.
-template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG, bool YF>
+// One (segment, head), column tile vt; NW * 64 threads, Lds::bytes of LDS. TS: states are stored by columns (KD adjacent
+// rows), else by rows (VD adjacent columns).
+template <bool BF, int KD, int VT, int NW, bool REV, bool INC, bool DG, bool YF, bool TS>
 __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int vt, char *smem) {
     using L = Lds<BF, KD, VT, NW, INC, DG>;
     constexpr int NT = NW * 64, CT = VT / (16 * NW), KT = KD / 16, KC = KD / 32;
@@ -296,16 +297,33 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) st[kt][ct] = zero4();
+    // where a lane's first entry of a state tile lies in a state, in bytes, and its four entries
+    const uint32_t vd4 = 4 * (uint32_t)A.VD;
+    auto state_at = [&](int lane, int kt, int ct) __attribute__((always_inline)) {
+        const uint32_t r = RK::state_row(kt, lane >> 4), c = col0 + 16 * ct + (lane & 15);
+        return TS ? (c * KD + r) * 4u : r * vd4 + c * 4u;
+    };
+    auto get_state = [&](const float *state, int lane, int kt, int ct) __attribute__((always_inline)) -> f32x4 {
+        const char *p = reinterpret_cast<const char *>(state);
+        const uint32_t at = state_at(lane, kt, ct);
+        if constexpr (TS) return *reinterpret_cast<const f32x4 *>(p + at);
+        f32x4 x;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float *>(p + (at + i * vd4));
+        return x;
+    };
     if constexpr (!INC) {
         auto add_state = [&](float d, const float *p) __attribute__((always_inline)) {  // st <- d st + the state at p
+            int at = lane;
+            asm volatile("" : "+v"(at));  // no addresses kept over the loop below
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x4 x = get_state(p, at, kt, ct);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        st[kt][ct][i] = fmaf(st[kt][ct][i], d,
-                                             p[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc]);
+                    for (int i = 0; i < 4; ++i) st[kt][ct][i] = fmaf(st[kt][ct][i], d, x[i]);
+                }
         };
         const bool first = REV ? sg.j == sg.nseg - 1 : sg.j == 0;
         if (!first && !A.fold) add_state(0.f, A.s_seg + (slot * A.H + h) * sstate);
@@ -324,11 +342,11 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x4 x = get_state(se, lane, kt, ct);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dot += st[kt][ct][i] * se[(int64_t)(RK::state_row(kt, g) + i) * A.sr +
-                                                  (int64_t)(col0 + 16 * ct + li) * A.sc];
+                    for (int i = 0; i < 4; ++i) dot += st[kt][ct][i] * x[i];
+                }
         }
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
@@ -694,13 +712,20 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     if (INC) so = A.s_inc + (slot * A.H + h) * sstate;
     else if (REV ? sg.j == 0 : sg.j == sg.nseg - 1) so = A.s_out ? A.s_out + nh * sstate : nullptr;
     if (so) {
+        int lane = lane0;
+        asm volatile("" : "+v"(lane));  // no address of the loop's other end is kept over it
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int ct = 0; ct < CT; ++ct) {
+                char *p = reinterpret_cast<char *>(so);
+                const uint32_t at = state_at(lane, kt, ct);
+                if constexpr (TS)
+                    *reinterpret_cast<f32x4 *>(p + at) = st[kt][ct];
+                else
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    so[(int64_t)(RK::state_row(kt, g) + i) * A.sr + (int64_t)(col0 + 16 * ct + li) * A.sc] = st[kt][ct][i];
+                    for (uint32_t i = 0; i < 4; ++i) *reinterpret_cast<float *>(p + (at + i * vd4)) = st[kt][ct][i];
+            }
     }
     if constexpr (INC) {  // the segment's whole decay: the wavefronts' sums
         btot = lane_value(btot, 0) + lane_value(btot, 32);
@@ -731,7 +756,7 @@ __global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_fwd_ker
     int64_t item;
     int r;
     if (!item_of(A, A.tiles, item, r)) return;
-    chunk_pass<BF, KD, VT, VT / 16, false, false, false, false>(A, item, r, smem);
+    chunk_pass<BF, KD, VT, VT / 16, false, false, false, false, false>(A, item, r, smem);
 }
 // The increments of the states (and, from workgroup tiles on, of their gradients).
 template <bool BF, int KD, int VT>
@@ -741,9 +766,9 @@ __global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_inc_ker
     int r;
     if (!item_of(F, both ? 2 * F.tiles : F.tiles, item, r)) return;
     if (r < F.tiles)
-        chunk_pass<BF, KD, VT, VT / 16, false, true, false, false>(F, item, r, smem);
+        chunk_pass<BF, KD, VT, VT / 16, false, true, false, false, false>(F, item, r, smem);
     else
-        chunk_pass<BF, KD, VT, VT / 16, true, true, false, false>(R, item, r - F.tiles, smem);
+        chunk_pass<BF, KD, VT, VT / 16, true, true, false, false, false>(R, item, r - F.tiles, smem);
 }
 // The three gradients of a (segment, head) as workgroups of one launch: dv and dk walk back through the same rows side
 // by side (what one fetches the other finds in L2), dq walks forward.
@@ -756,14 +781,14 @@ __global__ __launch_bounds__(VT * 4, kWavesPerSimd<VT / 16>) void kda_hd_grad_ke
     int r;
     if (!item_of(G.dv, G.dv.tiles + 2 * G.dk.tiles, item, r)) return;
     if (r < G.dv.tiles) {
-        chunk_pass<BF, K, VT, NW, true, false, DG, false>(G.dv, item, r, smem);
+        chunk_pass<BF, K, VT, NW, true, false, DG, false, false>(G.dv, item, r, smem);
         return;
     }
     r -= G.dv.tiles;
     if (r < G.dk.tiles)
-        chunk_pass<BF, V, VT, NW, true, false, false, YF>(G.dk, item, r, smem);
+        chunk_pass<BF, V, VT, NW, true, false, false, YF, true>(G.dk, item, r, smem);
     else
-        chunk_pass<BF, V, VT, NW, false, false, DG, YF>(G.dq, item, r - G.dk.tiles, smem);
+        chunk_pass<BF, V, VT, NW, false, false, DG, YF, true>(G.dq, item, r - G.dk.tiles, smem);
 }
 
 inline dim3 grid_of(const CoreArgs &a, int64_t per_item) {
