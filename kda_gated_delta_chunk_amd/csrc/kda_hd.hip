@@ -17,7 +17,7 @@ constexpr int64_t kLeastSegment = 256;
 // Up to this many segments a sequence, a workgroup of the forward pass reads what the segments before its own add and
 // forms the state that it starts from (4096 tokens of 96 heads, 5 segments: 157 -> 150 us). With more that would be too
 // many reads, half the segments' states on average, and a pass of its own carries the states over them first. So it
-// does for the gradients: two of the three read a state transposed, in pieces of 4 bytes, and took 370 -> 424 us.
+// does for the gradients, where three workgroups would form each state (478 us either way).
 constexpr int32_t kFold = 8;
 
 struct Plan {
