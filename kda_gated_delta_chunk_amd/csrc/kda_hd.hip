@@ -7,13 +7,15 @@
 // the other end.
 #include "kda_hd.hpp"
 
+#include <cmath>
+
 #include "kda_common.hpp"
 
 namespace kda {
 namespace hd {
 namespace {
 
-constexpr int64_t kLeastSegment = 256;
+constexpr int64_t kLeastSegment = 128;
 // Up to this many segments a sequence, a workgroup of the forward pass reads what the segments before its own add and
 // forms the state that it starts from (4096 tokens of 96 heads, 5 segments: 157 -> 150 us). With more that would be too
 // many reads, half the segments' states on average, and a pass of its own carries the states over them first. So it
@@ -42,21 +44,62 @@ int64_t cost(int64_t rows, int64_t inc_rows, int64_t heads, int64_t resident, in
     return c;
 }
 
+// The same for N packed sequences of T tokens in all, whose lengths the host does not know. They are taken for what N - 1
+// random cuts make of T: the longest is ln N + 0.6 times the average, N / (1 - e^(-seg / average)) segments of at most
+// `seg` tokens. A workgroup's token takes `alone` ns where it has a CU to itself, and the longest segment that many; all
+// together take what the chip's CUs can do. `scale`: percent of the times measured at K = V = 128 in bf16. Against a model
+// that takes one sequence for nearly all of the batch: 1531 tokens of 5 sequences, 12 heads, fp32: gradients 99 -> 81 us;
+// 6000 of 3, 8 heads, fp32: forward 115 -> 86; 50000 of 64, 96 heads: 1363 -> 1303; 8000 of 5, 32 heads: 130 -> 117.
+int64_t packed_cost(int64_t T, int64_t N, int64_t H, int64_t tiles, int64_t inc_tiles, int64_t resident, int64_t seg,
+                    int64_t longest, int64_t scale, int64_t state, bool bwd) {
+    const int64_t segs = seg < longest ? (int64_t)(N / (1.0 - std::exp(-(double)seg * N / (T > 0 ? T : 1)))) : N;
+    const int64_t groups = H * tiles * segs;
+    const int64_t alone = (bwd ? 100 : 62) * scale / 100, shared = (bwd ? 160 : 110) * scale / 100;
+    const int64_t more = groups <= 256 ? 0 : groups < resident ? groups - 256 : resident - 256;  // that share a CU
+    const int64_t lone = seg * (alone + (shared - alone) * more / (resident - 256));
+    const int64_t all = H * tiles * T / 256 * shared / 2 + (groups > resident ? lone / 4 : 0);
+    int64_t c = lone > all ? lone : all;
+    if (segs > N) {  // increments of all but the last segments
+        const int64_t one = seg * 40, inc = (int64_t)((double)(H * inc_tiles * T / 256) * (segs - N) / segs * 20);
+        c += (one > inc ? one : inc) * scale / 100 + H * segs * (bwd ? 100 : 50) * state / 16384 + 12000;
+    }
+    return c;
+}
+
 Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool packed, bool bf16, bool bwd) {
     Plan p;
     const int64_t whole = round64(T > 0 ? T : 1);
-    // workgroups of one segment per row (packed: one sequence may be nearly all of the batch)
     const int vt = bwd ? grad_tile(K, V, bf16) : fwd_tile(V, bf16);
-    const int64_t heads = (packed ? 1 : B) * H, rows = heads * (bwd ? 2 * (K / vt) + V / vt : V / vt);
-    const int64_t inc_rows = heads * (V / inc_tile(V)) * (bwd ? 2 : 1), resident = vt == 128 || bwd ? 512 : 768;
-    int64_t best = 1, least = cost(rows, inc_rows, heads, resident, whole, 1, bwd);
-    for (int64_t n = 2; n <= whole / kLeastSegment && rows * (n - 1) < 4 * resident; ++n) {
-        const int64_t c = cost(rows, inc_rows, heads, resident, whole, n, bwd);
-        if (c < least) best = n, least = c;
+    const int64_t tiles = bwd ? 2 * (K / vt) + V / vt : V / vt, inc_tiles = V / inc_tile(V) * (bwd ? 2 : 1);
+    const int64_t resident = vt == 128 || bwd ? 512 : 768;
+    if (packed) {
+        // A batch that needs no segments still gets them, at the longest length to be expected or as much as one workgroup
+        // does while the chip does all of the batch: one long sequence among short ones would otherwise run on alone (a
+        // launch that finds nothing costs 2 to 7%).
+        const int64_t likely = round64((int64_t)((std::log((double)N) + 0.6) * T / N) + 1);
+        const int64_t longest = N > 1 && likely < whole ? likely : whole;
+        const int64_t scale = bf16 ? (vt == 128 ? 100 : 75) : 180 * (bwd && V > K ? V : K) / 128;
+        const int64_t meanwhile = H * tiles * T / 256 * 4 / 5;
+        p.seg = round64(meanwhile > longest ? (meanwhile < whole ? meanwhile : whole) : longest);
+        int64_t least = packed_cost(T, N, H, tiles, inc_tiles, resident, longest, longest, scale, (int64_t)K * V, bwd);
+        for (int64_t n = 2; longest / n >= kLeastSegment && H * tiles * n < 4 * resident; ++n) {
+            const int64_t seg = round64((longest + n - 1) / n);
+            const int64_t c = packed_cost(T, N, H, tiles, inc_tiles, resident, seg, longest, scale, (int64_t)K * V, bwd);
+            if (c < least) p.seg = seg, least = c;
+        }
+        p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
+        p.slots = T / p.seg + N;
+    } else {
+        const int64_t heads = B * H, rows = heads * tiles;
+        int64_t best = 1, least = cost(rows, heads * inc_tiles, heads, resident, whole, 1, bwd);
+        for (int64_t n = 2; n <= whole / kLeastSegment && rows * (n - 1) < 4 * resident; ++n) {
+            const int64_t c = cost(rows, heads * inc_tiles, heads, resident, whole, n, bwd);
+            if (c < least) best = n, least = c;
+        }
+        p.seg = round64((whole + best - 1) / best);
+        p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
+        p.slots = B * p.nseg;
     }
-    p.seg = round64((whole + best - 1) / best);
-    p.nseg = (int32_t)(T > 0 ? (T + p.seg - 1) / p.seg : 1);
-    p.slots = packed ? T / p.seg + N : B * p.nseg;
     p.several = p.nseg > 1;
     p.fold = !bwd && p.nseg <= kFold;
     return p;

@@ -68,8 +68,8 @@ kda_status_t check_hd_sizes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t
     // a chunk's rows of all heads (32 tokens) stay below 2^31 bytes, the kernels' offsets within it; heads and states
     // are 32-bit
     if (H >= (1 << 16) || (int64_t)num_seqs * H >= ((int64_t)1 << 26)) return KDA_ERROR_INVALID_VALUE;
-    // workgroups of a pass (at most 9 for each head of a segment, at least 256 tokens or a sequence) stay below 2^32
-    if ((B * ((T + 255) / 256) + num_seqs) > ((int64_t)1 << 27) / H) return KDA_ERROR_INVALID_VALUE;
+    // workgroups of a pass (at most 9 for each head of a segment, at least 128 tokens or a sequence) stay below 2^32
+    if ((B * ((T + 127) / 128) + num_seqs) > ((int64_t)1 << 27) / H) return KDA_ERROR_INVALID_VALUE;
     return KDA_SUCCESS;
 }
 
