@@ -29,10 +29,11 @@
 // products, one barrier, the state's products) follow each other, so what bounds it is their latency and the vector
 // instructions that convert, scale and address, with two workgroups of 8 wavefronts a CU to hide behind one another.
 // 4096 tokens of 96 heads: 97 us in the forward kernel (87 without the state's update, 94 without the rows' loads, 24
-// without both and the products), 49 us in the increments, 9 us in carrying them; 372 us in the gradients' kernel. What
+// without both and the products), 48 us in the increments; 360 us in the gradients' kernel. What
 // brought it there from 427 us of simple kernels: rows one chunk ahead (271), fewer exponentials (249), chunks of 32
 // tokens on 128 columns (198), zero weights in place of cleared rows (180), 8 wavefronts and addresses made anew (174),
-// decays made 16 chunks at a time (162), stores without branches and 16-byte operand reads (156).
+// decays made 16 chunks at a time (162), stores without branches and 16-byte operand reads (156), segments' states formed
+// by the workgroups that start from them (150).
 #pragma once
 
 #include "kda_common.hpp"

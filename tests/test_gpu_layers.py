@@ -348,6 +348,24 @@ def test_hd_long_offsets():
         assert float(d.max()) < 1e-5 * float(S1.abs().max())
 
 
+def test_hd_gradients_at_long_offsets():
+    """The same for the gradients: they equal those of the last sequences alone."""
+    H, K = 96, 128
+    T = (1 << 31) // (H * K) + 5000
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v, do = [torch.empty((1, T, H, K), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(4)]
+    g = -torch.rand((1, T, H), device="cuda", generator=gen).to(torch.bfloat16)
+    cu = torch.tensor([0, T - 4096, T - 77, T], dtype=torch.int32, device="cuda")
+    r = kda.hd_chunk_bwd(q, k, v, g, do, cu_seqlens=cu, scale=0.1)
+    for n, (a, b) in enumerate([(T - 4096, T - 77), (T - 77, T)]):
+        r1 = kda.hd_chunk_bwd(*[t[:, a:b].contiguous() for t in (q, k, v, g, do)], scale=0.1)
+        for name in ("dq", "dk", "dv"):
+            x, y = r[name][:, a:b].float(), r1[name].float()
+            assert float(((x - y).abs() / (y.abs() + y.abs().mean())).max()) < 2.0 ** -6, name
+        d = (r["dS0"][n + 1] - r1["dS0"][0]).abs()
+        assert float(d.max()) < 1e-5 * float(r1["dS0"].abs().max())
+
+
 def test_hd_refusals():
     x = hd_inputs(1, 8, 4, 2, 32, 32, "bf16", 91)
     q, k, v, g = (x[n] for n in ("q", "k", "v", "g"))
@@ -370,6 +388,13 @@ def test_hd_refusals():
     many = [torch.zeros(1, 1, 1 << 16, 32, device="cuda") for _ in range(3)]
     with pytest.raises(kda.KDAError):
         kda.hd_chunk_fwd(*many, torch.zeros(1, 1, 1 << 16, device="cuda"))
+    off = torch.zeros(q.numel() + 1, device="cuda", dtype=q.dtype)[1:].view(q.shape)  # 2 bytes behind a 16-byte border
+    with pytest.raises(kda.KDAError):
+        kda.hd_chunk_fwd(off, k, v, g)
+    with pytest.raises(kda.KDAError):
+        kda.rotary(off, kda.rotary_freqs(32))
+    with pytest.raises(kda.KDAError):
+        kda.layer_norm_fwd(off)
     S = torch.zeros(8, 4, 32, 32, device="cuda")
     with pytest.raises(ValueError):
         kda.hd_decode_step(q[0], k[0], v[0], g[0], S[:7])
