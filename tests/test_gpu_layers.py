@@ -483,7 +483,8 @@ NORMS = [((1, 1), 1), ((7, 3), 1), ((5, 16), 0), ((33, 64), 1), ((9, 100), 1), (
          ((2, 8192), 1), ((2, 16384), 1), ((3, 9999), 1), ((300, 3, 24), 2), ((1500, 128), 1),
          # more rows than the backward's grid takes at a time: groups that divide a workgroup's rows and that do not
          ((20000, 17), 1), ((9000, 4, 40), 2), ((9000, 3, 128), 2), ((700, 64, 32), 2), ((5000, 2, 300), 2),
-         ((1030, 5, 300), 2), ((1100, 2500), 1), ((650, 5001), 1), ((520, 8200), 1), ((515, 9001), 1)]
+         ((1030, 5, 300), 2), ((1100, 2500), 1), ((650, 5001), 1), ((520, 8200), 1), ((515, 9001), 1),
+         ((5000, 200), 1), ((4300, 3, 136), 2), ((2000, 513), 1), ((1100, 2, 1024), 2), ((700, 3, 640), 2)]
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
