@@ -16,10 +16,10 @@ namespace hd {
 namespace {
 
 constexpr int64_t kLeastSegment = 128;
-// Up to this many segments a sequence, a workgroup of the forward pass reads what the segments before its own add and
-// forms the state that it starts from (4096 tokens of 96 heads, 5 segments: 157 -> 150 us). With more that would be too
-// many reads, half the segments' states on average, and a pass of its own carries the states over them first. So it
-// does for the gradients, where three workgroups would form each state (478 us either way).
+// Where a sequence has up to this many segments, a workgroup of the forward pass reads what the segments before its own
+// add and forms the state that it starts from (4096 tokens of 96 heads, 5 segments: 157 -> 150 us). With more that would
+// be too many reads, half the segments' states on average, and a pass of its own carries the states over them first. So
+// it does for the gradients, where three workgroups would form each state (478 us either way).
 constexpr int32_t kFold = 8;
 
 struct Plan {
@@ -27,7 +27,7 @@ struct Plan {
     int32_t nseg;       // segments per row (not packed)
     int64_t slots;      // workgroups' slots: an upper bound when packed
     bool several;       // some sequence may have more than one segment
-    bool fold;          // workgroups form the states they start from themselves
+    int32_t fold;       // sequences of up to so many segments: workgroups form the states they start from themselves
 };
 
 int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
@@ -101,7 +101,7 @@ Plan plan(int64_t B, int64_t T, int32_t H, int32_t K, int32_t V, int32_t N, bool
         p.slots = B * p.nseg;
     }
     p.several = p.nseg > 1;
-    p.fold = !bwd && p.nseg <= kFold;
+    p.fold = bwd ? 0 : kFold;
     return p;
 }
 
@@ -180,10 +180,10 @@ struct CarryArgs {
     const float *decay, *init;
 };
 // In place: what each segment adds becomes the state it starts from (rev: the state gradient it ends with). A thread
-// carries four adjacent state entries over the segments of its sequence.
+// carries four adjacent state entries over the segments of its sequence, if they are more than `fold`.
 __global__ __launch_bounds__(256) void kda_hd_carry_kernel(const CarryArgs F, const CarryArgs R,
                                                            const SeqSlots *__restrict__ seqs, int32_t N, int32_t nseg,
-                                                           int32_t H, int64_t kv4) {
+                                                           int32_t fold, int32_t H, int64_t kv4) {
     const int rev = blockIdx.z;
     float *seg = rev ? R.seg : F.seg;
     const float *decay = rev ? R.decay : F.decay, *init = rev ? R.init : F.init;
@@ -193,6 +193,7 @@ __global__ __launch_bounds__(256) void kda_hd_carry_kernel(const CarryArgs F, co
     if (e >= kv4 || n >= N) return;
     const int h = (int)(nh - n * H);
     const int32_t first = seqs ? seqs[n].first : (int32_t)(n * nseg), count = seqs ? seqs[n].count : nseg;
+    if (count <= fold) return;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (init) s = reinterpret_cast<const f32x4 *>(init)[nh * kv4 + e];
 #pragma unroll 4
@@ -215,7 +216,8 @@ hipError_t launch_carry(const CarryArgs &f, const CarryArgs *r, const SeqSlots *
     const int64_t kv4 = (int64_t)a.K * a.V / 4, nh = (int64_t)a.num_seqs * a.H;
     dim3 grid = wide_grid(nh * ((kv4 + 255) / 256));
     if (r) grid.z = 2;
-    hipLaunchKernelGGL(kda_hd_carry_kernel, grid, dim3(256), 0, st, f, r ? *r : f, seqs, a.num_seqs, p.nseg, a.H, kv4);
+    hipLaunchKernelGGL(kda_hd_carry_kernel, grid, dim3(256), 0, st, f, r ? *r : f, seqs, a.num_seqs, p.nseg, p.fold, a.H,
+                       kv4);
     return hipGetLastError();
 }
 
@@ -425,7 +427,7 @@ hipError_t segment_states(const HdArgs &a, const Call &c, bool bwd, hipStream_t 
     const CarryArgs cf{f.s_inc, f.seg_decay, a.S0};
     if (!bwd) {
         KDA_TRY(inc_pass(a.io_bf16, f, nullptr, a.K, inc_tile(a.V), st));
-        if (c.p.fold) return hipSuccess;
+        if (c.p.nseg <= c.p.fold) return hipSuccess;
         return launch_carry(cf, nullptr, c.seqs, c.p, a, st);
     }
     const CoreArgs r = increments(a, c, true);

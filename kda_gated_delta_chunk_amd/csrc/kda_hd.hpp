@@ -26,8 +26,8 @@ struct CoreArgs {
     bool g_head;
     const void *g;              // [B*T, H] I/O type, or [H] fp32 (g_head)
     const float *s_init;        // state before the first segment (REV: after the last), or null
-    const float *s_seg;         // states the other segments start from, per slot and head; fold: what each adds
-    bool fold;
+    const float *s_seg;         // states the other segments start from, per slot and head; of sequences of up to `fold`
+    int32_t fold;               //   segments: what each adds
     float *s_out;               // state after the last segment (REV: before the first), or null
     float *s_inc;               // what a segment adds (the increment passes), per slot and head
     float *seg_decay;           // log2 of a segment's decay, per slot and head

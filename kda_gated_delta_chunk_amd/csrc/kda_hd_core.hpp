@@ -327,9 +327,10 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
                 }
         };
         const bool first = REV ? sg.j == sg.nseg - 1 : sg.j == 0;
-        if (!first && !A.fold) add_state(0.f, A.s_seg + (slot * A.H + h) * sstate);
+        const bool fold = !REV && sg.nseg <= A.fold;
+        if (!first && !fold) add_state(0.f, A.s_seg + (slot * A.H + h) * sstate);
         else if (A.s_init) add_state(0.f, A.s_init + nh * sstate);
-        if (A.fold)  // forward in time only
+        if (fold)
             for (int64_t at = (slot - sg.j) * A.H + h; at < slot * A.H; at += A.H)
                 add_state(__builtin_amdgcn_exp2f(A.seg_decay[at]), A.s_seg + at * sstate);
     }

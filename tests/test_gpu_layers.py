@@ -227,6 +227,20 @@ def test_hd_packed(io, cu):
     check_bwd(x, r, cu=c.cpu())
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_hd_one_long_sequence_among_short_ones(io):
+    """Of one packed batch some sequences have many segments, some few, some one."""
+    cu = torch.tensor([0, 700, 7900, 7901, 8100, 8990], dtype=torch.int32, device="cuda")
+    x = hd_inputs(1, 9000, 1, 1, 32, 32, io, 33, N=5)
+    for n in ("q", "k", "v", "do", "g"):
+        x[n][:, 8990:] = 0.0
+    o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"], cu_seqlens=cu, out=torch.zeros_like(x["v"]))
+    check_fwd(x, o, S, cu=cu.cpu())
+    res = {n: torch.zeros_like(x[m]) for n, m in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"))}
+    r = kda.hd_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=cu, out=res)
+    check_bwd(x, r, cu=cu.cpu())
+
+
 def test_hd_many_packed_sequences():
     """More sequences than the table kernel takes at a time, most of them empty or of one token."""
     N, T = 2500, 3000
