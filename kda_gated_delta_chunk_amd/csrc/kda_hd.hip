@@ -2,9 +2,9 @@
 // chunk kernel's passes (kda_hd_core.hpp) in a forward or backward call.
 //
 // A call whose heads and column tiles do not fill the chip cuts its sequences into segments. A first pass forms what
-// each segment adds to a zero state (and its total decay), a second carries the states over the segments, and then
-// every segment runs as if it were a sequence of its own. The backward does the same for the states' gradients, from
-// the other end.
+// each segment adds to a zero state (and its total decay), a second carries the states over the segments (few segments
+// of the forward pass: their workgroups do), and then every segment runs as if it were a sequence of its own. The
+// backward does the same for the states' gradients, from the other end.
 #include "kda_hd.hpp"
 
 #include <cmath>
