@@ -489,7 +489,8 @@ size_t kda_hd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t
  *              are neither read nor written
  *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
  * The state is fp32 throughout; for bf16 I/O what is added to it is exact to
- * fp32. A non-finite q, k, v or g spoils its own head and sequence, from the
+ * fp32, and it is read, like a chunk's weighted products, as a pair of bf16
+ * (2^-16 of a term). A non-finite q, k, v or g spoils its own head and sequence, from the
  * first token of its 32-token chunk on. Errors as for kda_chunk_fwd
  * (INVALID_VALUE also for H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a
  * scale that is not finite).

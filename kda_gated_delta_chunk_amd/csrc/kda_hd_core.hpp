@@ -19,10 +19,11 @@
 // products D (a.b) go through LDS once, shared by all wavefronts.
 //
 // Precision (bf16 I/O). Products of inputs are exact in the matrix cores' fp32 sums. Three operands are computed
-// values. The weighted products D (a.b) go in as two bf16 parts (16 bits: with one, a result's error is 1.4 times its own
-// rounding, with two 1.05 times, for 1% of the time). The state as an operand is one bf16 part, two (SLO) where the
-// log-decays' gradient is summed from what it gives, for its terms cancel. wup c, which everything later in the sequence
-// is summed from, goes in as three parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
+// values. The weighted products D (a.b) and the state as an operand go in as two bf16 parts each, which hold a value to
+// 2^-16: the error of a bf16 result against fp64 is then its own rounding's, 0.0017 of its size (with the weighted
+// products in one part 1.4 times that, with the state in one part 1.1 to 1.2 times; the state's second part takes the
+// forward pass of 4096 tokens of 96 heads from 151 to 160 us). wup c, which everything later in the sequence is summed
+// from, goes in as three parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
 //
 // What bounds it. Per token and head of K = V = 128 in bf16 the forward pass moves 1 KB and multiplies 0.36 MFLOP, of
 // which 0.2 MFLOP are the three parts of wup c: at the card's rates the bytes take longer, but a chunk's steps (weighted
@@ -190,21 +191,23 @@ __device__ __forceinline__ float lane_value(float x, int lane) {  // the same fo
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
-// Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
-__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<true> &hi, Frag8<true> &lo) {
-    split_bf16(u.x, u.y, hi.p[0], lo.p[0]);
-    split_bf16(u.z, u.w, hi.p[1], lo.p[1]);
-    split_bf16(w.x, w.y, hi.p[2], lo.p[2]);
-    split_bf16(w.z, w.w, hi.p[3], lo.p[3]);
-}
-__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<false> &hi, Frag8<false> &lo) {
-    hi = Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
-    lo = hi;
-}
 // The pair as it was packed: the compiler would convert each half again to take it from its value.
 __device__ __forceinline__ uint32_t seen(uint32_t x) {
     asm("" : "+v"(x));
     return x;
+}
+// Two fp32 tiles of the state (rows 32c .. 32c+31, one column tile) as a left operand, and the rest of its rounding.
+__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<true> &hi, Frag8<true> &lo) {
+    const float x[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi.p[i] = seen(pack_bf16(x[2 * i], x[2 * i + 1]));
+        lo.p[i] = pack_bf16(x[2 * i] - bf_lo(hi.p[i]), x[2 * i + 1] - bf_hi(hi.p[i]));
+    }
+}
+__device__ __forceinline__ void state_frag(const f32x4 &u, const f32x4 &w, Frag8<false> &hi, Frag8<false> &lo) {
+    hi = Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
+    lo = hi;
 }
 // w c as three bf16 operands whose sum has all 24 bits (fp32: as it is)
 __device__ __forceinline__ void scaled_frags(const Frag8<true> &c, const float (&w)[8], Frag8<true> (&f)[3]) {
@@ -261,7 +264,6 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
     constexpr int C = kChunk, TT = C / 16, SC = C / 32;  // token tiles; 32-token steps
     constexpr int DB = L::DB, NB = L::NB;
     constexpr int NPART = BF ? 3 : 1;
-    constexpr bool SLO = BF && DG;
     static_assert(CT >= 1 && CT * 16 * NW == VT, "column tiles per wavefront");
     using E = typename IO<BF>::T;
     using RK = Rows<BF, KD>;
@@ -594,7 +596,7 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         y[ct][tt] = mma32(y[ct][tt], hi[ct], f);
-                        if constexpr (SLO) y[ct][tt] = mma32(y[ct][tt], lo[ct], f);
+                        if constexpr (BF) y[ct][tt] = mma32(y[ct][tt], lo[ct], f);
                     }
                 }
             }
