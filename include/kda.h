@@ -490,9 +490,9 @@ size_t kda_hd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t
  *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
  * The state is fp32 throughout; for bf16 I/O what is added to it is exact to
  * fp32, and it is read, like a chunk's weighted products, as a pair of bf16
- * (2^-16 of a term). A non-finite q, k, v or g spoils its own head and sequence, from the
- * first token of its 32-token chunk on. Errors as for kda_chunk_fwd
- * (INVALID_VALUE also for H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a
+ * (2^-16 of a term). A non-finite q, k, v or g spoils its own head and
+ * sequence from its own token on (garbage behind a prompt that shares its row
+ * does not reach it). Errors as for kda_chunk_fwd (INVALID_VALUE also for H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a
  * scale that is not finite).
  */
 kda_status_t kda_hd_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
@@ -510,7 +510,10 @@ kda_status_t kda_hd_chunk_fwd(const void *q, const void *k, const void *v, const
  *              here: NOT_SUPPORTED)
  *   dS0        [num_seqs, H, K, V] fp32, or NULL to skip
  * Nothing from a forward call is needed; the result is deterministic. Rows of
- * tokens outside every sequence are not written.
+ * tokens outside every sequence are not written. A non-finite value reaches,
+ * in its own head and sequence, what depends on it: a k or v dq from its token
+ * on, a q or d_o dk and dv up to its token, a g these and the rest of its
+ * 32-token chunk; and any of them may spoil every dg.
  */
 kda_status_t kda_hd_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
                               const int32_t *cu_seqlens, const void *d_o, const float *dS_final, int64_t B, int64_t T,

@@ -109,6 +109,9 @@ template <int NCOL> struct Rows<true, NCOL> {
     static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
         *reinterpret_cast<uint2 *>(t + quad(row, col)) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
     }
+    static __device__ __forceinline__ float load_one(const char *t, int row, int col) {
+        return bf2f(*reinterpret_cast<const uint16_t *>(t + quad(row, col) + 2 * (col & 3)));
+    }
     static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
         const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, col));
         x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
@@ -143,6 +146,9 @@ template <int NCOL> struct Rows<false, NCOL> {
     static __device__ __forceinline__ Frag8<false> tile_frag(const char *t, int at, int kt) { return col_frag(t, at, kt); }
     static __device__ __forceinline__ void store_quad(char *t, int row, int col, float a, float b, float c, float d) {
         *reinterpret_cast<float4 *>(t + quad(row, col)) = make_float4(a, b, c, d);
+    }
+    static __device__ __forceinline__ float load_one(const char *t, int row, int col) {
+        return *reinterpret_cast<const float *>(t + quad(row, col));
     }
     static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
         const float4 u = *reinterpret_cast<const float4 *>(t + quad(row, col));
@@ -223,6 +229,21 @@ __device__ __forceinline__ void scaled_frags(const Frag8<true> &c, const float (
 __device__ __forceinline__ void scaled_frags(const Frag8<false> &c, const float (&w)[8], Frag8<false> (&f)[1]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[0].f[i] = c.f[i] * w[i];
+}
+
+// Whether all entries of an operand in the wavefront are finite: 0 times them is 0.
+__device__ __forceinline__ bool all_finite(const Frag8<true> &f) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, f.p[i]), __builtin_bit_cast(bf16x2, 0u), z, false);
+    return __builtin_amdgcn_ballot_w64(z != 0.f) == 0;
+}
+__device__ __forceinline__ bool all_finite(const Frag8<false> &f) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z = fmaf(f.f[i], 0.f, z);
+    return __builtin_amdgcn_ballot_w64(z != 0.f) == 0;
 }
 
 // One wait for a whole register tile of products (see mfma_fence).
@@ -658,11 +679,32 @@ __device__ __forceinline__ void chunk_pass(const CoreArgs &A, int64_t item, int 
             for (int ct = 0; ct < CT; ++ct) {
                 const Frag8<BF> cf = RV::col_frag(s_c + 32 * s * RV::RB, colv, ct);
                 if constexpr (!INC) {
+                    if (all_finite(cf)) {
 #pragma unroll
-                    for (int tt = 0; tt < TT; ++tt) {
-                        if (REV ? 2 * s + 1 < tt : 2 * s > tt) continue;
-                        y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p + 16 * tt * RP::RB, rowp, s));
-                        if constexpr (BF) y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl + 16 * tt * RP::RB, rowp, s));
+                        for (int tt = 0; tt < TT; ++tt) {
+                            if (REV ? 2 * s + 1 < tt : 2 * s > tt) continue;
+                            y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_p + 16 * tt * RP::RB, rowp, s));
+                            if constexpr (BF)
+                                y[ct][tt] = mma32(y[ct][tt], cf, RP::row_frag(s_pl + 16 * tt * RP::RB, rowp, s));
+                        }
+                    } else {
+                        // A masked weight is 0, and 0 times infinity is NaN, which a token must not take from one that
+                        // it does not see: source by source, for those that see it. (The check that it takes to get
+                        // here costs up to 1.5%.)
+#pragma unroll 1
+                        for (int j = 32 * s; j < 32 * s + 32; ++j) {
+                            float x[4];
+                            RV::load_quad(s_c + rbuf * SZ_V, j, wave * CT * 16 + 16 * ct + 4 * g, x);
+#pragma unroll
+                            for (int tt = 0; tt < TT; ++tt) {
+                                const int t = 16 * tt + li;
+                                float p = RP::load_one(s_p, t, j);
+                                if constexpr (BF) p += RP::load_one(s_pl, t, j);
+                                if (REV ? j >= t && j < n : j <= t)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) y[ct][tt][i] = fmaf(p, x[i], y[ct][tt][i]);
+                            }
+                        }
                     }
                 }
                 scaled_frags(cf, w, cw[ct]);
