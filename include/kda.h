@@ -492,8 +492,9 @@ size_t kda_hd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t
  * fp32, and it is read, like a chunk's weighted products, as a pair of bf16
  * (2^-16 of a term). A non-finite q, k, v or g spoils its own head and
  * sequence from its own token on (garbage behind a prompt that shares its row
- * does not reach it). Errors as for kda_chunk_fwd (INVALID_VALUE also for H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a
- * scale that is not finite).
+ * does not reach it). Errors as for kda_chunk_fwd (INVALID_VALUE also for
+ * H % Hk != 0, H >= 65536, num_seqs * H >= 2^26 and a scale that is not
+ * finite).
  */
 kda_status_t kda_hd_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *S0,
                               const int32_t *cu_seqlens, int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K,

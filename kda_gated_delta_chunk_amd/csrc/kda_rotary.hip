@@ -76,28 +76,29 @@ __device__ __forceinline__ void store_run(void *p, const float (&x)[E]) {
     *reinterpret_cast<W *>(p) = w;
 }
 
-// E pairs of a unit: (x[i], y[i]), or adjacent channels of x followed by y.
+// E pairs of a unit: (x[i], y[i]), or adjacent channels of x followed by y. The first n turn; the others (adjacent channels
+// alone have any) are copied and not turned by nothing: a channel is to keep its bits whatever its neighbour holds.
 template <int E, bool INTER>
-__device__ __forceinline__ void turn_run(float (&x)[E], float (&y)[E], const float (&cs)[E], const float (&sn)[E]) {
-    auto turn = [](float &a, float &b, float c, float s) __attribute__((always_inline)) {
-        const float r = a * c - b * s;
-        b = a * s + b * c;
-        a = r;
+__device__ __forceinline__ void turn_run(float (&x)[E], float (&y)[E], const float (&cs)[E], const float (&sn)[E], int n) {
+    auto turn = [&](float &a, float &b, int i) __attribute__((always_inline)) {
+        const float r = a * cs[i] - b * sn[i], q = a * sn[i] + b * cs[i];
+        a = !INTER || i < n ? r : a;
+        b = !INTER || i < n ? q : b;
     };
     if constexpr (!INTER || E == 1) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) turn(x[i], y[i], cs[i], sn[i]);
+        for (int i = 0; i < E; ++i) turn(x[i], y[i], i);
     } else {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-            turn(y[2 * i], y[2 * i + 1], cs[E / 2 + i], sn[E / 2 + i]);
+            turn(x[2 * i], x[2 * i + 1], i);
+            turn(y[2 * i], y[2 * i + 1], E / 2 + i);
         }
     }
 }
 
-// A unit is a run of E pairs or, behind them, a run of 2E copied channels; an interleaved unit that straddles R turns
-// its pairs from R on by nothing. Threads of a workgroup: `units` consecutive ones per head, heads_par heads at a
+// A unit is a run of E pairs or, behind them, a run of 2E copied channels; an interleaved unit that straddles R copies
+// its pairs from R on. Threads of a workgroup: `units` consecutive ones per head, heads_par heads at a
 // time, tok_par tokens at a time. q_out and k_out may be q and k: a thread reads its channels before it writes them.
 template <bool BF, int E, bool INTER>
 __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const void *kp, void *qo, void *ko,
@@ -149,9 +150,8 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 sincos_turn(fr[i] * (uint64_t)pos, sn[i], cs[i]);
-                const bool turned = u * E + i < R / 2;
-                sn[i] *= turned ? sgn * scale : 0.f;
-                cs[i] *= turned ? scale : 1.f;
+                sn[i] *= sgn * scale;
+                cs[i] *= scale;
             }
         }
         for (int h = hsub; h < Hq + Hk; h += heads_par) {
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
             const bool more = h + heads_par < Hq + Hk;
             take(more ? t : t + step, more ? h + heads_par : hsub, next);
             if (r.live) {
-                if (pairs) turn_run<E, INTER>(r.x, r.y, cs, sn);
+                if (pairs) turn_run<E, INTER>(r.x, r.y, cs, sn, R / 2 - u * E);
                 store_run<BF, E>(r.d + c0 * ES, r.x);
                 if (two) store_run<BF, E>(r.d + c1 * ES, r.y);
             }

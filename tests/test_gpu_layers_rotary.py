@@ -1,0 +1,33 @@
+"""GPU tests of rotary positions where values or arguments are unusual."""
+import pytest
+import torch
+
+import kda_gated_delta_chunk_amd as kda
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+BITS = {"bf16": torch.int16, "fp32": torch.int32}
+
+
+def rnd(shape, seed, dt=torch.float32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dt).cuda()
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,R", [(96, 22), (96, 2), (64, 34), (80, 40), (36, 6), (18, 10), (257, 130), (9, 8)])
+def test_copied_channels_keep_their_bits(D, R, layout, io):
+    """Channels behind R are copied whatever they hold (infinities, NaN, negative zeros), and reach no others; in place
+    too, there they are what they were."""
+    q = rnd((5, 3, D), 1, DT[io])
+    odd = torch.tensor([float("inf"), float("nan"), -0.0, float("-inf")]).to(q)
+    q[..., R:] = odd[torch.arange(D - R, device="cuda") % 4]
+    f = kda.rotary_freqs(R)
+    clean = q.clone()
+    clean[..., R:] = 1.0
+    want = kda.rotary(clean, f, layout=layout)
+    place = q.clone()
+    for y in (kda.rotary(q, f, layout=layout), kda.rotary(place, f, layout=layout, out=place)):
+        assert torch.equal(y[..., R:].view(BITS[io]), q[..., R:].view(BITS[io]))
+        assert torch.equal(y[..., :R], want[..., :R])
