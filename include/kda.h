@@ -540,7 +540,8 @@ kda_status_t kda_hd_decode_step(const void *q, const void *k, const void *v, con
  * and the others are copied. inverse = 1 turns back: with the same scale, the
  * gradient of the call with inverse = 0 (and the other way round).
  *   freqs      [R/2] fp64, radians per position: angles are reduced in
- *              64-bit fixed point, exact at any 32-bit position
+ *              64-bit fixed point, exact at any 32-bit position; an infinite
+ *              or NaN frequency makes its pair NaN
  *   positions  [tokens] int32 (any sign), or NULL: token index modulo T
  * q_out may be q and k_out may be k (in place).
  */

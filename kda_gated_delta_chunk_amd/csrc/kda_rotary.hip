@@ -19,7 +19,7 @@
 namespace kda {
 namespace {
 
-__device__ __forceinline__ uint64_t turn_fraction(double freq) {
+__device__ __forceinline__ uint64_t turn_fraction(double freq) {  // of a finite frequency
     double t = freq * 0.15915494309189535;  // 1 / (2 pi)
     t -= floor(t);
     return t >= 1.0 || !(t >= 0.0) ? 0ull : (uint64_t)(t * 18446744073709551616.0);
@@ -115,8 +115,13 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     const int np = (R / 2 + E - 1) / E;  // units with pairs to turn
     const bool pairs = u < np;
     uint64_t fr[E];
+    uint32_t undefined = 0;  // pairs whose frequency is infinite or NaN: their angles are NaN at any position
 #pragma unroll
-    for (int i = 0; i < E; ++i) fr[i] = pairs && u * E + i < R / 2 ? turn_fraction(freqs[u * E + i]) : 0ull;
+    for (int i = 0; i < E; ++i) {
+        const double f = pairs && u * E + i < R / 2 ? freqs[u * E + i] : 0.0;
+        fr[i] = turn_fraction(f);
+        undefined |= (uint32_t)!(fabs(f) < HUGE_VAL) << i;
+    }
     // the two runs of a unit: (x1 run, x2 run) of "half", 2E adjacent channels otherwise
     const int c0 = INTER ? 2 * E * u : pairs ? E * u : R + 2 * E * (u - np);
     const int c1 = pairs && !INTER ? c0 + R / 2 : c0 + E;
@@ -152,6 +157,7 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
                 sincos_turn(fr[i] * (uint64_t)pos, sn[i], cs[i]);
                 sn[i] *= sgn * scale;
                 cs[i] *= scale;
+                if (undefined >> i & 1) sn[i] = cs[i] = __builtin_nanf("");
             }
         }
         for (int h = hsub; h < Hq + Hk; h += heads_par) {

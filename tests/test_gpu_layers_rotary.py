@@ -31,3 +31,18 @@ def test_copied_channels_keep_their_bits(D, R, layout, io):
     for y in (kda.rotary(q, f, layout=layout), kda.rotary(place, f, layout=layout, out=place)):
         assert torch.equal(y[..., R:].view(BITS[io]), q[..., R:].view(BITS[io]))
         assert torch.equal(y[..., :R], want[..., :R])
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_frequencies_that_are_no_numbers(bad, layout, io):
+    """An angle that is no number turns its pair into NaN, at position 0 too, and no other pair."""
+    q, f = rnd((4, 3, 40), 1, DT[io]), kda.rotary_freqs(24)
+    want = kda.rotary(q, f, layout=layout)
+    f[5] = bad
+    y = kda.rotary(q, f, layout=layout)
+    hit = torch.zeros(40, dtype=torch.bool, device="cuda")
+    hit[[5, 17] if layout == "half" else [10, 11]] = True
+    assert bool(y[..., hit].isnan().all())
+    assert torch.equal(y[..., ~hit], want[..., ~hit])
