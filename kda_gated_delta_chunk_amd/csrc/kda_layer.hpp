@@ -50,7 +50,7 @@ struct RotaryArgs {
     void *q_out, *k_out;
     const double *freqs;       // [R / 2] radians per position
     const int32_t *positions;  // [tokens], or null: token index modulo T
-    int64_t tokens, T;
+    int64_t tokens, T;         // 1 <= T <= tokens
     int32_t Hq, Hk, D, R;
     bool io_bf16, interleaved, inverse;
     float scale;

@@ -215,7 +215,8 @@ kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const
     if (st != KDA_SUCCESS) return st;
     kda::RotaryArgs a{};
     a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out; a.freqs = freqs; a.positions = positions;
-    a.tokens = tokens; a.T = T > 0 ? T : 1;
+    a.tokens = tokens;
+    a.T = T > 0 && T < tokens ? T : tokens;  // a period past the last token changes nothing (and is 32-bit if tokens are)
     a.Hq = Hq; a.Hk = Hk; a.D = D; a.R = R;
     a.io_bf16 = io == KDA_DTYPE_BF16;
     a.interleaved = layout == KDA_ROTARY_INTERLEAVED;

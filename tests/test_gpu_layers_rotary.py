@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import kda_gated_delta_chunk_amd as kda
+from kda_gated_delta_chunk_amd import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,25 @@ def test_frequencies_that_are_no_numbers(bad, layout, io):
     hit[[5, 17] if layout == "half" else [10, 11]] = True
     assert bool(y[..., hit].isnan().all())
     assert torch.equal(y[..., ~hit], want[..., ~hit])
+
+
+@pytest.mark.parametrize("T", [1, 3, 9, 10, 11, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 40, 2 ** 63 - 1])
+def test_period_of_the_positions(T):
+    """Without positions a token's is its index modulo T, for any T (the C interface; Python's T is an axis)."""
+    n, H, D = 10, 2, 32
+    q, f = rnd((n, H, D), 1), kda.rotary_freqs(D)
+    y = torch.empty_like(q)
+    st = _lib.load().kda_rotary(q.data_ptr(), None, f.data_ptr(), None, y.data_ptr(), None, n, T, H, 0, D, D, 0, 0, 0, 1.0,
+                                torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    pos = torch.tensor([t % T for t in range(n)], dtype=torch.int32, device="cuda")
+    assert torch.equal(y, kda.rotary(q, f, positions=pos))
+
+
+def test_period_is_ignored_beside_positions():
+    q, f = rnd((10, 2, 32), 1), kda.rotary_freqs(32)
+    y, pos = torch.empty_like(q), torch.arange(10, dtype=torch.int32, device="cuda") * 7
+    for T in (-1, 0, 1, 2 ** 32):
+        st = _lib.load().kda_rotary(q.data_ptr(), None, f.data_ptr(), pos.data_ptr(), y.data_ptr(), None, 10, T, 2, 0, 32, 32,
+                                    0, 0, 0, 1.0, torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(y, kda.rotary(q, f, positions=pos))
