@@ -560,7 +560,9 @@ kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const
  *   x, o_gate, y  [rows, C] in `io` (o_gate or NULL)
  *   weight, bias  [groups, C] fp32 or NULL (1 and 0); row r has those of
  *                 group r % groups (groups = heads for rows [.., H, C]);
- *                 rows % groups == 0
+ *                 rows % groups == 0; groups * C at most 2^27 and
+ *                 groups / gcd(groups, 32) below 2^24 (a grid's threads are
+ *                 32-bit), else INVALID_VALUE
  * Statistics and sums are fp32, the variance from the centered values.
  */
 kda_status_t kda_layer_norm_fwd(const void *x, const float *weight, const float *bias, const void *o_gate, void *y,

@@ -72,6 +72,7 @@ struct NormArgs {
     float *dweight, *dbias;
     void *workspace;
 };
+bool norm_grid_fits(int64_t rows, int32_t G, int32_t C);  // a grid's threads are 32-bit (many groups of narrow rows)
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t G, int32_t C);
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st);

@@ -230,6 +230,7 @@ static kda_status_t check_norm_sizes(int64_t rows, int32_t groups, int32_t C) {
     if (C > 16384) return KDA_ERROR_NOT_SUPPORTED;
     // a workgroup of 1024 threads for 64 parameters: a grid's threads are 32-bit
     if (rows > kMaxElems / C || (int64_t)groups * C > (1 << 27)) return KDA_ERROR_INVALID_VALUE;
+    if (!kda::norm_grid_fits(rows, groups, C)) return KDA_ERROR_INVALID_VALUE;
     return KDA_SUCCESS;
 }
 

@@ -397,11 +397,13 @@ int64_t grid_for(int64_t rows, int G, int rpw, int64_t most) {
     return wgs;
 }
 
+constexpr int kFwdWG = 2048;  // the same for the forward pass
+
 template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
 hipError_t run_gate(const NormArgs &a, bool bwd, hipStream_t st) {
     constexpr int RPW = NT / TPR;
     if (!bwd) {
-        const int64_t wgs = grid_for(a.rows, a.G, RPW, 2048);
+        const int64_t wgs = grid_for(a.rows, a.G, RPW, kFwdWG);
         hipLaunchKernelGGL((kda_norm_fwd_kernel<BF, VEC, TPR, NT, EPT, GATE>), dim3((uint32_t)wgs), dim3(NT), 0, st,
                            a.x, a.gate, a.weight, a.bias, a.y, a.rows, a.G, a.C, a.eps, (int)a.center);
         return hipGetLastError();
@@ -445,8 +447,15 @@ hipError_t by_type(const NormArgs &a, bool bwd, hipStream_t st) {
 
 }  // namespace
 
+static int rows_per_wg(int32_t C) {  // NT / TPR of by_width
+    return C <= 64 ? 32 : C <= 128 ? 16 : C <= 256 ? 8 : C <= 512 ? 4 : C <= 1024 ? 2 : 1;
+}
+bool norm_grid_fits(int64_t rows, int32_t G, int32_t C) {
+    const int64_t threads = C <= 2048 ? 256 : C <= 4096 ? 512 : 1024;  // NT of by_width
+    return grid_for(rows, G, rows_per_wg(C), kFwdWG) * threads < (int64_t)1 << 32;
+}
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t G, int32_t C) {
-    const int rpw = C <= 64 ? 32 : C <= 128 ? 16 : C <= 256 ? 8 : C <= 512 ? 4 : C <= 1024 ? 2 : 1;  // NT / TPR of by_width
+    const int rpw = rows_per_wg(C);
     return (size_t)(grid_for(rows, G, rpw, kMaxWG) * parts_of(rpw, G)) * C * 2 * sizeof(float);
 }
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
