@@ -460,7 +460,9 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
  *   KDA_DECAY_PER_HEAD   [H] fp32: a constant of each head
  * Log-decays are at most 0 in use; -inf (a token that clears the state) is
  * allowed, everything below -104 counts as e^-104 = 0 in fp32. Positive ones
- * are used as given as long as their sums stay in range.
+ * are used as given as long as their sums stay in range. What is added to a
+ * state is held scaled by up to 2^24 between two chunks: products of k and v
+ * (of q and d_o) above 2^103 can overflow.
  */
 typedef enum {
     KDA_DECAY_PER_TOKEN = 0,
@@ -563,7 +565,9 @@ kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const
  *                 rows % groups == 0; groups * C at most 2^27 and
  *                 groups / gcd(groups, 32) below 2^24 (a grid's threads are
  *                 32-bit), else INVALID_VALUE
- * Statistics and sums are fp32, the variance from the centered values.
+ * Statistics and sums are fp32, the variance from the centered values (their
+ * squares have to stay in range: rows of values above 2^57 can come out as
+ * zeros).
  */
 kda_status_t kda_layer_norm_fwd(const void *x, const float *weight, const float *bias, const void *o_gate, void *y,
                                 int64_t rows, int32_t groups, int32_t C, float eps, int32_t center, kda_dtype_t io,

@@ -56,3 +56,22 @@ def test_hd_gradient_operands(B, T, H, Hk, K, V, scale, decay, want_dg, io):
     mag = ol.hd_backward(a["q"], a["k"], a["v"], a["g"], a["do"], a["S0"], a["dS"], None, abs(scale))
     for name in ("dq", "dk", "dv"):
         close(name, r[name], ref[name], half_step(dt) * ref[name].abs() + (PAIR[io] + n * U) * mag[name])
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H", [(97, 3), (700, 1)])
+def test_hd_growing_states(T, H, io):
+    """Log-decays of both signs, whose sums stay in range: states that grow by up to e^9 over a sequence and shrink again."""
+    x = hd_inputs(1, T, H, H, 64, 64, io, 900 + T)
+    wave = torch.sin(torch.arange(T, dtype=torch.float32) * (6.3 / T)) * (28.0 / T)
+    x["g"] = wave[None, :, None].expand(1, T, H).to(DT[io]).contiguous().cuda()
+    a, dt, n = _abs(x), DT[io], roundings(T, 64, 64)
+    o, S = kda.hd_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0=x["S0"])
+    (ref, rS), (mag, mS) = (ol.hd_forward(*[y[m] for m in ("q", "k", "v", "g", "S0")]) for y in (x, a))
+    close("o", o, ref, half_step(dt) * ref.abs() + (PAIR[io] + n * U) * mag)
+    close("S_final", S, rS, n * U * mS)
+    r = kda.hd_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_final=x["dS"])
+    ref, mag = (ol.hd_backward(*[y[m] for m in ("q", "k", "v", "g", "do", "S0", "dS")]) for y in (x, a))
+    for name in ("dq", "dk", "dv"):
+        close(name, r[name], ref[name], half_step(dt) * ref[name].abs() + (PAIR[io] + n * U) * mag[name])
+    close("dS0", r["dS0"], ref["dS0"], n * U * mag["dS0"])
