@@ -35,7 +35,8 @@ int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
 // How long a call with n segments per row takes, in ns as measured at K = V = 128 in bf16: the main pass's rounds over
 // the workgroups that the chip holds (a token of the forward pass takes 110 ns, of the gradients 160; three quarters of
 // that where no two share a CU); with several segments also the increments' rounds (80 ns), the states' traffic (50 ns
-// per head and segment, twice for the gradients) and two more launches.
+// per head and segment, twice for the gradients) and two more launches. (The forward pass's 110 is of the state read in one
+// part; with the 13% more of two parts 2% of random sizes would be cut otherwise, by the model for 3% of their time.)
 int64_t cost(int64_t rows, int64_t inc_rows, int64_t heads, int64_t resident, int64_t T, int64_t n, bool bwd) {
     const int64_t seg = round64((T + n - 1) / n), groups = rows * n;
     int64_t c = (groups + resident - 1) / resident * seg * (bwd ? 160 : 110);

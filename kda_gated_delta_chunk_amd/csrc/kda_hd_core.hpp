@@ -22,19 +22,19 @@
 // values. The weighted products D (a.b) and the state as an operand go in as two bf16 parts each, which hold a value to
 // 2^-16: the error of a bf16 result against fp64 is then its own rounding's, 0.0017 of its size (with the weighted
 // products in one part 1.4 times that, with the state in one part 1.1 to 1.2 times; the state's second part takes the
-// forward pass of 4096 tokens of 96 heads from 151 to 160 us). wup c, which everything later in the sequence is summed
+// forward pass of 4096 tokens of 96 heads from 151 to 161 us). wup c, which everything later in the sequence is summed
 // from, goes in as three parts, all 24 bits of it, so the fp32 state carries no rounding of its operands.
 //
-// What bounds it. Per token and head of K = V = 128 in bf16 the forward pass moves 1 KB and multiplies 0.36 MFLOP, of
-// which 0.2 MFLOP are the three parts of wup c: at the card's rates the bytes take longer, but a chunk's steps (weighted
-// products, one barrier, the state's products) follow each other, so what bounds it is their latency and the vector
-// instructions that convert, scale and address, with two workgroups of 8 wavefronts a CU to hide behind one another.
-// 4096 tokens of 96 heads: 97 us in the forward kernel (87 without the state's update, 94 without the rows' loads, 24
-// without both and the products), 48 us in the increments; 360 us in the gradients' kernel. What
-// brought it there from 427 us of simple kernels: rows one chunk ahead (271), fewer exponentials (249), chunks of 32
-// tokens on 128 columns (198), zero weights in place of cleared rows (180), 8 wavefronts and addresses made anew (174),
-// decays made 16 chunks at a time (162), stores without branches and 16-byte operand reads (156), segments' states formed
-// by the workgroups that start from them (150).
+// What bounds it. Per token and head of K = V = 128 in bf16 the forward pass moves 1 KB and multiplies 0.27 MFLOP in its
+// two passes, of which 0.18 MFLOP are the three parts of wup c: at the card's rates the bytes take longer, but a chunk's
+// steps (weighted products, one barrier, the state's products) follow each other, so what bounds it is their latency and
+// the vector instructions that convert, scale and address, with two workgroups of 8 wavefronts a CU to hide behind one
+// another: of the forward kernel's cycles 58% issue a vector instruction and 32% a matrix one. 4096 tokens of 96 heads:
+// 110 us in the forward kernel, 48 us in the increments; 369 us in the gradients' kernel (the fastest of 20 dispatches).
+// What brought the forward call there from 427 us of simple kernels: rows one chunk ahead (271), fewer exponentials (249),
+// chunks of 32 tokens on 128 columns (198), zero weights in place of cleared rows (180), 8 wavefronts and addresses made
+// anew (174), decays made 16 chunks at a time (162), stores without branches and 16-byte operand reads (156), segments'
+// states formed by the workgroups that start from them (150); the state's second part took it to 161.
 #pragma once
 
 #include "kda_common.hpp"

@@ -246,9 +246,10 @@ def rotary(q, freqs, k=None, positions=None, layout: str = "half", inverse: bool
     in pairs j by the angle position * freqs[j] and copies the others. Returns the turned q, or (q, k).
 
     ``layout``: "half" pairs (j, j + len(freqs)), "interleaved" pairs (2j, 2j + 1). ``freqs``: fp64 (rotary_freqs());
-    angles are exact at any int32 position. ``positions``: int32 of q's leading shape; None counts 0 .. T-1 along the
-    third axis from the end. ``scale`` multiplies the turned channels. ``inverse`` turns back: the gradient of the same
-    call without it. ``out`` / ``k_out`` may be q / k themselves (in place).
+    angles are exact at any int32 position, a frequency that is not finite makes its pair NaN. ``positions``: int32 of
+    q's leading shape; None counts 0 .. T-1 along the third axis from the end. ``scale`` multiplies the turned channels.
+    ``inverse`` turns back: the gradient of the same call without it. ``out`` / ``k_out`` may be q / k themselves (in
+    place).
     """
     lib = _lib.load()
     dev = _cuda(q)
