@@ -533,6 +533,81 @@ kda_status_t kda_hd_decode_step(const void *q, const void *k, const void *v, con
                                 kda_decay_t decay, float scale, void *stream);
 
 /*
+ * The gated delta rule with one decay per head. Per sequence and head, with
+ * the state S in R^{K x V}:
+ *
+ *   S <- exp(g_t) S;   w_t <- beta_t (v_t - S^T k_t);   S <- S + k_t w_t^T
+ *   o_t <- scale * S^T q_t
+ *
+ * g and beta are [B, T, H] in `gates`: the I/O dtype, or fp32 beside bf16.
+ * Log-decays are at most 0 in use; -inf (a token that clears the state) is
+ * allowed, everything below -104 counts as e^-104 = 0 in fp32. Positive ones
+ * are used as given as long as their sums stay in range. The rule contracts
+ * where beta |k|^2 <= 2; beyond that states grow from token to token.
+ */
+
+/*
+ * Workspace bytes of kda_gd_chunk_fwd and kda_gd_chunk_bwd (arguments as
+ * there; packed: whether cu_seqlens is given, 0 or 1). 0 for sizes that are
+ * not supported.
+ */
+size_t kda_gd_chunk_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                                        int32_t num_seqs, int32_t packed, kda_dtype_t io);
+size_t kda_gd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                                        int32_t num_seqs, int32_t packed, kda_dtype_t io);
+
+/*
+ * Chunked forward pass over whole sequences.
+ *   q, k       [B, T, Hk, K], v [B, T, H, V] in `io`; H % Hk == 0, head h
+ *              reads the q and k of head h / (H / Hk); K, V 32, 64 or 128
+ *   S0         [num_seqs, H, K, V] fp32 or NULL (zero)
+ *   cu_seqlens as for kda_chunk_fwd (clamped, made non-decreasing on the
+ *              device; empty sequences allowed: their S_final is S0)
+ *   o          [B, T, H, V] in `io`; rows of tokens outside every sequence
+ *              are neither read nor written
+ *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
+ * The state is fp32 throughout; for bf16 I/O what is added to it enters with
+ * all 24 bits, and what is read from it, and the pairs' weights, as a pair of
+ * bf16 (2^-17 of a term). A non-finite q, k, v, g or beta spoils its own head
+ * and sequence from its own token on (garbage behind a prompt that shares its
+ * row does not reach it). Errors as for kda_chunk_fwd (INVALID_VALUE also for
+ * H % Hk != 0, H >= 65536, num_seqs * H >= 2^26, gates of another type and a
+ * scale that is not finite).
+ */
+kda_status_t kda_gd_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                              const float *S0, const int32_t *cu_seqlens, int64_t B, int64_t T, int32_t H, int32_t Hk,
+                              int32_t K, int32_t V, int32_t num_seqs, kda_dtype_t io, kda_dtype_t gates, float scale,
+                              void *o, float *S_final, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients, given d_o = dL/do [B, T, H, V] in `io` and dS_final =
+ * dL/dS_final (fp32, or NULL: zero):
+ *   dq, dk     [B, T, Hk, K], dv [B, T, H, V] in `io` (dq and dk summed in
+ *              fp32 over the heads that share them), rounded once
+ *   dg, dbeta  [B, T, H] in `gates`
+ *   dS0        [num_seqs, H, K, V] fp32, or NULL to skip
+ * Nothing from a forward call is needed; the result is deterministic. Rows of
+ * tokens outside every sequence are not written. A non-finite value reaches,
+ * in its own head and sequence, what depends on it: a v dq and dk from its
+ * token on, a q or d_o dk and dv up to its token, a k dq from its token on and
+ * dk and dv up to it, a g or beta these and the rest of its 32-token chunk;
+ * and any of them may spoil every dg and dbeta.
+ */
+kda_status_t kda_gd_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                              const float *S0, const int32_t *cu_seqlens, const void *d_o, const float *dS_final,
+                              int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
+                              kda_dtype_t io, kda_dtype_t gates, float scale, void *dq, void *dk, void *dv, void *dg,
+                              void *dbeta, float *dS0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of N sequences: q, k [N, Hk, K], v [N, H, V], o [N, H, V] in
+ * `io`; g, beta [N, H] in `gates`; S [N, H, K, V] fp32, in place.
+ */
+kda_status_t kda_gd_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, float *S,
+                                void *o, int32_t N, int32_t H, int32_t Hk, int32_t K, int32_t V, kda_dtype_t io,
+                                kda_dtype_t gates, float scale, void *stream);
+
+/*
  * Rotary positions of q [tokens, Hq, D] and k [tokens, Hk, D] (Hk = 0 and
  * NULL: q alone) in `io`. Of each head's D channels (2..512) the first R
  * (even) turn in pairs j by the angle position * freqs[j]:

@@ -34,7 +34,9 @@ EXPORTS = ("kda_abi_version", "kda_status_string", "kda_chunk_fwd_workspace_byte
            "kda_chunk_bwd_workspace_bytes", "kda_chunk_bwd_segmented_workspace_bytes", "kda_chunk_bwd",
            "kda_chunk_fwd_no_alloc",
            "kda_hd_chunk_fwd_workspace_bytes", "kda_hd_chunk_bwd_workspace_bytes", "kda_hd_chunk_fwd",
-           "kda_hd_chunk_bwd", "kda_hd_decode_step", "kda_rotary", "kda_layer_norm_fwd",
+           "kda_hd_chunk_bwd", "kda_hd_decode_step",
+           "kda_gd_chunk_fwd_workspace_bytes", "kda_gd_chunk_bwd_workspace_bytes", "kda_gd_chunk_fwd",
+           "kda_gd_chunk_bwd", "kda_gd_decode_step", "kda_rotary", "kda_layer_norm_fwd",
            "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd")
 
 NO_ALLOC_SCRATCH_BYTES = 16 * 1024 * 1024  # KDA_NO_ALLOC_SCRATCH_BYTES
@@ -110,6 +112,17 @@ def load() -> ctypes.CDLL:
     lib.kda_hd_chunk_bwd.restype = ci
     lib.kda_hd_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ci, ci, f32, vp]
     lib.kda_hd_decode_step.restype = ci
+    for fn in (lib.kda_gd_chunk_fwd_workspace_bytes, lib.kda_gd_chunk_bwd_workspace_bytes):
+        fn.argtypes = [i64, i64, i32, i32, i32, i32, i32, i32, ci]
+        fn.restype = sz
+    lib.kda_gd_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, ci, ci, f32, vp, vp,
+                                     vp, sz, vp]
+    lib.kda_gd_chunk_fwd.restype = ci
+    lib.kda_gd_chunk_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, ci, ci, f32,
+                                     vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_gd_chunk_bwd.restype = ci
+    lib.kda_gd_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ci, ci, f32, vp]
+    lib.kda_gd_decode_step.restype = ci
     lib.kda_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, ci, ci, i32, f32, vp]
     lib.kda_rotary.restype = ci
     lib.kda_layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, ci, vp]

@@ -1,0 +1,127 @@
+// The gated delta rule with one decay per head: what its translation units share. Internal to the library.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+struct GdArgs {
+    const void *q, *k, *v;     // q, k [B,T,Hk,K]; v [B,T,H,V]
+    const void *g, *beta;      // [B,T,H] in the I/O dtype, or fp32 (gates_fp32)
+    const float *S0;           // [N,H,K,V] or null
+    const int32_t *cu_seqlens;
+    int64_t B, T;
+    int32_t H, Hk, K, V, num_seqs;
+    bool io_bf16, gates_fp32;
+    float scale;
+    void *o;
+    float *S_final;            // or null
+    // backward only
+    const void *dout;          // dL/do [B,T,H,V]
+    const float *dS_final;     // or null
+    void *dq, *dk, *dv;        // I/O dtype
+    void *dg, *dbeta;          // the gates' dtype
+    float *dS0;                // or null
+    void *workspace;
+};
+size_t gd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
+                              bool packed, bool io_bf16);
+size_t gd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
+                              bool packed, bool io_bf16);
+hipError_t launch_gd_fwd(const GdArgs &a, hipStream_t st);
+hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st);
+
+struct GdDecodeArgs {
+    const void *q, *k, *v, *g, *beta;
+    float *S;
+    void *o;
+    int32_t N, H, Hk, K, V;
+    bool io_bf16, gates_fp32;
+    float scale;
+};
+hipError_t launch_gd_decode(const GdDecodeArgs &a, hipStream_t st);
+
+namespace gd {
+
+constexpr int kChunkTokens = 32;
+constexpr int kSegmentChunks = 8;  // chunks of a workgroup of the gradients' kernel
+
+// A sequence: its tokens in the flattened [B * T], the number of its first chunk and of its first segment among all.
+struct Seq {
+    int64_t t0, t1, first, seg;
+};
+
+// A chunk's record, made once per (chunk, head) and read by the passes over the states. Matrices lie in the order in
+// which a wavefront's lanes read them as operands: [16-row tile][half][lane][16 bytes], the halves a bf16 pair's parts
+// or the first and last four of eight fp32 slots.
+enum Mat { kMatN = 0, kMatP = 1, kMatNT = 1, kMatPT = 2 };  // forward: N, P; backward: N, its transpose, P's
+constexpr int kMatBytes = 4096;
+enum Weight { kEnter, kEnterScaled, kLeave, kLeaveBeta, kBeta, kSumHi, kSumLo, kTotal, kWeights };
+constexpr int rec_bytes(bool bwd) { return (bwd ? 3 : 2) * kMatBytes + kWeights * kChunkTokens * 4; }
+constexpr int rec_weights(bool bwd) { return (bwd ? 3 : 2) * kMatBytes; }
+
+struct Common {
+    const Seq *seqs;   // or null: rows of T tokens
+    int64_t T, ntok, slots, segs;  // slots, segs: chunks and segments of all sequences (upper bounds when packed)
+    int32_t nch, nseg;  // per row (not packed)
+    int32_t N, H, Hk;
+    char *rec;          // [slots][H] records
+};
+
+struct StateArgs {
+    Common c;
+    const void *q, *k, *v;   // v: the rows of V channels (backward: dL/do)
+    const float *s_init;     // the state before the first chunk (reverse: its gradient behind the last), or null
+    float *s_end;            // at the other end, or null
+    void *o;                 // forward: [B,T,H,V]; reverse: dv
+    char *rows;              // backward: [slots][H] tiles of [V][32]: the errors z, or the writes' gradients
+    float *seed;             // backward: states at the segments' borders [segs][H][K][V]
+    int32_t tiles;           // column tiles
+};
+
+struct GradArgs {
+    Common c;
+    const void *q, *k, *dout;
+    const char *z, *dw;      // tiles of [V][32] per (chunk, head)
+    const float *S0, *dS_final, *seed_s, *seed_g;
+    void *dq, *dk;           // I/O dtype, or fp32 per v head
+    float *dk_part;          // [B,T,H,K]: what the walk forward adds to dk
+    void *dg, *dbeta;
+    float scale;
+    int gates_fp32;
+};
+
+constexpr int state_tile(int V) { return V < 64 ? V : 64; }
+
+enum Mode { kForward, kErrors, kReverse };  // outputs; the errors and states for the gradients; the state's gradients
+hipError_t state_pass(bool bf16, Mode mode, const StateArgs &a, int K, int V, hipStream_t st);
+hipError_t grad_pass_bf16(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
+hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st);
+
+#ifdef __HIPCC__
+__device__ __forceinline__ Seq seq_of(const Common &c, int64_t n) {
+    if (c.seqs) return c.seqs[n];
+    return Seq{n * c.T, (n + 1) * c.T, n * c.nch, n * c.nseg};
+}
+// The last sequence whose first chunk (segment) is at most `slot`, by 64 entries at a time. One wavefront, all lanes.
+template <bool SEG>
+__device__ __forceinline__ int64_t find_seq(const Common &c, int64_t slot, int lane) {
+    if (!c.seqs) return slot / (SEG ? c.nseg : c.nch);
+    int64_t lo = 0, len = c.N;
+    while (true) {
+        const int64_t step = (len + 63) / 64, i = lo + lane * step;
+        const bool at_most = i < lo + len && (SEG ? c.seqs[i].seg : c.seqs[i].first) <= slot;
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(at_most));  // the entries do not decrease
+        if (n == 0) return lo;
+        const int64_t end = lo + len;
+        lo += (n - 1) * step;
+        if (step == 1) return lo;
+        len = end - lo < step ? end - lo : step;
+    }
+}
+#endif
+
+}  // namespace gd
+}  // namespace kda

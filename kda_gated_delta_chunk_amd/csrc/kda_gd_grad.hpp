@@ -1,0 +1,465 @@
+// The gated delta rule with one decay per head: the gradients of q, k, g and beta.
+//
+// Given the errors z and the gradients dw of what is written (w = beta z), the recurrence is a plain decaying sum of
+// k_i w_i^T, and what is left are four such sums, two forward in time over the state S and two backward over its gradient
+// G (E_ri = e^{b_r - b_i}; M_ri = dw_r.z_i):
+//   dq_r = scale ( e^{b_r} S do_r + sum_{i<=r} E_ri (do_r.w_i) k_i )
+//   dk_r = - beta_r ( e^{b_r} S dw_r + sum_{i<r} E_ri beta_i M_ri k_i )                                  (read)
+//        + e^{b_C - b_r} beta_r G z_r + sum_{j>=r} scale E_jr (do_j.w_r) q_j - sum_{j>r} E_jr beta_j beta_r M_jr k_j
+//   dbeta_r = M_rr
+// Each pair and state that a token's log-decay spans is in a row's read and another's write: with db_r = q_r.dq_r +
+// k_r.dk_r(read) - k_r.dk_r(rest),  dg_t = sum_{r>=t} db_r up to a border, and what the border passes on, <G, S> there.
+#pragma once
+
+#include "kda_gd_core.hpp"
+
+namespace kda {
+namespace gd {
+
+template <bool BF, int K, int V>
+struct GradLds {
+    static constexpr int C = kChunkTokens, NP = BF ? 2 : 1, NW = K / 16;
+    static constexpr int T_ = Rows<BF, C>::bytes(V), M_ = Rows<BF, C>::bytes(C);  // a part of a [V][32] tile, of a matrix
+    static constexpr int K_ = Rows<BF, K>::bytes(C), O_ = Rows<BF, V>::bytes(C);
+    static constexpr int dout = 0, z = dout + O_, dw = z + NP * T_, k = dw + NP * T_, q = k + K_, m1 = q + K_,
+                         m2 = m1 + NP * M_, wt = m2 + NP * M_, u = wt + kWeights * C * 4,
+                         db = u + NW * C * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
+};
+
+// One segment of a (sequence, head); a wavefront 16 columns of K, all V rows of the transposed states in its registers.
+// YF: dq and dk in fp32 per v head.
+template <bool BF, int K, int V, bool YF>
+__global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A) {
+    using L = GradLds<BF, K, V>;
+    using RK = Rows<BF, K>;
+    using RV = Rows<BF, V>;
+    using RC = Rows<BF, kChunkTokens>;
+    constexpr int NW = K / 16, NT = NW * 64, VT = V / 16, VC = V / 32, C = kChunkTokens, NP = L::NP;
+    constexpr int EB = BF ? 2 : 4;
+    __shared__ __align__(16) char smem[L::bytes];
+    char *const s_do = smem + L::dout, *const s_z = smem + L::z, *const s_dw = smem + L::dw, *const s_k = smem + L::k,
+         *const s_q = smem + L::q, *const s_m1 = smem + L::m1, *const s_m2 = smem + L::m2;
+    float *const s_wt = reinterpret_cast<float *>(smem + L::wt), *const s_red = reinterpret_cast<float *>(smem + L::red);
+    float(*const s_u)[C] = reinterpret_cast<float(*)[C]>(smem + L::u);
+    float *const s_db = reinterpret_cast<float *>(smem + L::db);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
+              li = lane & 15;
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, slot = blk / A.c.H;
+    const int h = (int)(blk - slot * A.c.H), group = A.c.H / A.c.Hk;
+    if (slot >= A.c.segs) return;
+    const int64_t n = find_seq<true>(A.c, slot, lane);
+    const Seq sq = seq_of(A.c, n);
+    const int64_t len = sq.t1 - sq.t0;
+    const int all = (int)((len + C - 1) / C);  // the sequence's chunks
+    if (slot < sq.seg || (slot - sq.seg) * kSegmentChunks >= all) return;
+    const int c0 = (int)(slot - sq.seg) * kSegmentChunks, c1 = c0 + kSegmentChunks < all ? c0 + kSegmentChunks : all;
+    const int nch = c1 - c0, col = wave * 16;
+    const int64_t sstate = (int64_t)K * V, nh = n * A.c.H + h;
+
+    // a state [K][V] in memory as tiles of its transpose
+    auto add_state = [&](const float *s, f32x4 (&st)[VT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt)
+            st[vt] = s ? *reinterpret_cast<const f32x4 *>(s + (int64_t)(col + li) * V + RV::state_row(vt, g)) : zero4();
+    };
+    f32x4 st[VT];
+    add_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
+    hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
+
+    const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (V * EB);
+    const char *pk = reinterpret_cast<const char *>(A.k) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
+    const char *pq = reinterpret_cast<const char *>(A.q) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
+    const char *pd = reinterpret_cast<const char *>(A.dout) + (sq.t0 * A.c.H + h) * (V * EB);
+    const int64_t tile = (int64_t)V * (C * 4);
+    Stage<BF, K, C, NT> rk, rq;
+    Stage<BF, V, C, NT> rd;
+    Stage<BF, C, V, NT> rz[NP], rw[NP];
+    u32x4 rwt;
+    auto take = [&](int c) __attribute__((always_inline)) {
+        const int64_t t = (int64_t)c * C, at = (sq.first + c) * A.c.H + h;
+        const int m = (int)(len - t < C ? len - t : C);
+        rk.take(tid, pk + t * lk, lk, m);
+        rq.take(tid, pq + t * lk, lk, m);
+        rd.take(tid, pd + t * lv, lv, m);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            rz[p].take(tid, A.z + at * tile + p * (V * C * EB), C * EB, V);
+            rw[p].take(tid, A.dw + at * tile + p * (V * C * EB), C * EB, V);
+        }
+        rwt = *reinterpret_cast<const u32x4 *>(A.c.rec + at * rec_bytes(true) + rec_weights(true) + (tid & 63) * 16);
+    };
+    auto put = [&]() __attribute__((always_inline)) {
+        rk.put(tid, s_k);
+        rq.put(tid, s_q);
+        rd.put(tid, s_do);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            rz[p].put(tid, s_z + p * L::T_);
+            rw[p].put(tid, s_dw + p * L::T_);
+        }
+        if (tid < 64) *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(s_wt) + tid * 16) = rwt;
+    };
+    const int rowv0 = RV::row_at(lane), colc0 = RC::col_at(lane), rowc0 = RC::row_at(lane);
+    const int colk0 = BF ? RK::col_at(lane) ^ (wave << 5) : RK::col_at(lane) + 64 * wave, tilev0 = RV::tile_at(lane);
+    // V channels (32 vc ..) x tokens (16 tt + l % 16) of a [V][32] tile
+    auto tile_cols = [&](const char *s, int vc, int tt) __attribute__((always_inline)) {
+        Pair<BF> p;
+        if constexpr (BF) {
+            p.hi = RC::col_frag(s + 32 * vc * RC::RB, colc0, tt);
+            p.lo = RC::col_frag(s + L::T_ + 32 * vc * RC::RB, colc0, tt);
+        } else {
+            p.f = RC::col_frag(s + 32 * vc * RC::RB, colc0, tt);
+        }
+        return p;
+    };
+    // rows of the state's tile vt x the chunk's tokens
+    const int rows0 = tok_row_at<BF, C>(lane);
+    auto tile_rows = [&](const char *s, int vt) __attribute__((always_inline)) {
+        Pair<BF> p;
+        if constexpr (BF) {
+            p.hi = tok_row_frag<true, C>(s + 32 * (vt >> 1) * RC::RB, rows0, vt & 1, 0);
+            p.lo = tok_row_frag<true, C>(s + L::T_ + 32 * (vt >> 1) * RC::RB, rows0, vt & 1, 0);
+        } else {
+            p.f = RC::row_frag(s + 16 * vt * RC::RB, rowc0, 0);
+        }
+        return p;
+    };
+    auto mat_row = [&](const char *s, int tt) __attribute__((always_inline)) {
+        Pair<BF> p;
+        if constexpr (BF) {
+            p.hi = RC::row_frag(s + 16 * tt * RC::RB, rowc0, 0);
+            p.lo = RC::row_frag(s + L::M_ + 16 * tt * RC::RB, rowc0, 0);
+        } else {
+            p.f = RC::row_frag(s + 16 * tt * RC::RB, rowc0, 0);
+        }
+        return p;
+    };
+    auto put_mat = [&](char *s, int row, int c, const f32x4 &w) __attribute__((always_inline)) {
+        const int at = RC::quad(row, c);
+        if constexpr (BF) {
+            uint2 hi, lo;
+            split_bf16(w.x, w.y, hi.x, lo.x);
+            split_bf16(w.z, w.w, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(s + at) = hi;
+            *reinterpret_cast<uint2 *>(s + L::M_ + at) = lo;
+        } else {
+            *reinterpret_cast<f32x4 *>(s + at) = w;
+        }
+    };
+    auto clear_mats = [&]() __attribute__((always_inline)) {  // the tiles across the diagonal are read, never computed
+        for (int i = tid; i < 2 * NP * L::M_ / 16; i += NT) reinterpret_cast<uint4 *>(s_m1)[i] = make_uint4(0, 0, 0, 0);
+    };
+    auto weights = [&](int which, float (&w)[8]) __attribute__((always_inline)) {
+        *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of<BF>(0, g));
+        *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of<BF>(1, g));
+    };
+    // e^{b_r - b_i} of a lane's four rows against one token
+    auto decays = [&](int t, int s0, bool later, f32x4 &e) __attribute__((always_inline)) {
+        const float th = s_wt[kSumHi * C + t], tl = s_wt[kSumLo * C + t];
+        const f32x4 sh = *reinterpret_cast<const f32x4 *>(s_wt + kSumHi * C + s0);
+        const f32x4 sl = *reinterpret_cast<const f32x4 *>(s_wt + kSumLo * C + s0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            e[i] = __builtin_amdgcn_exp2f(later ? (sh[i] - th) + (sl[i] - tl) : (th - sh[i]) + (tl - sl[i]));
+    };
+    // a token's dot of rows x with a result y (columns 4g + i of token 16 tt + l % 16), over this wavefront's columns
+    auto dot = [&](const char *x, int tt, const f32x4 &y) __attribute__((always_inline)) {
+        float r[4];
+        RK::load_quad(x, 16 * tt + li, col + 4 * g, r);
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d = fmaf(r[i], y[i], d);
+        return d;
+    };
+    auto store = [&](void *p, int64_t t, const f32x4 &y, bool live) __attribute__((always_inline)) {
+        if (!live) return;
+        const int64_t at = (t * A.c.H + h) * K + col + 4 * g;
+        if constexpr (BF && !YF)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + at) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        else
+            *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p) + at) = y;
+    };
+
+    // y += the first matrix times the rows at s (f, x: this wavefront's columns of them); see all_finite
+    auto mix = [&](f32x4 (&y)[2], const Frag8<BF> &f, const float (&x)[8], const char *s, bool later, int m)
+                   __attribute__((always_inline)) {
+        if (all_finite(x)) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], f, mat_row(s_m1, tt));
+            return;
+        }
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {
+            float r[4];
+            RK::load_quad(s, j, col + 4 * g, r);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                const int t = 16 * tt + li;
+                float w = RC::load_one(s_m1, t, j);
+                if constexpr (BF) w += RC::load_one(s_m1 + L::M_, t, j);
+                if (later ? j >= t : j <= t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[tt][i] = fmaf(w, r[i], y[tt][i]);
+            }
+        }
+    };
+
+    // ================================================================ forward in time
+    take(c0);
+    clear_mats();
+    for (int c = c0; c < c1; ++c) {
+        const int64_t tc = sq.t0 + (int64_t)c * C;
+        const int m = (int)(sq.t1 - tc < C ? sq.t1 - tc : C);
+        __syncthreads();  // the last chunk's rows and matrices are read
+        put();
+        if (c + 1 < c1) take(c + 1);
+        else take(c);  // the walk back begins with the last one
+        __syncthreads();
+        // ---- the pairs' weights: lane holds sources i = 16 ts + 4g .. of token r = 16 tt + l % 16
+        for (int p = wave; p < 6; p += NW) {
+            const int which = p >= 3, x = which ? p - 3 : p, tt = x > 0, ts = x > 1;
+            f32x4 acc = zero4(), e;
+            const int r = 16 * tt + li, i0 = 16 * ts + 4 * g;
+#pragma unroll
+            for (int vc = 0; vc < VC; ++vc) {
+                const Pair<BF> z = tile_cols(s_z, vc, ts);
+                if (which) acc = mm(acc, z, tile_cols(s_dw, vc, tt));
+                else acc = mm(acc, z, RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc));
+            }
+            decays(r, i0, false, e);
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(s_wt + kBeta * C + i0);
+            const float f = which ? -s_wt[kBeta * C + r] : A.scale;
+            mfma_fence(acc);
+            if (which && tt == ts && r < m) {  // M's diagonal
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i0 + i == r) {
+                        const int64_t at = (tc + r) * A.c.H + h;
+                        if (BF && !A.gates_fp32) IO<true>::st(reinterpret_cast<uint16_t *>(A.dbeta), at, acc[i]);
+                        else reinterpret_cast<float *>(A.dbeta)[at] = acc[i];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i] = (which ? i0 + i < r : i0 + i <= r) && r < m ? f * acc[i] * e[i] * be[i] : 0.f;
+            put_mat(which ? s_m2 : s_m1, r, i0, acc);
+        }
+        // ---- what the state gives
+        f32x4 y1[2] = {zero4(), zero4()}, y2[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int vc = 0; vc < VC; ++vc) {
+            const Pair<BF> s = pair_of<BF>(st[2 * vc], st[2 * vc + 1]);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                y1[tt] = mm(y1[tt], s, RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc));
+                y2[tt] = mm(y2[tt], s, tile_cols(s_dw, vc, tt));
+            }
+        }
+        mfma_fence(y1[0], y1[1], y2[0], y2[1]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const int t = 16 * tt + li;
+            y1[tt] *= s_wt[kEnterScaled * C + t];
+            y2[tt] *= -s_wt[kEnter * C + t] * s_wt[kBeta * C + t];
+        }
+        __syncthreads();
+        const Frag8<BF> kf = RK::col_frag(s_k, colk0, 0);
+        float kx[8];
+        widen(kf, kx);
+        mix(y1, kf, kx, s_k, false, m);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) y2[tt] = mm(y2[tt], kf, mat_row(s_m2, tt));
+        // ---- the state's update
+        const float total = s_wt[kTotal * C];
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) st[vt] *= total;
+        {
+            float w[8];
+            weights(kLeaveBeta, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] *= kx[i];
+            Pair<BF> kp;
+            set_pair(kp, w);
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt) st[vt] = mm(st[vt], tile_rows(s_z, vt), kp);
+        }
+        // ---- results
+        mfma_fence(y1[0], y1[1], y2[0], y2[1]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const int t = 16 * tt + li;
+            store(A.dq, tc + t, y1[tt], t < m);
+            if (t < m) *reinterpret_cast<f32x4 *>(A.dk_part + ((tc + t) * A.c.H + h) * K + col + 4 * g) = y2[tt];
+            float d = dot(s_q, tt, y1[tt]) + dot(s_k, tt, y2[tt]);
+            d += __shfl_xor(d, 16);
+            d += __shfl_xor(d, 32);
+            if (g == 0) s_u[wave][t] = d;
+        }
+        __syncthreads();
+        if (tid < C) {
+            float d = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
+            s_db[(c - c0) * C + tid] = tid < m ? d : 0.f;
+        }
+        hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
+    }
+    // ---- what the border behind the segment passes on
+    f32x4 gt[VT];
+    add_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
+    float border = 0.f;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) border = fmaf(gt[vt][i], st[vt][i], border);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) border += __shfl_xor(border, d);
+    if (lane == 0) s_red[wave] = border;
+    hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(gt));
+
+    // ================================================================ backward in time
+    __syncthreads();
+    clear_mats();
+    for (int c = c1 - 1; c >= c0; --c) {
+        const int64_t tc = sq.t0 + (int64_t)c * C;
+        const int m = (int)(sq.t1 - tc < C ? sq.t1 - tc : C);
+        __syncthreads();
+        put();
+        if (c > c0) take(c - 1);
+        __syncthreads();
+        // ---- the pairs' weights the other way round: lane holds tokens j = 16 ts + 4g .. that see token r = 16 tt + l % 16
+        for (int p = wave; p < 6; p += NW) {
+            const int which = p >= 3, x = which ? p - 3 : p, ts = x > 0, tt = x > 1;
+            f32x4 acc = zero4(), e;
+            const int r = 16 * tt + li, j0 = 16 * ts + 4 * g;
+#pragma unroll
+            for (int vc = 0; vc < VC; ++vc) {
+                const Pair<BF> z = tile_cols(s_z, vc, tt);
+                if (which) acc = mm(acc, tile_cols(s_dw, vc, ts), z);
+                else acc = mm(acc, RV::row_frag(s_do + 16 * ts * RV::RB, rowv0, vc), z);
+            }
+            decays(r, j0, true, e);
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(s_wt + kBeta * C + j0);
+            const float f = s_wt[kBeta * C + r];
+            mfma_fence(acc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i] = (which ? j0 + i > r : j0 + i >= r) && j0 + i < m ? f * acc[i] * e[i] * (which ? -be[i] : A.scale) : 0.f;
+            put_mat(which ? s_m2 : s_m1, r, j0, acc);
+        }
+        f32x4 y[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int vc = 0; vc < VC; ++vc) {
+            const Pair<BF> s = pair_of<BF>(gt[2 * vc], gt[2 * vc + 1]);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], s, tile_cols(s_z, vc, tt));
+        }
+        mfma_fence(y[0], y[1]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) y[tt] *= s_wt[kLeaveBeta * C + 16 * tt + li];
+        __syncthreads();
+        const Frag8<BF> kf = RK::col_frag(s_k, colk0, 0), qf = RK::col_frag(s_q, colk0, 0);
+        float qx[8], kx[8];
+        widen(qf, qx);
+        widen(kf, kx);
+        mix(y, qf, qx, s_q, true, m);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], kf, mat_row(s_m2, tt));
+        // ---- the state gradient's update
+        const float total = s_wt[kTotal * C];
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) gt[vt] *= total;
+        {
+            float w[8], e[8], be[8];
+            weights(kEnterScaled, w);
+            weights(kEnter, e);
+            weights(kBeta, be);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                w[i] *= qx[i];
+                e[i] *= -be[i] * kx[i];
+            }
+            Pair<BF> qp, kp;
+            set_pair(qp, w);
+            set_pair(kp, e);
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt) {
+                gt[vt] = mm(gt[vt], RV::tile_frag(s_do, tilev0, vt), qp);
+                gt[vt] = mm(gt[vt], tile_rows(s_dw, vt), kp);
+            }
+        }
+        mfma_fence(y[0], y[1]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const int t = 16 * tt + li;
+            float d = dot(s_k, tt, y[tt]);
+            if (t < m) y[tt] += *reinterpret_cast<const f32x4 *>(A.dk_part + ((tc + t) * A.c.H + h) * K + col + 4 * g);
+            store(A.dk, tc + t, y[tt], t < m);
+            d += __shfl_xor(d, 16);
+            d += __shfl_xor(d, 32);
+            if (g == 0) s_u[wave][t] = d;
+        }
+        __syncthreads();
+        if (tid < C && tid < m) {
+            float d = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
+            s_db[(c - c0) * C + tid] -= d;
+        }
+        hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(gt));
+    }
+    __syncthreads();
+    // ---- dg: the sums from a token to the border, in fp64
+    if (wave == 0) {
+        constexpr int PER = kSegmentChunks * C / 64;
+        double own[PER], sum = 0.0, later = 0.0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+            const int t = lane * PER + i;
+            sum += t < nch * C ? (double)s_db[t] : 0.0;
+            own[i] = sum;
+        }
+        double upto = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double x = __shfl_down(upto, d);
+            if (lane + d < 64) upto += x;
+        }
+        later = upto - sum;
+        double b = 0.0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) b += s_red[w];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t t = sq.t0 + (int64_t)c0 * C + lane * PER + i;
+            const float x = (float)(own[i] + later + b);
+            if (t < sq.t1 && lane * PER + i < nch * C) {
+                if (BF && !A.gates_fp32) IO<true>::st(reinterpret_cast<uint16_t *>(A.dg), t * A.c.H + h, x);
+                else reinterpret_cast<float *>(A.dg)[t * A.c.H + h] = x;
+            }
+        }
+    }
+}
+
+template <bool BF, int K, int V, bool YF>
+hipError_t launch_grad(const GradArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((kda_gd_grad_kernel<BF, K, V, YF>), hd::wide_grid(a.c.segs * a.c.H), dim3(K * 4), 0, st, a);
+    return hipGetLastError();
+}
+template <bool BF, int K, bool YF>
+hipError_t grad_by_v(const GradArgs &a, int V, hipStream_t st) {
+    return V == 32   ? launch_grad<BF, K, 32, YF>(a, st)
+           : V == 64 ? launch_grad<BF, K, 64, YF>(a, st)
+                     : launch_grad<BF, K, 128, YF>(a, st);
+}
+template <bool BF, bool YF>
+hipError_t grad_by_k(const GradArgs &a, int K, int V, hipStream_t st) {
+    return K == 32   ? grad_by_v<BF, 32, YF>(a, V, st)
+           : K == 64 ? grad_by_v<BF, 64, YF>(a, V, st)
+                     : grad_by_v<BF, 128, YF>(a, V, st);
+}
+
+}  // namespace gd
+}  // namespace kda
