@@ -63,16 +63,15 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
 
 // ------------------------------------------------------------------ the chunks' records
 // One wavefront per (chunk, q/k head): the products k_r.k_i and q_r.k_i once, then for every v head that shares them the
-// decays, A and its inverse. N comes by substitution, a column in each lane (backward: N in lanes 0-31, N' in 32-63): row
-// r is minus row r of A times the rows before it.
+// decays, A and its inverse.
 constexpr int kPitch = kChunkTokens + 4;
 template <bool BF, bool GF, int K, bool BWD>
-__global__ __launch_bounds__(64, 3) void kda_gd_prep_kernel(const Common cm, const void *__restrict__ qp,
+__global__ __launch_bounds__(64) void kda_gd_prep_kernel(const Common cm, const void *__restrict__ qp,
                                                          const void *__restrict__ kp, const void *__restrict__ gp,
                                                          const void *__restrict__ bp, float scale) {
-    constexpr int C = kChunkTokens, KC = K / 32, EB = BF ? 2 : 4;
+    constexpr int C = kChunkTokens, KC = K / 32, EB = BF ? 2 : 4, NM = BWD ? 2 : 1;
     using GE = typename IO<!GF>::T;
-    __shared__ __align__(16) float s_a[BWD ? 2 : 1][C][kPitch], s_p[C][kPitch];
+    __shared__ __align__(16) float s_a[NM][C][kPitch], s_p[C][kPitch];
     __shared__ __align__(16) float s_bh[C], s_bl[C], s_be[C];
     const int lane = threadIdx.x, g = lane >> 4, li = lane & 15;
     const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, slot = blk / cm.Hk;
@@ -176,41 +175,88 @@ __global__ __launch_bounds__(64, 3) void kda_gd_prep_kernel(const Common cm, con
             *reinterpret_cast<f32x4 *>(&s_p[r][i0]) = w;
         }
         __syncthreads();
-        // ---- (1 + A)^-1 by columns
-        float(*const A)[kPitch] = s_a[BWD ? lane >> 5 : 0];
-        float inv[C];
+        // ---- the strict part N of (1 + A)^-1, in A's place (backward: both matrices)
+        bool usual = true;
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            f32x4 sum = zero4();
+        for (int m = 0; m < NM; ++m) {
+            float s = 0.f;
 #pragma unroll
-            for (int l = 0; l < r; l += 4) {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(&A[r][l]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (l + i < r) sum[i] = fmaf(a[i], inv[l + i], sum[i]);
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(&s_a[m][lane >> 1][16 * (lane & 1) + 4 * i]);
+                s = fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, fmaf(a.w, 0.f, s))));
             }
-            const float s = (sum.x + sum.y) + (sum.z + sum.w);
-            inv[r] = r == t ? 1.f : r > t ? -s : 0.f;
+            usual = usual && s == 0.f;
         }
-        __syncthreads();
-        if (BWD || lane < C)
+        if (__builtin_amdgcn_ballot_w64(!usual) == 0) {
+            // The blocks on the diagonal by substitution, a column in each lane: row r is minus row r of A times the rows
+            // before it. Then the block below them, -(1 + N_11) A_10 (1 + N_00).
+            float inv[16];
+            {
+                float(*const A)[kPitch] = s_a[NM == 2 ? g >> 1 : 0];
+                const int o = 16 * (g & 1);
 #pragma unroll
-            for (int r = 0; r < C; ++r) A[r][t] = r > t ? inv[r] : 0.f;
-        __syncthreads();
+                for (int r = 0; r < 16; ++r) {
+                    f32x4 sum = zero4();
+#pragma unroll
+                    for (int l = 0; l < r; l += 4) {
+                        const f32x4 a = *reinterpret_cast<const f32x4 *>(&A[o + r][o + l]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (l + i < r) sum[i] = fmaf(a[i], inv[l + i], sum[i]);
+                    }
+                    inv[r] = r == li ? 1.f : -((sum.x + sum.y) + (sum.z + sum.w));
+                }
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < 16; ++r) A[o + r][o + li] = inv[r];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                float(*const A)[kPitch] = s_a[m];
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(&A[16 + li][4 * g]);
+                const f32x4 c = *reinterpret_cast<const f32x4 *>(&A[16 + li][16 + 4 * g]);
+                f32x4 x = zero4(), y = zero4();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], A[4 * g + i][li], x, 0, 0, 0);
+                mfma_fence(x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y = __builtin_amdgcn_mfma_f32_16x16x4f32(c[i], x[i], y, 0, 0, 0);
+                mfma_fence(y);
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    A[16 + 4 * g + i][li] = -y[i];
+                    if (li == 4 * g + i) A[li][li] = A[16 + li][16 + li] = 0.f;
+                }
+            }
+            __syncthreads();
+        } else {
+            // Something is not finite: row by row and no zeros times it, for the rows before it keep their values.
+            for (int m = 0; m < NM; ++m)
+                for (int r = 0; r < C; ++r) {
+                    float s = 0.f;
+                    for (int l = 0; l < r; ++l)
+                        s += l == t ? s_a[m][r][l] : l > t ? s_a[m][r][l] * s_a[m][l][t] : 0.f;
+                    __syncthreads();
+                    if (lane < C && t < r) s_a[m][r][t] = -s;
+                    __syncthreads();
+                }
+        }
         // ---- as operands
         auto rows = [&](const float (&m)[C][kPitch], int r, float (&x)[8]) __attribute__((always_inline)) {
-            *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(&m[r][token_of<BF>(0, g)]);
-            *reinterpret_cast<f32x4 *>(x + 4) = *reinterpret_cast<const f32x4 *>(&m[r][token_of<BF>(1, g)]);
+            *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(&m[r][token_of(0, g)]);
+            *reinterpret_cast<f32x4 *>(x + 4) = *reinterpret_cast<const f32x4 *>(&m[r][token_of(1, g)]);
         };
         auto cols = [&](const float (&m)[C][kPitch], int c, float (&x)[8]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = m[slot_token<BF>(g, j)][c];
+            for (int j = 0; j < 8; ++j) x[j] = m[slot_token(g, j)][c];
         };
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
             float x[8];
             Pair<BF> f;
-            rows(s_a[0], token_row<BF>(tt, li), x);
+            rows(s_a[0], 16 * tt + li, x);
             set_pair(f, x);
             store_mat(rec + kMatN * kMatBytes, tt, lane, f);
             if constexpr (!BWD) {
@@ -218,10 +264,10 @@ __global__ __launch_bounds__(64, 3) void kda_gd_prep_kernel(const Common cm, con
                 set_pair(f, x);
                 store_mat(rec + kMatP * kMatBytes, tt, lane, f);
             } else {
-                cols(s_a[BWD], token_row<BF>(tt, li), x);
+                cols(s_a[BWD], 16 * tt + li, x);
                 set_pair(f, x);
                 store_mat(rec + kMatNT * kMatBytes, tt, lane, f);
-                cols(s_p, token_row<BF>(tt, li), x);
+                cols(s_p, 16 * tt + li, x);
                 set_pair(f, x);
                 store_mat(rec + kMatPT * kMatBytes, tt, lane, f);
             }

@@ -33,11 +33,24 @@ template <bool BF> struct Pair;
 template <> struct Pair<true> { Frag8<true> hi, lo; };
 template <> struct Pair<false> { Frag8<false> f; };
 
+// What rounding a pair left of its first (second) value: x - hi, exact, in one instruction. Where the pair's other value
+// is not finite the result is NaN: only for pairs that are summed over, or of finite values. (-1 comes in a register: as
+// an inline constant the instruction takes it for the upper half's.)
+__device__ __forceinline__ float rest_lo(float x, uint32_t hi) {
+    uint32_t one = 0x0000bf80u;
+    asm("" : "+s"(one));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, hi), __builtin_bit_cast(bf16x2, one), x, false);
+}
+__device__ __forceinline__ float rest_hi(float x, uint32_t hi) {
+    uint32_t one = 0xbf800000u;
+    asm("" : "+s"(one));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, hi), __builtin_bit_cast(bf16x2, one), x, false);
+}
 __device__ __forceinline__ void set_pair(Pair<true> &p, const float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        p.hi.p[i] = hd::seen(pack_bf16(x[2 * i], x[2 * i + 1]));
-        p.lo.p[i] = pack_bf16(x[2 * i] - bf_lo(p.hi.p[i]), x[2 * i + 1] - bf_hi(p.hi.p[i]));
+        p.hi.p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        p.lo.p[i] = pack_bf16(rest_lo(x[2 * i], p.hi.p[i]), rest_hi(x[2 * i + 1], p.hi.p[i]));
     }
 }
 __device__ __forceinline__ void set_pair(Pair<false> &p, const float (&x)[8]) {
@@ -56,10 +69,10 @@ template <bool BF> constexpr int kParts = BF ? 3 : 1;
 __device__ __forceinline__ void set_parts(Frag8<true> (&f)[3], const float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[0].p[i] = hd::seen(pack_bf16(x[2 * i], x[2 * i + 1]));
-        const float a = x[2 * i] - bf_lo(f[0].p[i]), b = x[2 * i + 1] - bf_hi(f[0].p[i]);
-        f[1].p[i] = hd::seen(pack_bf16(a, b));
-        f[2].p[i] = pack_bf16(a - bf_lo(f[1].p[i]), b - bf_hi(f[1].p[i]));
+        f[0].p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        const float a = rest_lo(x[2 * i], f[0].p[i]), b = rest_hi(x[2 * i + 1], f[0].p[i]);
+        f[1].p[i] = pack_bf16(a, b);
+        f[2].p[i] = pack_bf16(rest_lo(a, f[1].p[i]), rest_hi(b, f[1].p[i]));
     }
 }
 __device__ __forceinline__ void set_parts(Frag8<false> (&f)[1], const float (&x)[8]) {
@@ -96,17 +109,196 @@ __device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<true> &a, const Frag8<tr
 }
 __device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<false> &a, const Frag8<false> &b) { return mma32(c, a.f, b); }
 
-// ------------------------------------------------------------------ tokens
-// An accumulator of 32 tokens is two tiles of 16 rows; row m of tile tt is the token that slot 4 tt + m % 4 of lane group
-// m / 4 stands for, so the two tiles are, as they are, an operand whose slots are the chunk's tokens.
-template <bool BF> __device__ __forceinline__ int token_of(int tt, int g) {  // of row 4g (the next three follow)
-    return BF ? 8 * g + 4 * tt : 16 * tt + 4 * g;
+// Two products at a time, their steps in turn: a matrix instruction waits for the one before it on its accumulator.
+__device__ __forceinline__ const Frag8<true> &part_of(const Pair<true> &p, int i) { return i ? p.lo : p.hi; }
+__device__ __forceinline__ const Frag8<false> &part_of(const Pair<false> &p, int) { return p.f; }
+template <bool BF>
+__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Frag8<BF> (&a)[2], const Pair<BF> &b) {
+#pragma unroll
+    for (int p = 0; p < (BF ? 2 : 1); ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], a[t], part_of(b, p));
 }
-template <bool BF> __device__ __forceinline__ int token_row(int tt, int m) {
-    return token_of<BF>(tt, m >> 2) + (m & 3);
+template <bool BF>
+__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> &a, const Frag8<BF> (&b)[2]) {
+#pragma unroll
+    for (int p = 0; p < (BF ? 2 : 1); ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a, p), b[t]);
 }
-template <bool BF> __device__ __forceinline__ int slot_token(int g, int j) { return token_of<BF>(j >> 2, g) + (j & 3); }
+template <bool BF>
+__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> (&a)[2], const Frag8<BF> (&b)[2]) {
+#pragma unroll
+    for (int p = 0; p < (BF ? 2 : 1); ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a[t], p), b[t]);
+}
+// (the two small parts' own product is left out)
+template <bool BF>
+__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> (&a)[2], const Pair<BF> &b) {
+#pragma unroll
+    for (int p = 0; p < (BF ? 3 : 1); ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a[t], p == 2), part_of(b, p == 1));
+}
+template <bool BF>
+__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> &a, const Pair<BF> (&b)[2]) {
+#pragma unroll
+    for (int p = 0; p < (BF ? 3 : 1); ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a, p == 2), part_of(b[t], p == 1));
+}
+// The compiler would sink loads to where they are used.
+#define KDA_ORDER __builtin_amdgcn_sched_barrier(0)
 
+// ------------------------------------------------------------------ tokens
+// An accumulator of 32 tokens is two tiles of 16; slot 4 tt + i of lane group g is row 4g + i of tile tt, token 16 tt + 4g
+// + i. So the two tiles are, as they are, an operand whose slots are the chunk's tokens.
+__device__ __forceinline__ int token_of(int tt, int g) { return 16 * tt + 4 * g; }
+__device__ __forceinline__ int slot_token(int g, int j) { return token_of(j >> 2, g) + (j & 3); }
+
+// ------------------------------------------------------------------ rows in LDS
+// NCOL elements a row. bf16: the 16-byte slots of a row are permuted by an exclusive or with its index, so that 16 rows
+// at one slot (the lanes of a row read) and 8 rows at two adjacent ones (of a transposing read) fall on different banks.
+// fp32: rows padded by 16 bytes to the same end. Channels: slots 0-7 of a 32-deep product are channels 32c + 8g + j (bf16,
+// one 16-byte read) or 4g + i and 16 + 4g + i (fp32), and a state's tile kt has its rows in the same order.
+template <bool BF, int NCOL> struct Rw;
+template <int NCOL> struct Rw<true, NCOL> {
+    static constexpr int NS = NCOL / 8, RB = NCOL * 2;
+    static constexpr int bytes(int rows) { return rows * RB; }
+    static __device__ __forceinline__ int swz(int row) {
+        const int line = NCOL == 128 ? row & 7 : NCOL == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+        return (line << 1) | ((row >> 3) & 1);
+    }
+    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + ((s ^ swz(row)) << 4); }
+    static __device__ __forceinline__ int state_row(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
+    // channels 32c .. 32c + 31 of row l % 16 (+ what is added to t)
+    static __device__ __forceinline__ int row_at(int lane) { return slot(lane & 15, lane >> 4); }
+    static __device__ __forceinline__ Frag8<true> row_frag(const char *t, int at, int c) {
+        const u32x4 u = *reinterpret_cast<const u32x4 *>(t + (at ^ (c << 6)));
+        return Frag8<true>{{u.x, u.y, u.z, u.w}};
+    }
+    // The transposing read gives lane i of sixteen column i of a 4 x 16 block, of which its lane j holds the four elements
+    // j % 4 of row j / 4. Rows 4g .. and, from `next` bytes on, the second four.
+    static __device__ __forceinline__ Frag8<true> tr_frag(const char *t, int next) {
+        typedef __attribute__((address_space(3))) s16x4 *lds4;
+        const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t)));
+        const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(t + next)));
+        return Frag8<true>{{a.x, a.y, b.x, b.y}};
+    }
+    // the chunk's tokens at column 16w + l % 16
+    static __device__ __forceinline__ int col_at(int lane, int w) {
+        return slot(4 * (lane >> 4) + ((lane >> 2) & 3), 2 * w + ((lane >> 1) & 1)) + (lane & 1) * 8;
+    }
+    static __device__ __forceinline__ Frag8<true> col_frag(const char *t, int at) { return tr_frag(t + at, 16 * RB); }
+    // the chunk's tokens at the channels of a state's tile kt
+    static __device__ __forceinline__ int tile_at(int lane) {
+        return slot(4 * (lane >> 4) + ((lane >> 2) & 3), lane & 3);
+    }
+    static __device__ __forceinline__ Frag8<true> tile_frag(const char *t, int at, int kt) {
+        return tr_frag(t + (at ^ (kt >> 1 << 6)) + 8 * (kt & 1), 16 * RB);
+    }
+    static __device__ __forceinline__ int quad(int row, int col) { return slot(row, col >> 3) + ((col & 4) << 1); }
+    static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, col));
+        x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+    }
+    static __device__ __forceinline__ float load_one(const char *t, int row, int col) {
+        return bf2f(*reinterpret_cast<const uint16_t *>(t + quad(row, col) + 2 * (col & 3)));
+    }
+};
+template <int NCOL> struct Rw<false, NCOL> {
+    static constexpr int NS = NCOL / 4, RB = (NCOL + 4) * 4;
+    static constexpr int bytes(int rows) { return rows * RB; }
+    static __device__ __forceinline__ int slot(int row, int s) { return row * RB + (s << 4); }
+    static __device__ __forceinline__ int state_row(int kt, int g) { return 16 * kt + 4 * g; }
+    static __device__ __forceinline__ int row_at(int lane) { return slot(lane & 15, lane >> 4); }
+    static __device__ __forceinline__ Frag8<false> row_frag(const char *t, int at, int c) {
+        const f32x4 u = *reinterpret_cast<const f32x4 *>(t + at + 128 * c);
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(t + at + 128 * c + 64);
+        return Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
+    }
+    static __device__ __forceinline__ int col_at(int lane, int w) {
+        return 4 * (lane >> 4) * RB + (16 * w + (lane & 15)) * 4;
+    }
+    static __device__ __forceinline__ Frag8<false> col_frag(const char *t, int at) {
+        Frag8<false> f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.f[j] = *reinterpret_cast<const float *>(t + at + j * RB);
+            f.f[4 + j] = *reinterpret_cast<const float *>(t + at + (16 + j) * RB);
+        }
+        return f;
+    }
+    static __device__ __forceinline__ int tile_at(int lane) { return col_at(lane, 0); }
+    static __device__ __forceinline__ Frag8<false> tile_frag(const char *t, int at, int kt) { return col_frag(t + 64 * kt, at); }
+    static __device__ __forceinline__ int quad(int row, int col) { return row * RB + col * 4; }
+    static __device__ __forceinline__ void load_quad(const char *t, int row, int col, float (&x)[4]) {
+        const f32x4 u = *reinterpret_cast<const f32x4 *>(t + quad(row, col));
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    }
+    static __device__ __forceinline__ float load_one(const char *t, int row, int col) {
+        return *reinterpret_cast<const float *>(t + quad(row, col));
+    }
+};
+
+// C rows on their way to LDS, `pitch` bytes apart: a lane's offsets are made once, a chunk's place goes into the buffer's
+// descriptor, and rows behind the last of `n` come as zeros (past the buffer's end). take() issues the loads, put() waits
+// for them: a chunk's rows travel while the one before it is worked on.
+template <bool BF, int NCOL, int C, int NT>
+struct RowsIn {
+    static constexpr int NS = Rw<BF, NCOL>::NS, RL = NT / NS;  // rows per round of loads
+    static constexpr int NL = C > RL ? C / RL : 1, SIZE = NCOL * (BF ? 2 : 4);
+    static_assert(NT % NS == 0 && C % (RL < C ? RL : C) == 0, "whole rounds of whole rows");
+    uint32_t from[NL], pitch;
+    int to[NL];
+    u32x4 w[NL];
+    __device__ __forceinline__ void init(int tid, uint32_t bytes) {
+        pitch = bytes;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            int row = tid / NS + i * RL;
+            if (RL > C) row &= C - 1;  // lanes left over bring a row once more
+            from[i] = row * pitch + (tid % NS) * 16;
+            to[i] = Rw<BF, NCOL>::slot(row, tid % NS);
+        }
+    }
+    __device__ __forceinline__ void take(const char *p, int n) {
+        const auto rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (n - 1) * pitch + SIZE, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, from[i], 0, 0);
+    }
+    __device__ __forceinline__ void put(char *t) const {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) *reinterpret_cast<u32x4 *>(t + to[i]) = w[i];
+    }
+};
+// The same for consecutive bytes.
+template <int BYTES, int NT>
+struct BytesIn {
+    static constexpr int NL = (BYTES / 16 + NT - 1) / NT;
+    static_assert(BYTES % 16 == 0, "16 bytes a load");
+    uint32_t at[NL];
+    u32x4 w[NL];
+    __device__ __forceinline__ void init(int tid) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            at[i] = (i * NT + tid) * 16;
+            if (at[i] >= BYTES) at[i] = BYTES - 16;  // lanes left over bring the last bytes once more
+        }
+    }
+    __device__ __forceinline__ void take(const char *p) {
+        const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, BYTES, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b128(b, at[i], 0, 0);
+    }
+    __device__ __forceinline__ void put(char *t) const {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) *reinterpret_cast<u32x4 *>(t + at[i]) = w[i];
+    }
+};
+
+// ------------------------------------------------------------------ records
 // A tile of a record's matrix as an operand, and one of its entries: row m of the tile, source slot j of lane group g.
 __device__ __forceinline__ void load_mat(const char *m, int tt, int lane, Pair<true> &p) {
     const u32x4 u = *reinterpret_cast<const u32x4 *>(m + ((2 * tt) * 64 + lane) * 16);
@@ -146,6 +338,15 @@ __device__ __forceinline__ bool all_finite(const float (&x)[8]) {
     for (int i = 0; i < 8; ++i) z = fmaf(x[i], 0.f, z);
     return __builtin_amdgcn_ballot_w64(z != 0.f) == 0;
 }
+// (Of a pair that rounds to an infinity the values count as such.)
+__device__ __forceinline__ bool finite(const Pair<true> &p) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p.hi.p[i]), __builtin_bit_cast(bf16x2, 0u), z, false);
+    return __builtin_amdgcn_ballot_w64(z != 0.f) == 0;
+}
+__device__ __forceinline__ bool finite(const Pair<false> &p) { return all_finite(p.f.f); }
 // acc[token][column] += sum over sources j of M[token][j] x_j[column], x in the lanes of their columns. REV: sources from
 // the token on, else up to it.
 template <bool BF, bool REV>
@@ -156,12 +357,12 @@ __device__ __forceinline__ void mix_rows(f32x4 (&acc)[2], const float (&x)[8], c
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float xs = __shfl(x[j], 16 * gs + li);
-            const int src = slot_token<BF>(gs, j);
+            const int src = slot_token(gs, j);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int t = token_of<BF>(tt, g) + i;
+                    const int t = token_of(tt, g) + i;
                     const float w = mat_entry<BF>(mat, tt, 4 * g + i, gs, j);
                     if (REV ? src >= t : src <= t) acc[tt][i] = fmaf(w, xs, acc[tt][i]);
                 }
@@ -175,7 +376,7 @@ __device__ __forceinline__ void mix_cols(f32x4 (&acc)[2], const float (&x)[8], c
     for (int gs = 0; gs < 4; ++gs)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int src = slot_token<BF>(gs, j);
+            const int src = slot_token(gs, j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float xs = __shfl(x[j], 16 * gs + 4 * g + i);
@@ -188,45 +389,11 @@ __device__ __forceinline__ void mix_cols(f32x4 (&acc)[2], const float (&x)[8], c
         }
 }
 
-// Consecutive bytes on their way to LDS.
-template <int BYTES, int NT>
-struct Copy {
-    static constexpr int NL = (BYTES / 16 + NT - 1) / NT;
-    static_assert(BYTES % 16 == 0, "16 bytes a load");
-    u32x4 w[NL];
-    __device__ __forceinline__ void take(int tid, const char *p) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int at = (i * NT + tid) * 16;
-            w[i] = *reinterpret_cast<const u32x4 *>(p + (at < BYTES ? at : BYTES - 16));
-        }
-    }
-    __device__ __forceinline__ void put(int tid, char *t) const {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int at = (i * NT + tid) * 16;
-            if (at < BYTES) *reinterpret_cast<u32x4 *>(t + at) = w[i];
-        }
-    }
-};
-
 // ------------------------------------------------------------------ the pass over the states
-// Rows 16-row tiles read at the tokens of token_row: the lane's address for tile 0, and how tile 1's differs from it.
-template <bool BF, int NCOL> __device__ __forceinline__ int tok_row_at(int lane) {
-    if constexpr (BF) return Rows<true, NCOL>::slot(token_row<true>(0, lane & 15), lane >> 4);
-    else return Rows<false, NCOL>::row_at(lane);
-}
-template <bool BF, int NCOL>
-__device__ __forceinline__ Frag8<BF> tok_row_frag(const char *t, int at, int tt, int c) {
-    using R = Rows<BF, NCOL>;
-    if constexpr (BF) return R::row_frag(t + (tt ? 4 * R::RB : 0), tt ? at ^ 16 : at, c);
-    else return R::row_frag(t + 16 * tt * R::RB, at, c);
-}
-
 template <bool BF, int K, int VT, int MODE>
 struct StateLds {
     static constexpr int C = kChunkTokens, NB = BF ? 2 : 1;
-    static constexpr int K_ = Rows<BF, K>::bytes(C), V_ = Rows<BF, VT>::bytes(C), R_ = rec_bytes(MODE != kForward);
+    static constexpr int K_ = Rw<BF, K>::bytes(C), V_ = Rw<BF, VT>::bytes(C), R_ = rec_bytes(MODE != kForward);
     static constexpr int k = 0, q = k + NB * K_, v = q + (MODE == kErrors ? 0 : NB * K_), rec = v + NB * V_;
     static constexpr int bytes = rec + NB * R_;
 };
@@ -236,8 +403,8 @@ struct StateLds {
 template <bool BF, int K, int VT, int MODE>
 __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs A, int V) {
     using L = StateLds<BF, K, VT, MODE>;
-    using RK = Rows<BF, K>;
-    using RV = Rows<BF, VT>;
+    using RK = Rw<BF, K>;
+    using RV = Rw<BF, VT>;
     constexpr int NW = VT / 16, NT = NW * 64, KT = K / 16, KC = K / 32, C = kChunkTokens, NB = L::NB;
     constexpr int EB = BF ? 2 : 4;
     constexpr bool REV = MODE == kReverse;
@@ -253,8 +420,8 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
     const int h = (int)(item - n * A.c.H), group = A.c.H / A.c.Hk;
     if (n >= A.c.N) return;
     const Seq sq = seq_of(A.c, n);
-    const int64_t len = sq.t1 - sq.t0;
-    const int nch = (int)((len + C - 1) / C);
+    const int len = (int)(sq.t1 - sq.t0);  // under 2^31
+    const int nch = (int)(((int64_t)len + C - 1) / C);
     const int col = vt * VT + wave * 16;  // this wavefront's first column
 
     // ---- the state at its start
@@ -280,169 +447,175 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 
     hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][KT]>(st));  // the loads end here: no waits for them in the loop
 
+    // ---- the rows' ways
     const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (uint32_t)(V * EB);
-    const char *pk = reinterpret_cast<const char *>(A.k) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
-    const char *pq = reinterpret_cast<const char *>(A.q) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
-    const char *pv = reinterpret_cast<const char *>(A.v) + ((sq.t0 * A.c.H + h) * V + vt * VT) * EB;
     constexpr int RECB = L::R_;
-    const char *prec = A.c.rec + (sq.first * A.c.H + h) * RECB;
-    const int64_t rec_step = (int64_t)A.c.H * RECB;
-
-    Stage<BF, K, C, NT> rk, rq;
-    Stage<BF, VT, C, NT> rv;
-    Copy<RECB, NT> rr;
-    auto chunk_of = [&](int i) __attribute__((always_inline)) { return REV ? nch - 1 - i : i; };
-    auto take = [&](int i) __attribute__((always_inline)) {
-        const int64_t c = chunk_of(i), t = c * C;
-        const int m = (int)(len - t < C ? len - t : C);
-        rk.take(tid, pk + t * lk, lk, m);
-        if constexpr (MODE != kErrors) rq.take(tid, pq + t * lk, lk, m);
-        rv.take(tid, pv + t * lv, lv, m);
-        rr.take(tid, prec + c * rec_step);
+    RowsIn<BF, K, C, NT> rk, rq;
+    RowsIn<BF, VT, C, NT> rv;
+    BytesIn<RECB, NT> rr;
+    rk.init(tid, lk);
+    rq.init(tid, lk);
+    rv.init(tid, lv);
+    rr.init(tid);
+    // the next chunk to be asked for, and where it lies
+    const int64_t c_first = REV ? nch - 1 : 0, step = REV ? -1 : 1;
+    const char *pk = reinterpret_cast<const char *>(A.k) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
+    const char *pq = reinterpret_cast<const char *>(A.q) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
+    const char *pv = reinterpret_cast<const char *>(A.v) + (((sq.t0 + c_first * C) * A.c.H + h) * V + vt * VT) * EB;
+    const char *prec = A.c.rec + ((sq.first + c_first) * A.c.H + h) * RECB;
+    char *po = reinterpret_cast<char *>(A.o) + ((sq.t0 + c_first * C) * A.c.H + h) * V * EB;
+    const int64_t step_k = step * C * lk, step_v = step * C * lv, step_r = step * A.c.H * RECB;
+    auto tokens_of = [&](int c) __attribute__((always_inline)) { return len - c * C < C ? len - c * C : C; };
+    auto take = [&](int c) __attribute__((always_inline)) {
+        const int m = tokens_of(c);
+        rk.take(pk, m);
+        if constexpr (MODE != kErrors) rq.take(pq, m);
+        rv.take(pv, m);
+        rr.take(prec);
+        pk += step_k;
+        if constexpr (MODE != kErrors) pq += step_k;
+        pv += step_v;
+        prec += step_r;
     };
     auto put = [&](int b) __attribute__((always_inline)) {
-        rk.put(tid, smem + L::k + b * L::K_);
-        if constexpr (MODE != kErrors) rq.put(tid, smem + L::q + b * L::K_);
-        rv.put(tid, smem + L::v + b * L::V_);
-        rr.put(tid, smem + L::rec + b * L::R_);
+        rk.put(smem + L::k + b * L::K_);
+        if constexpr (MODE != kErrors) rq.put(smem + L::q + b * L::K_);
+        rv.put(smem + L::v + b * L::V_);
+        rr.put(smem + L::rec + b * L::R_);
     };
+    auto chunk_of = [&](int i) __attribute__((always_inline)) { return REV ? nch - 1 - i : i; };
     if (nch > 0) {
-        take(0);
+        take(chunk_of(0));
         if constexpr (NB == 2) {
             put(0);
-            if (nch > 1) take(1);
+            if (nch > 1) take(chunk_of(1));
         }
     }
-    const int tok0 = tok_row_at<BF, K>(lane), row0 = RK::row_at(lane), tile0 = RK::tile_at(lane);
-    const int col0 = BF ? RV::col_at(lane) ^ (wave << 5) : RV::col_at(lane) + 64 * wave;
-
+    const int row0 = RK::row_at(lane), tile0 = RK::tile_at(lane), col0 = RV::col_at(lane, wave);
+    Pair<BF> sf[KC];  // the state as an operand
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) sf[kc] = pair_of<BF>(st[2 * kc], st[2 * kc + 1]);
     for (int cc = 0; cc < nch; ++cc) {
         const int c = chunk_of(cc), b = cc & (NB - 1);
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
         if constexpr (NB == 1) {
             put(0);
-            if (cc + 1 < nch) take(cc + 1);
+            if (cc + 1 < nch) take(chunk_of(cc + 1));
             __syncthreads();
         } else if (cc + 1 < nch) {
             put(b ^ 1);
-            if (cc + 2 < nch) take(cc + 2);
+            if (cc + 2 < nch) take(chunk_of(cc + 2));
         }
         const char *sk = smem + L::k + b * L::K_, *sv = smem + L::v + b * L::V_, *sr = smem + L::rec + b * L::R_;
         const char *sq_ = smem + L::q + b * L::K_;
         (void)sq_;
         const float *wt = reinterpret_cast<const float *>(sr + rec_weights(MODE != kForward));
         auto weights = [&](int which, float (&w)[8]) __attribute__((always_inline)) {  // of the tokens in a lane's slots
-            *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of<BF>(0, g));
-            *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of<BF>(1, g));
+            *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of(0, g));
+            *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of(1, g));
         };
         if (MODE == kErrors && c > 0 && c % kSegmentChunks == 0)
             put_state(A.seed + ((sq.seg + c / kSegmentChunks) * A.c.H + h) * sstate);
         if (MODE == kReverse && c + 1 < nch && (c + 1) % kSegmentChunks == 0)
             put_state(A.seed + ((sq.seg + c / kSegmentChunks) * A.c.H + h) * sstate);
 
-        // ---- products with the state: K S, and S^T q
+        // ---- products with the state: K S, and S^T q. The operands are asked for ahead of the products.
         f32x4 x[2] = {zero4(), zero4()}, y[2] = {zero4(), zero4()};
+        Frag8<BF> kf[KC][2], qf[KC][2];
+        Pair<BF> mat[2];
+        float vx[8], r[8], z[8], w[8];
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-            const Pair<BF> s = pair_of<BF>(st[2 * kc], st[2 * kc + 1]);
+        for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) x[tt] = mm(x[tt], tok_row_frag<BF, K>(sk, tok0, tt, kc), s);
-            if constexpr (MODE == kForward)
+            for (int tt = 0; tt < 2; ++tt) kf[kc][tt] = RK::row_frag(sk + 16 * tt * RK::RB, row0, kc);
+        const Frag8<BF> vf = RV::col_frag(sv, col0);
+        weights(REV ? kLeave : kEnter, w);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], s, RK::row_frag(sq_ + 16 * tt * RK::RB, row0, kc));
-        }
-        const Frag8<BF> vf = RV::col_frag(sv, col0, 0);
-        float vx[8], z[8];
+        for (int tt = 0; tt < 2; ++tt) load_mat(sr + (REV ? kMatPT : kMatN) * kMatBytes, tt, lane, mat[tt]);
+        if constexpr (MODE == kForward)
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) qf[kc][tt] = RK::row_frag(sq_ + 16 * tt * RK::RB, row0, kc);
+        KDA_ORDER;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) mm2(x, kf[kc], sf[kc]);
+        KDA_ORDER;
+        if constexpr (MODE == kForward)
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc) mm2(y, sf[kc], qf[kc]);
+        KDA_ORDER;
         widen(vf, vx);
-        mfma_fence(x[0], x[1], y[0], y[1]);
+        mfma_fence(x[0], x[1]);
         if constexpr (!REV) {
             // ---- z = r + N r,  r = v - e^b K S
-            float w[8];
-            weights(kEnter, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = fmaf(-w[i], x[i >> 2][i & 3], vx[i]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = z[i];
-            if (all_finite(z)) {
-                Pair<BF> r, m;
-                set_pair(r, z);
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    load_mat(sr + kMatN * kMatBytes, tt, lane, m);
-                    x[tt] = mm(x[tt], m, r);
-                }
-            } else {
-                mix_rows<BF, false>(x, z, sr + kMatN * kMatBytes, lane);
-            }
+            for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = r[i] = fmaf(-w[i], x[i >> 2][i & 3], vx[i]);
         } else {
             // ---- D = e^{b_C - b} K G + P^T do, then dw = D + N'^T D
-            float w[8];
-            weights(kLeave, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] *= w[i];
-            if (all_finite(vx)) {
-                Pair<BF> m;
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    load_mat(sr + kMatPT * kMatBytes, tt, lane, m);
-                    x[tt] = mm(x[tt], m, vf);
-                }
+            const bool fine = all_finite(vx);
+            if (fine) {
+                const Frag8<BF> f[2] = {vf, vf};
+                mm2(x, mat, f);
             } else {
                 mix_rows<BF, true>(x, vx, sr + kMatPT * kMatBytes, lane);
             }
             mfma_fence(x[0], x[1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
-            if (all_finite(z)) {
-                Pair<BF> r, m;
-                set_pair(r, z);
+            for (int i = 0; i < 8; ++i) r[i] = x[i >> 2][i & 3];
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    load_mat(sr + kMatNT * kMatBytes, tt, lane, m);
-                    x[tt] = mm(x[tt], m, r);
-                }
-            } else {
-                mix_rows<BF, true>(x, z, sr + kMatNT * kMatBytes, lane);
+            for (int tt = 0; tt < 2; ++tt) load_mat(sr + kMatNT * kMatBytes, tt, lane, mat[tt]);
+        }
+        {
+            Pair<BF> rp;
+            set_pair(rp, r);
+            mm2(x, mat, rp);
+        }
+        KDA_ORDER;
+        // the update's operands, while those products run
+        Frag8<BF> kt_f[KT];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) kt_f[kt] = RK::tile_frag(sk, tile0, kt);
+        const float total = wt[kTotal * C];
+        if constexpr (!REV) weights(kLeaveBeta, w);
+        if constexpr (MODE == kForward) {
+            // ---- o^T = scale e^b S^T q + P z
+            mfma_fence(y[0], y[1]);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                y[tt] *= wt[kEnterScaled * C + 16 * tt + li];
+                load_mat(sr + kMatP * kMatBytes, tt, lane, mat[tt]);
             }
         }
+        KDA_ORDER;
         mfma_fence(x[0], x[1]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
-
-        if constexpr (MODE == kForward) {
-            // ---- o^T = scale e^b S^T q + P z
+        Pair<BF> zp;
+        set_pair(zp, z);
+        if (!finite(zp)) {  // a source that is not shows in its own row
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) y[tt] *= wt[kEnterScaled * C + 16 * tt + li];
-            if (all_finite(z)) {
-                Pair<BF> zp, m;
-                set_pair(zp, z);
+            for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = r[i];
+            mix_rows<BF, REV>(x, r, sr + (REV ? kMatNT : kMatN) * kMatBytes, lane);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    load_mat(sr + kMatP * kMatBytes, tt, lane, m);
-                    y[tt] = mm(y[tt], zp, m);
-                }
-            } else {
+            for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
+            if constexpr (MODE == kForward) {
                 mix_cols<BF>(y, z, sr + kMatP * kMatBytes, lane);
-            }
-            mfma_fence(y[0], y[1]);
-            const int64_t t = sq.t0 + (int64_t)c * C;
-            const int m = (int)(sq.t1 - t < C ? sq.t1 - t : C);
-            // the hardware drops the stores behind the chunk's last row (past the buffer's end)
-            const auto out = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<char *>(A.o) + (t * A.c.H + h) * V * EB, 0, (m - 1) * lv + V * EB, 0x00027000);
-            const uint32_t at = li * lv + (uint32_t)(col + 4 * g) * EB;
+                zp = Pair<BF>{};
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-                if constexpr (BF)
-                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(y[tt].x, y[tt].y), pack_bf16(y[tt].z, y[tt].w)},
-                                                          out, at + 16 * tt * lv, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[tt]), out, at + 16 * tt * lv, 0, 0);
+                for (int tt = 0; tt < 2; ++tt) mat[tt] = Pair<BF>{};
+            } else if constexpr (BF) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split_bf16(z[2 * i], z[2 * i + 1], zp.hi.p[i], zp.lo.p[i]);
+            }
+        }
+        if constexpr (MODE == kForward) {
+            mm2(y, zp, mat);
         } else {
             // ---- z or dw by columns: [V][32], the parts one after the other
             char *rows = A.rows + ((sq.first + c) * A.c.H + h) * (int64_t)V * (C * 4);
-            Pair<BF> zp;
-            set_pair(zp, z);
             if constexpr (BF) {
                 char *p = rows + (col + li) * (C * 2) + 16 * g;
                 *reinterpret_cast<u32x4 *>(p) = u32x4{zp.hi.p[0], zp.hi.p[1], zp.hi.p[2], zp.hi.p[3]};
@@ -454,22 +627,20 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
             }
         }
         // ---- the state's update
-        const float total = wt[kTotal * C];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
         if constexpr (!REV) {
-            float w[8];
-            weights(kLeaveBeta, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] *= z[i];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
             Frag8<BF> f[kParts<BF>];
             set_parts(f, w);
+            constexpr int KG = KT < 4 ? KT : 4;  // products of different tiles follow each other
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Frag8<BF> a = RK::tile_frag(sk, tile0, kt);
+            for (int k0 = 0; k0 < KT; k0 += KG)
 #pragma unroll
-                for (int p = 0; p < kParts<BF>; ++p) st[kt] = mma32(st[kt], a, f[p]);
-            }
+                for (int p = 0; p < kParts<BF>; ++p)
+#pragma unroll
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], f[p]);
         } else {
             float wq[8], wk[8], be[8];
             weights(kEnterScaled, wq);
@@ -481,30 +652,52 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
                 wq[i] *= vx[i];
                 wk[i] *= -z[i];
             }
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
             Frag8<BF> f[kParts<BF>], e[kParts<BF>];
             set_parts(f, wq);
             set_parts(e, wk);
+            constexpr int KG = KT < 4 ? KT : 4;
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Frag8<BF> a = RK::tile_frag(sq_, tile0, kt), a2 = RK::tile_frag(sk, tile0, kt);
+            for (int k0 = 0; k0 < KT; k0 += KG) {
+                Frag8<BF> a[KG];
 #pragma unroll
-                for (int p = 0; p < kParts<BF>; ++p) {
-                    st[kt] = mma32(st[kt], a, f[p]);
-                    st[kt] = mma32(st[kt], a2, e[p]);
-                }
+                for (int j = 0; j < KG; ++j) a[j] = RK::tile_frag(sq_, tile0, k0 + j);
+#pragma unroll
+                for (int p = 0; p < kParts<BF>; ++p)
+#pragma unroll
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], a[j], f[p]);
+#pragma unroll
+                for (int p = 0; p < kParts<BF>; ++p)
+#pragma unroll
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], e[p]);
             }
-            const int64_t t = sq.t0 + (int64_t)c * C;
-            const int m = (int)(sq.t1 - t < C ? sq.t1 - t : C);
-            const auto out = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<char *>(A.o) + (t * A.c.H + h) * V * EB, 0, (m - 1) * lv + V * EB, 0x00027000);
+            const auto out = __builtin_amdgcn_make_buffer_rsrc(po, 0, (tokens_of(c) - 1) * lv + V * EB, 0x00027000);
+            po += step_v;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t at = (uint32_t)slot_token<BF>(g, i) * lv + (uint32_t)(col + li) * EB;
+                const uint32_t at = (uint32_t)slot_token(g, i) * lv + (uint32_t)(col + li) * EB;
                 if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(z[i], 0.f), out, at, 0, 0);
                 else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, z[i]), out, at, 0, 0);
             }
         }
+        if constexpr (MODE == kForward) {
+            mfma_fence(y[0], y[1]);
+            // the hardware drops the stores behind the chunk's last row (past the buffer's end)
+            const auto out = __builtin_amdgcn_make_buffer_rsrc(po, 0, (tokens_of(c) - 1) * lv + V * EB, 0x00027000);
+            po += step_v;
+            const uint32_t at = li * lv + (uint32_t)(col + 4 * g) * EB;
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+                if constexpr (BF)
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(y[tt].x, y[tt].y), pack_bf16(y[tt].z, y[tt].w)},
+                                                          out, at + 16 * tt * lv, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[tt]), out, at + 16 * tt * lv, 0, 0);
+        }
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][KT]>(st));
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) sf[kc] = pair_of<BF>(st[2 * kc], st[2 * kc + 1]);
     }
     if (A.s_end) put_state(A.s_end + nh * sstate);
 }

@@ -16,11 +16,87 @@
 namespace kda {
 namespace gd {
 
+// A tile of V channels x 32 tokens in LDS, from rows of the states' passes: 16 bytes of a row are the tokens of a lane
+// group's slots. bf16: the two halves (tiles of 16 tokens) in planes of their own, rows of 32 bytes ordered so that the
+// eight rows of a transposing read, and the sixteen of a row read, fall on different banks.
+template <bool BF, int V> struct Tile;
+template <int V> struct Tile<true, V> {
+    static constexpr int PLANE = V * 32, PART = 2 * PLANE, PARTS = 2;
+    static __device__ __forceinline__ int at(int row, int g) {
+        const int line = (row & 3) | (row & 24) >> 1 | (row & 4) << 2 | (row & ~31);
+        return line * 32 + ((g ^ ((row >> 3) & 2)) << 3);
+    }
+    // channels 32 vc .. x tokens 16 tt + l % 16; rows of the state's tile vt x the chunk's tokens
+    static __device__ __forceinline__ int cols_at(int lane) { return at(8 * (lane >> 4) + ((lane >> 2) & 3), lane & 3); }
+    static __device__ __forceinline__ Frag8<true> cols(const char *t, int at, int vc, int tt) {
+        return Rw<true, 32>::tr_frag(t + at + 1024 * vc + PLANE * tt, 512);  // 16 lines on: the row 4 on
+    }
+    static __device__ __forceinline__ int rows_at(int lane) {
+        return at(8 * ((lane >> 2) & 3) + (lane & 3), lane >> 4);
+    }
+    static __device__ __forceinline__ Frag8<true> rows(const char *t, int at, int vt) {
+        const char *p = t + at + 1024 * (vt >> 1) + 512 * (vt & 1);
+        const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + PLANE);
+        return Frag8<true>{{a.x, a.y, b.x, b.y}};
+    }
+    static __device__ __forceinline__ Pair<true> cols_pair(const char *t, int at, int vc, int tt) {
+        return Pair<true>{cols(t, at, vc, tt), cols(t + PART, at, vc, tt)};
+    }
+    static __device__ __forceinline__ Pair<true> rows_pair(const char *t, int at, int vt) {
+        return Pair<true>{rows(t, at, vt), rows(t + PART, at, vt)};
+    }
+};
+template <int V> struct Tile<false, V> {
+    using R = Rw<false, 32>;
+    static constexpr int PART = R::bytes(V), PARTS = 1;
+    static __device__ __forceinline__ int cols_at(int lane) { return R::col_at(lane, 0); }
+    static __device__ __forceinline__ int rows_at(int lane) { return R::row_at(lane); }
+    static __device__ __forceinline__ Pair<false> cols_pair(const char *t, int at, int vc, int tt) {
+        return Pair<false>{R::col_frag(t + 32 * vc * R::RB + 64 * tt, at)};
+    }
+    static __device__ __forceinline__ Pair<false> rows_pair(const char *t, int at, int vt) {
+        return Pair<false>{R::row_frag(t + 16 * vt * R::RB, at, 0)};
+    }
+};
+// On its way there: V * 128 bytes (both parts), 16 a load.
+template <bool BF, int V, int NT>
+struct TileIn {
+    static constexpr int NL = V * 8 / NT > 0 ? V * 8 / NT : 1;
+    static_assert(V * 8 % NT == 0 || NT % (V * 8) == 0, "whole rounds");
+    u32x4 w[NL];
+    int to[NL];
+    uint32_t from[NL];
+    __device__ __forceinline__ void init(int tid) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int u = (i * NT + tid) % (V * 8);
+            from[i] = u * 16;
+            if constexpr (BF) to[i] = u / (V * 4) * Tile<true, V>::PART + Tile<true, V>::at(u / 4 % V, u & 3);
+            else to[i] = Rw<false, 32>::slot(u / 8, u & 7);
+        }
+    }
+    __device__ __forceinline__ void take(const char *p) {
+        const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, V * 128, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b128(b, from[i], 0, 0);
+    }
+    __device__ __forceinline__ void put(char *t) const {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if constexpr (BF) {
+                *reinterpret_cast<uint2 *>(t + to[i]) = make_uint2(w[i].x, w[i].y);
+                *reinterpret_cast<uint2 *>(t + to[i] + Tile<true, V>::PLANE) = make_uint2(w[i].z, w[i].w);
+            } else {
+                *reinterpret_cast<u32x4 *>(t + to[i]) = w[i];
+            }
+    }
+};
+
 template <bool BF, int K, int V>
 struct GradLds {
     static constexpr int C = kChunkTokens, NP = BF ? 2 : 1, NW = K / 16;
-    static constexpr int T_ = Rows<BF, C>::bytes(V), M_ = Rows<BF, C>::bytes(C);  // a part of a [V][32] tile, of a matrix
-    static constexpr int K_ = Rows<BF, K>::bytes(C), O_ = Rows<BF, V>::bytes(C);
+    static constexpr int T_ = Tile<BF, V>::PART, M_ = Rw<BF, C>::bytes(C);  // a part of a tile, of a matrix
+    static constexpr int K_ = Rw<BF, K>::bytes(C), O_ = Rw<BF, V>::bytes(C);
     static constexpr int dout = 0, z = dout + O_, dw = z + NP * T_, k = dw + NP * T_, q = k + K_, m1 = q + K_,
                          m2 = m1 + NP * M_, wt = m2 + NP * M_, u = wt + kWeights * C * 4,
                          db = u + NW * C * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
@@ -31,9 +107,10 @@ struct GradLds {
 template <bool BF, int K, int V, bool YF>
 __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A) {
     using L = GradLds<BF, K, V>;
-    using RK = Rows<BF, K>;
-    using RV = Rows<BF, V>;
-    using RC = Rows<BF, kChunkTokens>;
+    using RK = Rw<BF, K>;
+    using RV = Rw<BF, V>;
+    using RC = Rw<BF, kChunkTokens>;
+    using TV = Tile<BF, V>;
     constexpr int NW = K / 16, NT = NW * 64, VT = V / 16, VC = V / 32, C = kChunkTokens, NP = L::NP;
     constexpr int EB = BF ? 2 : 4;
     __shared__ __align__(16) char smem[L::bytes];
@@ -72,59 +149,40 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     const char *pq = reinterpret_cast<const char *>(A.q) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
     const char *pd = reinterpret_cast<const char *>(A.dout) + (sq.t0 * A.c.H + h) * (V * EB);
     const int64_t tile = (int64_t)V * (C * 4);
-    Stage<BF, K, C, NT> rk, rq;
-    Stage<BF, V, C, NT> rd;
-    Stage<BF, C, V, NT> rz[NP], rw[NP];
+    RowsIn<BF, K, C, NT> rk, rq;
+    RowsIn<BF, V, C, NT> rd;
+    TileIn<BF, V, NT> rz, rw;
+    rk.init(tid, lk);
+    rq.init(tid, lk);
+    rd.init(tid, lv);
+    rz.init(tid);
+    rw.init(tid);
     u32x4 rwt;
     auto take = [&](int c) __attribute__((always_inline)) {
         const int64_t t = (int64_t)c * C, at = (sq.first + c) * A.c.H + h;
         const int m = (int)(len - t < C ? len - t : C);
-        rk.take(tid, pk + t * lk, lk, m);
-        rq.take(tid, pq + t * lk, lk, m);
-        rd.take(tid, pd + t * lv, lv, m);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            rz[p].take(tid, A.z + at * tile + p * (V * C * EB), C * EB, V);
-            rw[p].take(tid, A.dw + at * tile + p * (V * C * EB), C * EB, V);
-        }
+        rk.take(pk + t * lk, m);
+        rq.take(pq + t * lk, m);
+        rd.take(pd + t * lv, m);
+        rz.take(A.z + at * tile);
+        rw.take(A.dw + at * tile);
         rwt = *reinterpret_cast<const u32x4 *>(A.c.rec + at * rec_bytes(true) + rec_weights(true) + (tid & 63) * 16);
     };
     auto put = [&]() __attribute__((always_inline)) {
-        rk.put(tid, s_k);
-        rq.put(tid, s_q);
-        rd.put(tid, s_do);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            rz[p].put(tid, s_z + p * L::T_);
-            rw[p].put(tid, s_dw + p * L::T_);
-        }
+        rk.put(s_k);
+        rq.put(s_q);
+        rd.put(s_do);
+        rz.put(s_z);
+        rw.put(s_dw);
         if (tid < 64) *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(s_wt) + tid * 16) = rwt;
     };
-    const int rowv0 = RV::row_at(lane), colc0 = RC::col_at(lane), rowc0 = RC::row_at(lane);
-    const int colk0 = BF ? RK::col_at(lane) ^ (wave << 5) : RK::col_at(lane) + 64 * wave, tilev0 = RV::tile_at(lane);
-    // V channels (32 vc ..) x tokens (16 tt + l % 16) of a [V][32] tile
+    const int rowv0 = RV::row_at(lane), rowc0 = RC::row_at(lane), colk0 = RK::col_at(lane, wave), tilev0 = RV::tile_at(lane);
+    const int tcols0 = TV::cols_at(lane), trows0 = TV::rows_at(lane);
     auto tile_cols = [&](const char *s, int vc, int tt) __attribute__((always_inline)) {
-        Pair<BF> p;
-        if constexpr (BF) {
-            p.hi = RC::col_frag(s + 32 * vc * RC::RB, colc0, tt);
-            p.lo = RC::col_frag(s + L::T_ + 32 * vc * RC::RB, colc0, tt);
-        } else {
-            p.f = RC::col_frag(s + 32 * vc * RC::RB, colc0, tt);
-        }
-        return p;
+        return TV::cols_pair(s, tcols0, vc, tt);
     };
-    // rows of the state's tile vt x the chunk's tokens
-    const int rows0 = tok_row_at<BF, C>(lane);
-    auto tile_rows = [&](const char *s, int vt) __attribute__((always_inline)) {
-        Pair<BF> p;
-        if constexpr (BF) {
-            p.hi = tok_row_frag<true, C>(s + 32 * (vt >> 1) * RC::RB, rows0, vt & 1, 0);
-            p.lo = tok_row_frag<true, C>(s + L::T_ + 32 * (vt >> 1) * RC::RB, rows0, vt & 1, 0);
-        } else {
-            p.f = RC::row_frag(s + 16 * vt * RC::RB, rowc0, 0);
-        }
-        return p;
-    };
+    auto tile_rows = [&](const char *s, int vt) __attribute__((always_inline)) { return TV::rows_pair(s, trows0, vt); };
+    // The matrices of the pairs' weights: sixteen bytes of a row are the tokens of a lane group's slots, as in a tile.
     auto mat_row = [&](const char *s, int tt) __attribute__((always_inline)) {
         Pair<BF> p;
         if constexpr (BF) {
@@ -135,24 +193,32 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         }
         return p;
     };
-    auto put_mat = [&](char *s, int row, int c, const f32x4 &w) __attribute__((always_inline)) {
-        const int at = RC::quad(row, c);
+    auto put_mat = [&](char *s, int row, int ts, const f32x4 &w) __attribute__((always_inline)) {  // sources 16 ts + 4g ..
         if constexpr (BF) {
+            const int at = RC::slot(row, g) + 8 * ts;
             uint2 hi, lo;
             split_bf16(w.x, w.y, hi.x, lo.x);
             split_bf16(w.z, w.w, hi.y, lo.y);
             *reinterpret_cast<uint2 *>(s + at) = hi;
             *reinterpret_cast<uint2 *>(s + L::M_ + at) = lo;
         } else {
-            *reinterpret_cast<f32x4 *>(s + at) = w;
+            *reinterpret_cast<f32x4 *>(s + RC::quad(row, 16 * ts + 4 * g)) = w;
+        }
+    };
+    auto mat_one = [&](const char *s, int row, int j) __attribute__((always_inline)) -> float {
+        if constexpr (BF) {
+            const char *p = s + RC::slot(row, (j >> 2) & 3) + 8 * (j >> 4) + 2 * (j & 3);
+            return bf2f(*reinterpret_cast<const uint16_t *>(p)) + bf2f(*reinterpret_cast<const uint16_t *>(p + L::M_));
+        } else {
+            return RC::load_one(s, row, j);
         }
     };
     auto clear_mats = [&]() __attribute__((always_inline)) {  // the tiles across the diagonal are read, never computed
         for (int i = tid; i < 2 * NP * L::M_ / 16; i += NT) reinterpret_cast<uint4 *>(s_m1)[i] = make_uint4(0, 0, 0, 0);
     };
     auto weights = [&](int which, float (&w)[8]) __attribute__((always_inline)) {
-        *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of<BF>(0, g));
-        *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of<BF>(1, g));
+        *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of(0, g));
+        *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of(1, g));
     };
     // e^{b_r - b_i} of a lane's four rows against one token
     auto decays = [&](int t, int s0, bool later, f32x4 &e) __attribute__((always_inline)) {
@@ -197,8 +263,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const int t = 16 * tt + li;
-                float w = RC::load_one(s_m1, t, j);
-                if constexpr (BF) w += RC::load_one(s_m1 + L::M_, t, j);
+                const float w = mat_one(s_m1, t, j);
                 if (later ? j >= t : j <= t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[tt][i] = fmaf(w, r[i], y[tt][i]);
@@ -244,7 +309,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 acc[i] = (which ? i0 + i < r : i0 + i <= r) && r < m ? f * acc[i] * e[i] * be[i] : 0.f;
-            put_mat(which ? s_m2 : s_m1, r, i0, acc);
+            put_mat(which ? s_m2 : s_m1, r, ts, acc);
         }
         // ---- what the state gives
         f32x4 y1[2] = {zero4(), zero4()}, y2[2] = {zero4(), zero4()};
@@ -265,7 +330,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             y2[tt] *= -s_wt[kEnter * C + t] * s_wt[kBeta * C + t];
         }
         __syncthreads();
-        const Frag8<BF> kf = RK::col_frag(s_k, colk0, 0);
+        const Frag8<BF> kf = RK::col_frag(s_k, colk0);
         float kx[8];
         widen(kf, kx);
         mix(y1, kf, kx, s_k, false, m);
@@ -347,7 +412,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 acc[i] = (which ? j0 + i > r : j0 + i >= r) && j0 + i < m ? f * acc[i] * e[i] * (which ? -be[i] : A.scale) : 0.f;
-            put_mat(which ? s_m2 : s_m1, r, j0, acc);
+            put_mat(which ? s_m2 : s_m1, r, ts, acc);
         }
         f32x4 y[2] = {zero4(), zero4()};
 #pragma unroll
@@ -360,7 +425,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) y[tt] *= s_wt[kLeaveBeta * C + 16 * tt + li];
         __syncthreads();
-        const Frag8<BF> kf = RK::col_frag(s_k, colk0, 0), qf = RK::col_frag(s_q, colk0, 0);
+        const Frag8<BF> kf = RK::col_frag(s_k, colk0), qf = RK::col_frag(s_q, colk0);
         float qx[8], kx[8];
         widen(qf, qx);
         widen(kf, kx);
