@@ -631,6 +631,18 @@ kda_status_t kda_rotary(const void *q, const void *k, const double *freqs, const
                         kda_dtype_t io, kda_rotary_layout_t layout, int32_t inverse, float scale, void *stream);
 
 /*
+ * The same with several axes (time, height, width of images and video): pair
+ * j turns by the position of axis axes[j].
+ *   axes       [R/2] int32, 0 .. num_axes - 1 (1..16 axes); any other value
+ *              makes its pair NaN
+ *   positions  [num_axes, tokens] int32 (any sign)
+ */
+kda_status_t kda_rotary_axes(const void *q, const void *k, const double *freqs, const int32_t *axes,
+                             const int32_t *positions, void *q_out, void *k_out, int64_t tokens, int32_t num_axes,
+                             int32_t Hq, int32_t Hk, int32_t D, int32_t R, kda_dtype_t io, kda_rotary_layout_t layout,
+                             int32_t inverse, float scale, void *stream);
+
+/*
  * Layer norm of rows of C channels (1..16384), and the output gate behind it:
  *   n = (x - mean) / sqrt(mean((x - mean)^2) + eps)   (center = 0: mean = 0)
  *   y = n * weight + bias,   with o_gate z:  y * sigmoid(z)
@@ -659,6 +671,33 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weig
                                 const void *o_gate, void *dx, float *dweight, float *dbias, void *d_o_gate,
                                 int64_t rows, int32_t groups, int32_t C, float eps, int32_t center, kda_dtype_t io,
                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activation checkpoints in 8 bits: a tensor [rows, C] in `io` as codes
+ * [rows, C] int8 and scales [rows, ceil(C / 128)] fp32, one for 128 adjacent
+ * channels (the last of a row may be fewer):
+ *   scale = max |x| / 127,   code = 127 x / max |x| to the nearest whole
+ *   number, ties to even,    value = code * scale, rounded to `io`
+ * A value is off by at most half a scale. Channels that are all zero have
+ * scale 0; a block that holds an infinity or a NaN has scale NaN and comes
+ * back as NaN; one whose largest value is below 2^-119 loses precision to the
+ * range of its scale.
+ */
+kda_status_t kda_checkpoint8_save(const void *x, int8_t *codes, float *scales, int64_t rows, int32_t C, kda_dtype_t io,
+                                  void *stream);
+kda_status_t kda_checkpoint8_restore(const int8_t *codes, const float *scales, void *x, int64_t rows, int32_t C,
+                                     kda_dtype_t io, void *stream);
+
+/*
+ * kda_layer_norm_bwd with x out of such a checkpoint: the gradients at the
+ * values that it stands for, x never written out. Its workspace is that of
+ * kda_layer_norm_bwd.
+ */
+kda_status_t kda_layer_norm_bwd_checkpoint8(const void *dy, const int8_t *codes, const float *scales,
+                                            const float *weight, const float *bias, const void *o_gate, void *dx,
+                                            float *dweight, float *dbias, void *d_o_gate, int64_t rows, int32_t groups,
+                                            int32_t C, float eps, int32_t center, kda_dtype_t io, void *workspace,
+                                            size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

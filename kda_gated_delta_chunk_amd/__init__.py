@@ -11,8 +11,8 @@ states [num_seqs, H, K, V] fp32. With cu_seqlens (int32 [num_seqs+1], on the
 device), B must be 1 and sequences are packed along T.
 
 The operators around it (linear attention with one decay per head, rotary
-positions, layer norm) are in layers.py, the gated delta rule with one decay
-per head in delta.py; all are exported here.
+positions, layer norm, activation checkpoints in 8 bits) are in layers.py, the
+gated delta rule with one decay per head in delta.py; all are exported here.
 """
 from __future__ import annotations
 
@@ -25,7 +25,8 @@ __all__ = ["chunk_fwd", "chunk_prep", "chunk_state", "chunk_bwd", "decode_step",
            "min_workspace_bytes", "prep_workspace_bytes", "workspace_status", "bwd_workspace_bytes", "KDAError",
            "abi_version", "hd_chunk_fwd", "hd_chunk_bwd", "hd_decode_step", "hd_workspace_bytes",
            "hd_bwd_workspace_bytes", "gd_chunk_fwd", "gd_chunk_bwd", "gd_decode_step", "gd_workspace_bytes",
-           "gd_bwd_workspace_bytes", "rotary", "rotary_freqs", "layer_norm_fwd", "layer_norm_bwd"]
+           "gd_bwd_workspace_bytes", "rotary", "rotary_freqs", "rotary_axes", "rotary_sections", "layer_norm_fwd",
+           "layer_norm_bwd", "Checkpoint8", "checkpoint8", "restore8"]
 
 _DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_FP32}
 _NAME = {"bf16": torch.bfloat16, "fp32": torch.float32}
@@ -384,7 +385,8 @@ def chunk_bwd(q, k, v, g, beta, do, S0=None, dS_final=None, cu_seqlens=None, wan
 
 
 # layers.py and delta.py use the argument helpers above
-from .layers import (hd_bwd_workspace_bytes, hd_chunk_bwd, hd_chunk_fwd, hd_decode_step,  # noqa: E402
-                     hd_workspace_bytes, layer_norm_bwd, layer_norm_fwd, rotary, rotary_freqs)
+from .layers import (Checkpoint8, checkpoint8, hd_bwd_workspace_bytes, hd_chunk_bwd, hd_chunk_fwd,  # noqa: E402
+                     hd_decode_step, hd_workspace_bytes, layer_norm_bwd, layer_norm_fwd, restore8, rotary, rotary_axes,
+                     rotary_freqs, rotary_sections)
 from .delta import (gd_bwd_workspace_bytes, gd_chunk_bwd, gd_chunk_fwd, gd_decode_step,  # noqa: E402
                     gd_workspace_bytes)

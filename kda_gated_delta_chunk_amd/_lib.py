@@ -37,7 +37,8 @@ EXPORTS = ("kda_abi_version", "kda_status_string", "kda_chunk_fwd_workspace_byte
            "kda_hd_chunk_bwd", "kda_hd_decode_step",
            "kda_gd_chunk_fwd_workspace_bytes", "kda_gd_chunk_bwd_workspace_bytes", "kda_gd_chunk_fwd",
            "kda_gd_chunk_bwd", "kda_gd_decode_step", "kda_rotary", "kda_layer_norm_fwd",
-           "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd")
+           "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd", "kda_rotary_axes", "kda_checkpoint8_save",
+           "kda_checkpoint8_restore", "kda_layer_norm_bwd_checkpoint8")
 
 NO_ALLOC_SCRATCH_BYTES = 16 * 1024 * 1024  # KDA_NO_ALLOC_SCRATCH_BYTES
 
@@ -131,6 +132,15 @@ def load() -> ctypes.CDLL:
     lib.kda_layer_norm_bwd_workspace_bytes.restype = sz
     lib.kda_layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, ci, vp, sz, vp]
     lib.kda_layer_norm_bwd.restype = ci
+    lib.kda_rotary_axes.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, ci, ci, i32, f32, vp]
+    lib.kda_rotary_axes.restype = ci
+    lib.kda_checkpoint8_save.argtypes = [vp, vp, vp, i64, i32, ci, vp]
+    lib.kda_checkpoint8_save.restype = ci
+    lib.kda_checkpoint8_restore.argtypes = [vp, vp, vp, i64, i32, ci, vp]
+    lib.kda_checkpoint8_restore.restype = ci
+    lib.kda_layer_norm_bwd_checkpoint8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, ci,
+                                                   vp, sz, vp]
+    lib.kda_layer_norm_bwd_checkpoint8.restype = ci
     _lib = lib
     return lib
 

@@ -49,7 +49,9 @@ struct RotaryArgs {
     const void *q, *k;         // [tokens, Hq, D], [tokens, Hk, D] (k or null with Hk = 0)
     void *q_out, *k_out;
     const double *freqs;       // [R / 2] radians per position
-    const int32_t *positions;  // [tokens], or null: token index modulo T
+    const int32_t *positions;  // [tokens], or null: token index modulo T; with axes [naxes, tokens]
+    const int32_t *axes;       // [R / 2] the axis whose position turns a pair, or null: one axis
+    int32_t naxes;
     int64_t tokens, T;         // 1 <= T <= tokens
     int32_t Hq, Hk, D, R;
     bool io_bf16, interleaved, inverse;
@@ -60,6 +62,8 @@ hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st);
 // ------------------------------------------------------- layer norm
 struct NormArgs {
     const void *x, *gate;      // [rows, C]; gate pre-activation [rows, C] or null
+    const int8_t *codes;       // backward: x out of a checkpoint (x null), [rows, C] and [rows, ceil(C / 128)]
+    const float *scales;
     const float *weight, *bias;  // [G, C] or null
     void *y;
     int64_t rows;
@@ -76,5 +80,18 @@ bool norm_grid_fits(int64_t rows, int32_t G, int32_t C);  // a grid's threads ar
 size_t norm_bwd_workspace_bytes(int64_t rows, int32_t G, int32_t C);
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st);
+
+// ------------------------------------------------------- activation checkpoints in 8 bits
+constexpr int32_t kCkptBlock = 128;  // values along a row that share a step
+struct CkptArgs {
+    void *x;                   // [rows, C]
+    int8_t *codes;             // [rows, C]
+    float *scales;              // [rows, ceil(C / 128)]
+    int64_t rows;
+    int32_t C;
+    bool io_bf16;
+};
+hipError_t launch_ckpt_save(const CkptArgs &a, hipStream_t st);
+hipError_t launch_ckpt_restore(const CkptArgs &a, hipStream_t st);
 
 }  // namespace kda

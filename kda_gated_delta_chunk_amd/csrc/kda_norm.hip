@@ -16,6 +16,8 @@
 // apart, so its parameters, and its sums for their gradients, stay in registers over all of its rows. At the end a
 // workgroup adds up its row slots of one group where G divides their number, the sums leave as partial rows, and a
 // second kernel adds those in a fixed order (no atomics: the same inputs give the same bits).
+#include <type_traits>
+
 #include "kda_common.hpp"
 #include "kda_layer.hpp"
 
@@ -142,6 +144,50 @@ struct Slice {
     }
 };
 
+// The same elements out of a checkpoint in 8 bits: a code's step is that of its 128 channels, and the value it stands
+// for is of the I/O type.
+template <bool BF, bool VEC, int TPR, int EPT>
+struct Codes {
+    static constexpr int EL = BF ? 8 : 4, NR = VEC ? EPT / EL : EPT;
+    struct Raw {
+        int8_t e[NR][VEC ? EL : 1];
+        float step[NR];
+    };
+    static __device__ __forceinline__ int at(int i, int t) { return Slice<BF, VEC, TPR, EPT>::at(i, t); }
+    static __device__ __forceinline__ void load(const int8_t *codes, const float *scales, int64_t row, int C, int t, Raw &x) {
+        const int8_t *r = codes + row * C;
+        const float *s = scales + row * ((C + kCkptBlock - 1) / kCkptBlock);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int c = at(VEC ? i * EL : i, t);
+            const bool in = c < C;
+            if constexpr (VEC) {
+                using W = typename std::conditional<BF, uint2, uint32_t>::type;
+                W w{};
+                if (in) w = *reinterpret_cast<const W *>(r + c);
+                __builtin_memcpy(x.e[i], &w, EL);
+            } else {
+                x.e[i][0] = in ? r[c] : int8_t(0);
+            }
+            x.step[i] = in ? s[c / kCkptBlock] : 0.f;
+        }
+    }
+    static __device__ __forceinline__ void widen(const Raw &w, float (&x)[EPT]) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int r = VEC ? i / EL : i;
+            x[i] = (float)w.e[r][VEC ? i % EL : 0] * w.step[r];
+        }
+        if constexpr (BF)
+#pragma unroll
+            for (int i = 0; i < EPT; i += 2) {
+                const uint32_t p = pack_bf16(x[i], x[i + 1]);
+                x[i] = bf_lo(p);
+                x[i + 1] = bf_hi(p);
+            }
+    }
+};
+
 // A workgroup of 1024 threads with 16 elements each has no registers for a second row: no row in flight, one more round.
 template <int NT, int EPT>
 constexpr bool piped = NT * EPT < 1024 * 16;
@@ -223,14 +269,16 @@ __global__ __launch_bounds__(NT) void kda_norm_fwd_kernel(const void *__restrict
 __host__ __device__ constexpr int parts_of(int rpw, int G) { return rpw % G == 0 ? G : rpw; }
 
 // part: [2][partial rows][C] fp32, the sums of e n and of e over the rows of each
-template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE>
+template <bool BF, bool VEC, int TPR, int NT, int EPT, bool GATE, bool Q8>
 __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void kda_norm_bwd_kernel(const void *__restrict__ dyp, const void *__restrict__ xp,
+                                                          const float *__restrict__ scales,
                                                           const void *__restrict__ zp, const float *__restrict__ wp,
                                                           const float *__restrict__ bp, void *__restrict__ dxp,
                                                           void *__restrict__ dzp, float *__restrict__ part,
                                                           int want_dw, int want_db, int64_t rows, int G, int C,
                                                           float eps, int center) {
     using SL = Slice<BF, VEC, TPR, EPT>;
+    using SX = typename std::conditional<Q8, Codes<BF, VEC, TPR, EPT>, SL>::type;
     constexpr int RPW = NT / TPR;
     __shared__ float lds[2][4 * (NT / 64)];
     int turn = 0;
@@ -250,13 +298,18 @@ __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void 
     const int64_t turns = (rows + slots - 1) / slots;
     auto row_of = [&](int64_t i) { const int64_t r = i * slots + slot; return r < rows ? r : rows - 1; };
     constexpr bool PIPE = piped<NT, EPT>;
-    typename SL::Raw rx, rd, rz;
+    typename SX::Raw rx;
+    typename SL::Raw rd, rz;
     float x[EPT], mean[1];
+    auto load_x = [&](int64_t row) __attribute__((always_inline)) {
+        if constexpr (Q8) SX::load(reinterpret_cast<const int8_t *>(xp), scales, row, C, t, rx);
+        else SL::load(xp, row, C, t, rx);
+    };
     auto first_round = [&](int64_t i) __attribute__((always_inline)) {
-        SL::load(xp, row_of(i), C, t, rx);
+        load_x(row_of(i));
         SL::load(dyp, row_of(i), C, t, rd);
         if (GATE) SL::load(zp, row_of(i), C, t, rz);
-        SL::widen(rx, x);
+        SX::widen(rx, x);
         mean[0] = 0.f;
         if (!center) return;
 #pragma unroll
@@ -274,7 +327,7 @@ __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void 
         SL::widen(rd, d);
         if (GATE) SL::widen(rz, a);
         if (next) {
-            SL::load(xp, row_of(i + 1), C, t, rx);
+            load_x(row_of(i + 1));
             SL::load(dyp, row_of(i + 1), C, t, rd);
             if (GATE) SL::load(zp, row_of(i + 1), C, t, rz);
         }
@@ -294,7 +347,7 @@ __global__ __launch_bounds__(NT, NT == 256 || (NT == 512 && GATE) ? 1 : 4) void 
         }
         float nx[EPT];
         if (next) {
-            SL::widen(rx, nx);
+            SX::widen(rx, nx);
             if (center)
 #pragma unroll
                 for (int e = 0; e < EPT; ++e) s[3] += nx[e];
@@ -410,9 +463,11 @@ hipError_t run_gate(const NormArgs &a, bool bwd, hipStream_t st) {
     }
     const int64_t wgs = grid_for(a.rows, a.G, RPW, kMaxWG);
     float *part = reinterpret_cast<float *>(a.workspace);
-    hipLaunchKernelGGL((kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT, GATE>), dim3((uint32_t)wgs), dim3(NT), 0, st, a.dy,
-                       a.x, a.gate, a.weight, a.bias, a.dx, a.dgate, part, (int)(a.dweight != nullptr),
-                       (int)(a.dbias != nullptr), a.rows, a.G, a.C, a.eps, (int)a.center);
+    auto bwd_kernel = a.codes ? kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT, GATE, true>
+                              : kda_norm_bwd_kernel<BF, VEC, TPR, NT, EPT, GATE, false>;
+    hipLaunchKernelGGL(bwd_kernel, dim3((uint32_t)wgs), dim3(NT), 0, st, a.dy, a.codes ? a.codes : a.x, a.scales, a.gate,
+                       a.weight, a.bias, a.dx, a.dgate, part, (int)(a.dweight != nullptr), (int)(a.dbias != nullptr),
+                       a.rows, a.G, a.C, a.eps, (int)a.center);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
     const int64_t cols = (int64_t)a.G * a.C;

@@ -100,10 +100,12 @@ __device__ __forceinline__ void turn_run(float (&x)[E], float (&y)[E], const flo
 // A unit is a run of E pairs or, behind them, a run of 2E copied channels; an interleaved unit that straddles R copies
 // its pairs from R on. Threads of a workgroup: `units` consecutive ones per head, heads_par heads at a
 // time, tok_par tokens at a time. q_out and k_out may be q and k: a thread reads its channels before it writes them.
-template <bool BF, int E, bool INTER>
+// AXES: pair j turns by the position of axis axes[j], positions are [naxes, tokens].
+template <bool BF, int E, bool INTER, bool AXES>
 __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const void *kp, void *qo, void *ko,
                                                          const double *__restrict__ freqs,
-                                                         const int32_t *__restrict__ positions, int64_t tokens,
+                                                         const int32_t *__restrict__ positions,
+                                                         const int32_t *__restrict__ axes, int naxes, int64_t tokens,
                                                          int64_t T, int Hq, int Hk, int D, int R, int units,
                                                          int heads_par, int tok_par, float sgn, float scale) {
     constexpr int ES = BF ? 2 : 4;
@@ -121,6 +123,16 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
         const double f = pairs && u * E + i < R / 2 ? freqs[u * E + i] : 0.0;
         fr[i] = turn_fraction(f);
         undefined |= (uint32_t)!(fabs(f) < HUGE_VAL) << i;
+    }
+    int64_t line[AXES ? E : 1];  // where the positions of a pair's axis begin
+    if constexpr (AXES) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int a = pairs && u * E + i < R / 2 ? axes[u * E + i] : 0;
+            const bool known = a >= 0 && a < naxes;
+            undefined |= (uint32_t)!known << i;
+            line[i] = known ? a * tokens : 0;
+        }
     }
     // the two runs of a unit: (x1 run, x2 run) of "half", 2E adjacent channels otherwise
     const int c0 = INTER ? 2 * E * u : pairs ? E * u : R + 2 * E * (u - np);
@@ -150,10 +162,18 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     for (; t < tokens; t += step) {
         float cs[E], sn[E];
         if (pairs) {
-            const int64_t pos = positions ? (int64_t)positions[t]
-                              : tokens <= 0xffffffffll ? (int64_t)((uint32_t)t % (uint32_t)T) : t % T;
+            int64_t pos = 0;
+            int32_t at[AXES ? E : 1];
+            if constexpr (AXES) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) at[i] = positions[line[i] + t];
+            } else {
+                pos = positions ? (int64_t)positions[t]
+                    : tokens <= 0xffffffffll ? (int64_t)((uint32_t)t % (uint32_t)T) : t % T;
+            }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
+                if constexpr (AXES) pos = at[i];
                 sincos_turn(fr[i] * (uint64_t)pos, sn[i], cs[i]);
                 sn[i] *= sgn * scale;
                 cs[i] *= scale;
@@ -174,10 +194,9 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     }
 }
 
-template <bool BF, int E>
-hipError_t launch_e(const RotaryArgs &a, hipStream_t st) {
-    const int units = a.interleaved ? (a.D + 2 * E - 1) / (2 * E)
-                                    : a.R / (2 * E) + (a.D - a.R + 2 * E - 1) / (2 * E);
+template <bool BF, int E, bool INTER, bool AXES>
+hipError_t launch_i(const RotaryArgs &a, hipStream_t st) {
+    const int units = INTER ? (a.D + 2 * E - 1) / (2 * E) : a.R / (2 * E) + (a.D - a.R + 2 * E - 1) / (2 * E);
     const int H = a.Hq + a.Hk;
     int heads_par = 256 / units;  // D <= 512: at most 256 units
     if (heads_par > H) heads_par = H;
@@ -187,15 +206,15 @@ hipError_t launch_e(const RotaryArgs &a, hipStream_t st) {
     int64_t wgs = (a.tokens + tok_par - 1) / tok_par;
     if (wgs > 4096) wgs = 4096;  // a thread's frequencies serve several tokens
     const float sgn = a.inverse ? -1.f : 1.f;
-    if (a.interleaved)
-        hipLaunchKernelGGL((kda_rotary_kernel<BF, E, true>), dim3((uint32_t)wgs), dim3(256), 0, st, a.q, a.k, a.q_out,
-                           a.k_out, a.freqs, a.positions, a.tokens, a.T, a.Hq, a.Hk, a.D, a.R, units, heads_par,
-                           tok_par, sgn, a.scale);
-    else
-        hipLaunchKernelGGL((kda_rotary_kernel<BF, E, false>), dim3((uint32_t)wgs), dim3(256), 0, st, a.q, a.k, a.q_out,
-                           a.k_out, a.freqs, a.positions, a.tokens, a.T, a.Hq, a.Hk, a.D, a.R, units, heads_par,
-                           tok_par, sgn, a.scale);
+    hipLaunchKernelGGL((kda_rotary_kernel<BF, E, INTER, AXES>), dim3((uint32_t)wgs), dim3(256), 0, st, a.q, a.k, a.q_out,
+                       a.k_out, a.freqs, a.positions, a.axes, a.naxes, a.tokens, a.T, a.Hq, a.Hk, a.D, a.R, units,
+                       heads_par, tok_par, sgn, a.scale);
     return hipGetLastError();
+}
+template <bool BF, int E>
+hipError_t launch_e(const RotaryArgs &a, hipStream_t st) {
+    if (a.axes) return a.interleaved ? launch_i<BF, E, true, true>(a, st) : launch_i<BF, E, false, true>(a, st);
+    return a.interleaved ? launch_i<BF, E, true, false>(a, st) : launch_i<BF, E, false, false>(a, st);
 }
 
 }  // namespace

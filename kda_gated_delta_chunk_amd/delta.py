@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import _io_code, _lib, _ptr
-from .layers import _call, _cuda, _hd_seqs, _need, _result, _states, _workspace
+from .layers import _call, _cuda, _hd_seqs, _need, _restored, _result, _states, _workspace
 
 __all__ = ["gd_chunk_fwd", "gd_chunk_bwd", "gd_decode_step", "gd_workspace_bytes", "gd_bwd_workspace_bytes"]
 
@@ -84,9 +84,11 @@ def gd_chunk_bwd(q, k, v, g, beta, do, S0=None, dS_final=None, cu_seqlens=None, 
     """Gradients of gd_chunk_fwd's (o, S_final) given ``do`` = dL/do (o's shape, input dtype) and ``dS_final`` (fp32
     [num_seqs, H, K, V], or None: zero). Returns a dict: dq, dk, dv in the inputs' shapes and dtype (dq and dk summed
     over the heads that share them); dg and dbeta like g and beta; dS0 fp32 when ``want_dS0``. ``out`` may hold
-    preallocated results by these names. Nothing of a forward call is needed; deterministic.
+    preallocated results by these names. Nothing of a forward call is needed; deterministic. q, k and v may each be a
+    Checkpoint8.
     """
     lib = _lib.load()
+    q, k, v = _restored(q, k, v)
     dev = _cuda(q)
     N = _hd_seqs(q, cu_seqlens)
     B, T = q.shape[:2]

@@ -1,5 +1,5 @@
 """The operators around the recurrence: linear attention with one decay per head (chunked forward, backward, single
-token), rotary positions, layer norm and its gradient.
+token), rotary positions with one or several axes, layer norm and its gradient, activation checkpoints in 8 bits.
 
 Like the rest of the package this only marshals tensors into libkda.so: it checks shapes, dtypes and devices,
 allocates outputs and workspaces with torch, and passes pointers and torch's current stream of the tensors' device.
@@ -7,6 +7,7 @@ allocates outputs and workspaces with torch, and passes pointers and torch's cur
 from __future__ import annotations
 
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -14,7 +15,8 @@ from . import KDAError, _io_code, _lib, _ptr
 from . import _need as _explain
 
 __all__ = ["hd_chunk_fwd", "hd_chunk_bwd", "hd_decode_step", "hd_workspace_bytes", "hd_bwd_workspace_bytes", "rotary",
-           "rotary_freqs", "layer_norm_fwd", "layer_norm_bwd"]
+           "rotary_freqs", "rotary_axes", "rotary_sections", "layer_norm_fwd", "layer_norm_bwd", "Checkpoint8",
+           "checkpoint8", "restore8"]
 
 
 # the current stream's handle by device index, without making a Stream object of it
@@ -78,6 +80,67 @@ def _states(out, name, S, shape, dev):
         return torch.empty(shape, dtype=torch.float32, device=dev) if S is None else torch.empty_like(S)
     _need(out, name, shape, torch.float32, dev)
     return out
+
+
+# ---------------------------------------------------------------- activation checkpoints in 8 bits
+class Checkpoint8(NamedTuple):
+    """A tensor of ``dtype`` in 8 bits: int8 ``codes`` of its shape, and an fp32 scale for 128 adjacent values of its
+    last axis, [..., ceil(C / 128)]. It stands for codes * scales, rounded to ``dtype``. The backward passes that say so
+    take it in place of the tensor."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: torch.dtype
+
+
+def _blocks8(shape):
+    return (*shape[:-1], (shape[-1] + 127) // 128)
+
+
+def _need8(c, name, shape, dev):
+    _need(c.codes, name + ".codes", shape, torch.int8, dev)
+    _need(c.scales, name + ".scales", _blocks8(shape), torch.float32, dev)
+
+
+def checkpoint8(x, out=None):
+    """x [..., C] (bf16 or fp32) as a Checkpoint8: codes = 127 x / max |x| to the nearest whole number (ties to even),
+    scales = max |x| / 127, the maximum over 128 adjacent values of the last axis. A value is off by at most half a
+    scale; a block with an infinity or a NaN comes back as NaN. ``out`` may hold a Checkpoint8 to write into."""
+    lib = _lib.load()
+    dev, io = _cuda(x), _io_code(x.dtype)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x has shape %s, expected at least one value in a row" % (tuple(x.shape),))
+    _need(x, "x", x.shape, x.dtype, dev)
+    if out is None:
+        out = Checkpoint8(torch.empty(x.shape, dtype=torch.int8, device=dev),
+                          torch.empty(_blocks8(x.shape), dtype=torch.float32, device=dev), x.dtype)
+    else:
+        _need8(out, "out", x.shape, dev)
+        if out.dtype is not x.dtype:
+            raise TypeError("out.dtype is %s, expected %s" % (out.dtype, x.dtype))
+    _call(dev, lib.kda_checkpoint8_save, _ptr(x), _ptr(out.codes), _ptr(out.scales), math.prod(x.shape[:-1]),
+          x.shape[-1], io)
+    return out
+
+
+def restore8(c, out=None):
+    """The tensor that the Checkpoint8 ``c`` stands for."""
+    lib = _lib.load()
+    dev, io, shape = _cuda(c.codes), _io_code(c.dtype), c.codes.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("codes has shape %s, expected at least one value in a row" % (tuple(shape),))
+    _need8(c, "c", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=c.dtype, device=dev)
+    else:
+        _need(out, "out", shape, c.dtype, dev)
+    _call(dev, lib.kda_checkpoint8_restore, _ptr(c.codes), _ptr(c.scales), _ptr(out), math.prod(shape[:-1]), shape[-1],
+          io)
+    return out
+
+
+def _restored(*tensors):
+    """The tensors as they are, checkpoints restored."""
+    return tuple(restore8(t) if isinstance(t, Checkpoint8) else t for t in tensors)
 
 
 # ---------------------------------------------------------------- linear attention with one decay per head
@@ -163,9 +226,11 @@ def hd_chunk_bwd(q, k, v, g, do, S0=None, dS_final=None, cu_seqlens=None, scale:
     [num_seqs, H, K, V], or None: zero). Returns a dict: dq, dk, dv in the inputs' shapes and dtype (dq and dk summed
     over the heads that share them); dg [B, T, H] when g is per token and ``want_dg`` (a constant per head has no
     gradient here: give it per token and sum); dS0 fp32 when ``want_dS0``. ``out`` may hold preallocated results by
-    these names. Nothing of a forward call is needed; deterministic.
+    these names. Nothing of a forward call is needed; deterministic. q, k and v may each
+    be a Checkpoint8.
     """
     lib = _lib.load()
+    q, k, v = _restored(q, k, v)
     dev = _cuda(q)
     N = _hd_seqs(q, cu_seqlens)
     B, T = q.shape[:2]
@@ -277,6 +342,60 @@ def rotary(q, freqs, k=None, positions=None, layout: str = "half", inverse: bool
     return out if k is None else (out, k_out)
 
 
+def rotary_sections(sections, order: str = "runs", device="cuda"):
+    """The axis of every channel pair, int32 on ``device``, for rotary_axes: sections[a] pairs turn by axis a, in ``order``
+    "runs" (axis 0's pairs first, then axis 1's, ...) or "turns" (a pair of each axis in turn while it has any left)."""
+    left = [int(n) for n in sections]
+    if order not in ("runs", "turns"):
+        raise ValueError("order must be one of ['runs', 'turns']")
+    if not left or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections must be counts of pairs, one at least")
+    axes = []
+    if order == "runs":
+        axes = [a for a, n in enumerate(left) for _ in range(n)]
+    else:
+        while any(left):
+            for a, n in enumerate(left):
+                if n:
+                    axes.append(a)
+                    left[a] -= 1
+    return torch.tensor(axes, dtype=torch.int32).to(device)
+
+
+def rotary_axes(q, freqs, axes, positions, k=None, layout: str = "half", inverse: bool = False, scale: float = 1.0,
+                out=None, k_out=None):
+    """Rotary positions with several axes (time, height and width of images and video): as rotary(), but pair j turns by
+    the position of axis ``axes[j]``. Returns the turned q, or (q, k).
+
+    ``axes``: int32 of freqs' length (rotary_sections()); a pair whose axis is not one of positions' becomes NaN.
+    ``positions``: int32 [axes, *q's leading shape], up to 16 axes. The others as in rotary().
+    """
+    lib = _lib.load()
+    dev = _cuda(q)
+    if layout not in _lib.ROTARY_LAYOUTS:
+        raise ValueError("layout must be one of %s" % sorted(_lib.ROTARY_LAYOUTS))
+    if q.dim() < 3:
+        raise ValueError("q has shape %s, expected [..., heads, channels]" % (tuple(q.shape),))
+    lead, (Hq, D), dt = q.shape[:-2], q.shape[-2:], q.dtype
+    io = _io_code(dt)
+    _need(q, "q", q.shape, dt, dev)
+    _need(freqs, "freqs", (freqs.numel(),), torch.float64, dev)
+    _need(axes, "axes", freqs.shape, torch.int32, dev)
+    A = positions.shape[0] if positions.dim() else 0
+    _need(positions, "positions", (A,) + lead, torch.int32, dev)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[-2] if k.dim() == q.dim() else -1
+        _need(k, "k", lead + (Hk, D), dt, dev)
+        k_out = _result(k_out, "k_out", k)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    out = _result(out, "out", q)
+    _call(dev, lib.kda_rotary_axes, _ptr(q), _ptr(k), _ptr(freqs), _ptr(axes), _ptr(positions), _ptr(out), _ptr(k_out),
+          math.prod(lead), A, Hq, Hk, D, 2 * freqs.numel(), io, _lib.ROTARY_LAYOUTS[layout], int(bool(inverse)), scale)
+    return out if k is None else (out, k_out)
+
+
 # ---------------------------------------------------------------- layer norm
 def _norm_args(x, weight, bias, o_gate):
     """(rows, groups, C) of x, with its parameters checked: weight and bias are [C], or [H, C] for x [..., H, C]."""
@@ -319,8 +438,15 @@ def layer_norm_bwd(dy, x, weight=None, bias=None, o_gate=None, eps: float = 1e-5
                    out=None):
     """Gradients of layer_norm_fwd given ``dy`` (x's shape and dtype) and its arguments. Returns a dict: dx;
     dweight and dbias (fp32) for the parameters given; do_gate with ``o_gate``. ``out`` may hold preallocated results
-    by these names. Deterministic."""
+    by these names. Deterministic. ``x`` may be a Checkpoint8: the gradients are those at the values it stands for, and
+    the kernel reads its codes."""
     lib = _lib.load()
+    saved = x if isinstance(x, Checkpoint8) else None
+    if saved is not None:
+        x = dy  # of the shape and dtype that the checkpoint has to have
+        if saved.dtype is not dy.dtype:
+            raise TypeError("x stands for %s, dy has dtype %s" % (saved.dtype, dy.dtype))
+        _need8(saved, "x", dy.shape, _cuda(dy))
     io = _io_code(x.dtype)
     rows, groups, C = _norm_args(x, weight, bias, o_gate)
     dev, dt = x.device, x.dtype
@@ -339,7 +465,11 @@ def layer_norm_bwd(dy, x, weight=None, bias=None, o_gate=None, eps: float = 1e-5
     workspace = _workspace(workspace, lib.kda_layer_norm_bwd_workspace_bytes(rows, groups, C), dev,
                            "layer_norm_bwd(rows=%d, groups=%d, C=%d)", rows, groups, C)
     res = {n: _result(given.get(n), n, t) for n, t in like.items()}
-    _call(dev, lib.kda_layer_norm_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(o_gate), _ptr(res["dx"]),
+    if saved is None:
+        fn, inputs = lib.kda_layer_norm_bwd, (_ptr(x),)
+    else:
+        fn, inputs = lib.kda_layer_norm_bwd_checkpoint8, (_ptr(saved.codes), _ptr(saved.scales))
+    _call(dev, fn, _ptr(dy), *inputs, _ptr(weight), _ptr(bias), _ptr(o_gate), _ptr(res["dx"]),
           _ptr(res.get("dweight")), _ptr(res.get("dbias")), _ptr(res.get("do_gate")), rows, groups, C, eps,
           int(bool(center)), io, _ptr(workspace), workspace.numel())
     return res
