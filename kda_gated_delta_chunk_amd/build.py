@@ -17,7 +17,8 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libkda.so"
 SOURCES = ["kda_prefill.hip", "kda_decode.hip", "kda_backward.hip", "kda_api.hip", "kda_hd_fwd.hip",
            "kda_hd_grad_bf16.hip", "kda_hd_grad_fp32.hip", "kda_hd.hip", "kda_hd_decode.hip", "kda_rotary.hip", "kda_norm.hip",
-           "kda_layer_api.hip", "kda_gd.hip", "kda_gd_state.hip", "kda_gd_grad_bf16.hip", "kda_gd_grad_fp32.hip",
+           "kda_layer_api.hip", "kda_gd.hip", "kda_gd_state.hip", "kda_gd_grad_bf16.hip", "kda_gd_grad_gates.hip",
+           "kda_gd_grad_fp32.hip",
            "kda_gd_decode.hip", "kda_gd_api.hip", "kda_ckpt.hip", "kda_ckpt_api.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

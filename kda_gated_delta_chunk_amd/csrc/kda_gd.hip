@@ -257,18 +257,18 @@ __global__ __launch_bounds__(64) void kda_gd_prep_kernel(const Common cm, const 
             float x[8];
             Pair<BF> f;
             rows(s_a[0], 16 * tt + li, x);
-            set_pair(f, x);
+            set_multi(f, x);
             store_mat(rec + kMatN * kMatBytes, tt, lane, f);
             if constexpr (!BWD) {
                 rows(s_p, 16 * tt + li, x);
-                set_pair(f, x);
+                set_multi(f, x);
                 store_mat(rec + kMatP * kMatBytes, tt, lane, f);
             } else {
                 cols(s_a[BWD], 16 * tt + li, x);
-                set_pair(f, x);
+                set_multi(f, x);
                 store_mat(rec + kMatNT * kMatBytes, tt, lane, f);
                 cols(s_p, 16 * tt + li, x);
-                set_pair(f, x);
+                set_multi(f, x);
                 store_mat(rec + kMatPT * kMatBytes, tt, lane, f);
             }
         }
@@ -314,7 +314,8 @@ Sizes sizes(int64_t B, int64_t T, int32_t N, bool packed) {
     s.segs = packed ? T / (kChunkTokens * kSegmentChunks) + N : B * nseg;
     return s;
 }
-Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t N, bool packed, bool bwd) {
+Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t N, bool packed, bool bwd,
+              int tile_bytes) {
     Layout l{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -326,8 +327,8 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
     if (packed) l.seqs = take((size_t)N * sizeof(Seq));
     l.rec = take(ch * rec_bytes(bwd));
     if (bwd) {
-        l.z = take(ch * V * kChunkTokens * 4);
-        l.dw = take(ch * V * kChunkTokens * 4);
+        l.z = take(ch * V * kChunkTokens * tile_bytes);
+        l.dw = take(ch * V * kChunkTokens * tile_bytes);
         l.seed_s = take((size_t)s.segs * H * K * V * 4);
         l.seed_g = take((size_t)s.segs * H * K * V * 4);
         l.dk_part = take((size_t)ntok * H * K * 4);
@@ -346,6 +347,11 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
         if (e_ != hipSuccess) return e_;      \
     } while (0)
 
+// Of a value of the tiles between the backward call's passes: two bf16 parts where all that is summed from them leaves in
+// bf16, three beside fp32 gates (whose gradients are sums with cancellation: 1.4e-5 off from two parts).
+int tile_parts(bool io_bf16, bool gates_fp32) { return io_bf16 && gates_fp32 ? 3 : 2; }
+int tile_bytes(bool io_bf16, bool gates_fp32) { return 2 * tile_parts(io_bf16, gates_fp32); }
+
 struct Call {
     Layout l;
     char *ws;
@@ -355,7 +361,7 @@ Call prepare(const GdArgs &a, bool bwd) {
     Call x{};
     const bool packed = a.cu_seqlens != nullptr;
     const Sizes s = sizes(a.B, a.T, a.num_seqs, packed);
-    x.l = layout(s, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd);
+    x.l = layout(s, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd, tile_bytes(a.io_bf16, a.gates_fp32));
     x.ws = reinterpret_cast<char *>(a.workspace);
     x.c.seqs = packed ? reinterpret_cast<const Seq *>(x.ws + x.l.seqs) : nullptr;
     x.c.T = a.T;
@@ -403,11 +409,12 @@ hipError_t make_records(const GdArgs &a, const Call &x, bool bwd, hipStream_t st
 
 size_t gd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool) {
-    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, false).total;
+    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, false, 0).total;
 }
 size_t gd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
-                              bool packed, bool) {
-    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, true).total;
+                              bool packed, bool io_bf16) {
+    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, true,
+                      gd::tile_bytes(io_bf16, true)).total;
 }
 
 hipError_t launch_gd_fwd(const GdArgs &a, hipStream_t st) {
@@ -436,6 +443,7 @@ hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
     s.q = a.q;
     s.k = a.k;
     s.tiles = a.V / state_tile(a.V);
+    s.parts = tile_parts(a.io_bf16, a.gates_fp32);
     if (a.T > 0) {  // forward in time: the errors z, and the states at the segments' starts
         s.v = a.v;
         s.s_init = a.S0;
@@ -470,8 +478,9 @@ hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
     g.dg = a.dg;
     g.dbeta = a.dbeta;
     g.scale = a.scale;
-    g.gates_fp32 = a.gates_fp32 || !a.io_bf16;
-    KDA_TRY(a.io_bf16 ? grad_pass_bf16(g, a.K, a.V, grouped, st) : grad_pass_fp32(g, a.K, a.V, st));
+    KDA_TRY(!a.io_bf16     ? grad_pass_fp32(g, a.K, a.V, st)
+            : a.gates_fp32 ? grad_pass_bf16_gates_fp32(g, a.K, a.V, grouped, st)
+                           : grad_pass_bf16(g, a.K, a.V, grouped, st));
     if (!grouped) return hipSuccess;
     const int64_t per = (int64_t)a.Hk * a.K / 4, n = a.B * a.T * per;
     const dim3 grid((uint32_t)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192), 2);

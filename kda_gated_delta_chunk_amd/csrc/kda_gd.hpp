@@ -29,7 +29,7 @@ struct GdArgs {
 size_t gd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool io_bf16);
 size_t gd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
-                              bool packed, bool io_bf16);
+                              bool packed, bool io_bf16);  // for gates of either type
 hipError_t launch_gd_fwd(const GdArgs &a, hipStream_t st);
 hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st);
 
@@ -77,6 +77,7 @@ struct StateArgs {
     float *s_end;            // at the other end, or null
     void *o;                 // forward: [B,T,H,V]; reverse: dv
     char *rows;              // backward: [slots][H] tiles of [V][32]: the errors z, or the writes' gradients
+    int32_t parts;           // of a tile's values, bf16 I/O: 2, or 3 for all their bits
     float *seed;             // backward: states at the segments' borders [segs][H][K][V]
     int32_t tiles;           // column tiles
 };
@@ -90,7 +91,6 @@ struct GradArgs {
     float *dk_part;          // [B,T,H,K]: what the walk forward adds to dk
     void *dg, *dbeta;
     float scale;
-    int gates_fp32;
 };
 
 constexpr int state_tile(int V) { return V < 64 ? V : 64; }
@@ -98,6 +98,7 @@ constexpr int state_tile(int V) { return V < 64 ? V : 64; }
 enum Mode { kForward, kErrors, kReverse };  // outputs; the errors and states for the gradients; the state's gradients
 hipError_t state_pass(bool bf16, Mode mode, const StateArgs &a, int K, int V, hipStream_t st);
 hipError_t grad_pass_bf16(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
+hipError_t grad_pass_bf16_gates_fp32(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
 hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st);
 
 #ifdef __HIPCC__

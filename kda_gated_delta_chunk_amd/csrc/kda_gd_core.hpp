@@ -28,11 +28,6 @@ using hd::u32x2;
 using hd::u32x4;
 
 // ------------------------------------------------------------------ operands
-// A computed operand: bf16 I/O holds it as two bf16 parts (2^-18 of a value), fp32 I/O as it is.
-template <bool BF> struct Pair;
-template <> struct Pair<true> { Frag8<true> hi, lo; };
-template <> struct Pair<false> { Frag8<false> f; };
-
 // What rounding a pair left of its first (second) value: x - hi, exact, in one instruction. Where the pair's other value
 // is not finite the result is NaN: only for pairs that are summed over, or of finite values. (-1 comes in a register: as
 // an inline constant the instruction takes it for the upper half's.)
@@ -46,39 +41,63 @@ __device__ __forceinline__ float rest_hi(float x, uint32_t hi) {
     asm("" : "+s"(one));
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, hi), __builtin_bit_cast(bf16x2, one), x, false);
 }
-__device__ __forceinline__ void set_pair(Pair<true> &p, const float (&x)[8]) {
+// An operand in N bf16 parts (fp32 I/O: as it is): one for inputs, two hold a computed value to 2^-17 of it, three all
+// its 24 bits. Products leave out the parts' products that are too small to show beside the smallest part.
+template <bool BF, int N> struct Multi { Frag8<BF> p[BF ? N : 1]; };
+template <bool BF> using Exact = Multi<BF, 1>;
+template <bool BF> using Pair = Multi<BF, 2>;
+template <int N>
+__device__ __forceinline__ void set_multi(Multi<true, N> &m, const float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        p.hi.p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        p.lo.p[i] = pack_bf16(rest_lo(x[2 * i], p.hi.p[i]), rest_hi(x[2 * i + 1], p.hi.p[i]));
+        float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            m.p[n].p[i] = pack_bf16(a, b);
+            if (n + 1 < N) {
+                const float ra = rest_lo(a, m.p[n].p[i]), rb = rest_hi(b, m.p[n].p[i]);
+                a = ra;
+                b = rb;
+            }
+        }
     }
 }
-__device__ __forceinline__ void set_pair(Pair<false> &p, const float (&x)[8]) {
+template <int N>
+__device__ __forceinline__ void set_multi(Multi<false, N> &m, const float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p.f.f[i] = x[i];
+    for (int i = 0; i < 8; ++i) m.p[0].f[i] = x[i];
 }
-template <bool BF>
-__device__ __forceinline__ Pair<BF> pair_of(const f32x4 &u, const f32x4 &w) {
+template <bool BF, int N>
+__device__ __forceinline__ Multi<BF, N> multi_of(const f32x4 &u, const f32x4 &w) {
     const float x[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-    Pair<BF> p;
-    set_pair(p, x);
-    return p;
+    Multi<BF, N> m;
+    set_multi(m, x);
+    return m;
 }
-// The parts of a computed operand that the fp32 state is summed from: three bf16 parts are all 24 bits.
-template <bool BF> constexpr int kParts = BF ? 3 : 1;
-__device__ __forceinline__ void set_parts(Frag8<true> (&f)[3], const float (&x)[8]) {
+// c[i] += a[i] b[i] for M products at a time, their steps in turn: a matrix instruction waits for the one before it on its
+// accumulator. A single a or b serves all.
+template <bool BF, int M, int MA, int MB, int NA, int NB>
+__device__ __forceinline__ void mmx(f32x4 (&c)[M], const Multi<BF, NA> (&a)[MA], const Multi<BF, NB> (&b)[MB]) {
+    constexpr int PA = BF ? NA : 1, PB = BF ? NB : 1, MOST = PA > PB ? PA : PB;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[0].p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        const float a = rest_lo(x[2 * i], f[0].p[i]), b = rest_hi(x[2 * i + 1], f[0].p[i]);
-        f[1].p[i] = pack_bf16(a, b);
-        f[2].p[i] = pack_bf16(rest_lo(a, f[1].p[i]), rest_hi(b, f[1].p[i]));
-    }
-}
-__device__ __forceinline__ void set_parts(Frag8<false> (&f)[1], const float (&x)[8]) {
+    for (int s = 0; s < MOST; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[0].f[i] = x[i];
+        for (int i = 0; i <= s; ++i)
+            if (i < PA && s - i < PB)
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mma32(c[m], a[MA == 1 ? 0 : m].p[i], b[MB == 1 ? 0 : m].p[s - i]);
 }
+template <bool BF, int NA, int NB>
+__device__ __forceinline__ f32x4 mmx(f32x4 c, const Multi<BF, NA> &a, const Multi<BF, NB> &b) {
+    constexpr int PA = BF ? NA : 1, PB = BF ? NB : 1, MOST = PA > PB ? PA : PB;
+#pragma unroll
+    for (int s = 0; s < MOST; ++s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < PA && s - i < PB) c = mma32(c, a.p[i], b.p[s - i]);
+    return c;
+}
+
 __device__ __forceinline__ void widen(const Frag8<true> &f, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -91,63 +110,6 @@ __device__ __forceinline__ void widen(const Frag8<false> &f, float (&x)[8]) {
     for (int i = 0; i < 8; ++i) x[i] = f.f[i];
 }
 
-// Products of pairs (the two small parts' own product is left out) and of pairs with exact operands.
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<true> &a, const Pair<true> &b) {
-    c = mma32(c, a.hi, b.hi);
-    c = mma32(c, a.hi, b.lo);
-    return mma32(c, a.lo, b.hi);
-}
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<false> &a, const Pair<false> &b) { return mma32(c, a.f, b.f); }
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Frag8<true> &a, const Pair<true> &b) {
-    c = mma32(c, a, b.hi);
-    return mma32(c, a, b.lo);
-}
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Frag8<false> &a, const Pair<false> &b) { return mma32(c, a, b.f); }
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<true> &a, const Frag8<true> &b) {
-    c = mma32(c, a.hi, b);
-    return mma32(c, a.lo, b);
-}
-__device__ __forceinline__ f32x4 mm(f32x4 c, const Pair<false> &a, const Frag8<false> &b) { return mma32(c, a.f, b); }
-
-// Two products at a time, their steps in turn: a matrix instruction waits for the one before it on its accumulator.
-__device__ __forceinline__ const Frag8<true> &part_of(const Pair<true> &p, int i) { return i ? p.lo : p.hi; }
-__device__ __forceinline__ const Frag8<false> &part_of(const Pair<false> &p, int) { return p.f; }
-template <bool BF>
-__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Frag8<BF> (&a)[2], const Pair<BF> &b) {
-#pragma unroll
-    for (int p = 0; p < (BF ? 2 : 1); ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], a[t], part_of(b, p));
-}
-template <bool BF>
-__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> &a, const Frag8<BF> (&b)[2]) {
-#pragma unroll
-    for (int p = 0; p < (BF ? 2 : 1); ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a, p), b[t]);
-}
-template <bool BF>
-__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> (&a)[2], const Frag8<BF> (&b)[2]) {
-#pragma unroll
-    for (int p = 0; p < (BF ? 2 : 1); ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a[t], p), b[t]);
-}
-// (the two small parts' own product is left out)
-template <bool BF>
-__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> (&a)[2], const Pair<BF> &b) {
-#pragma unroll
-    for (int p = 0; p < (BF ? 3 : 1); ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a[t], p == 2), part_of(b, p == 1));
-}
-template <bool BF>
-__device__ __forceinline__ void mm2(f32x4 (&c)[2], const Pair<BF> &a, const Pair<BF> (&b)[2]) {
-#pragma unroll
-    for (int p = 0; p < (BF ? 3 : 1); ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mma32(c[t], part_of(a, p == 2), part_of(b[t], p == 1));
-}
 // The compiler would sink loads to where they are used.
 #define KDA_ORDER __builtin_amdgcn_sched_barrier(0)
 
@@ -300,24 +262,22 @@ struct BytesIn {
 
 // ------------------------------------------------------------------ records
 // A tile of a record's matrix as an operand, and one of its entries: row m of the tile, source slot j of lane group g.
-__device__ __forceinline__ void load_mat(const char *m, int tt, int lane, Pair<true> &p) {
+template <bool BF>
+__device__ __forceinline__ Pair<BF> load_mat(const char *m, int tt, int lane) {
+    Pair<BF> p;
     const u32x4 u = *reinterpret_cast<const u32x4 *>(m + ((2 * tt) * 64 + lane) * 16);
     const u32x4 w = *reinterpret_cast<const u32x4 *>(m + ((2 * tt + 1) * 64 + lane) * 16);
-    p.hi.p[0] = u.x; p.hi.p[1] = u.y; p.hi.p[2] = u.z; p.hi.p[3] = u.w;
-    p.lo.p[0] = w.x; p.lo.p[1] = w.y; p.lo.p[2] = w.z; p.lo.p[3] = w.w;
+    __builtin_memcpy(&p, &u, 16);
+    __builtin_memcpy(reinterpret_cast<char *>(&p) + 16, &w, 16);
+    return p;
 }
-__device__ __forceinline__ void load_mat(const char *m, int tt, int lane, Pair<false> &p) {
-    const f32x4 u = *reinterpret_cast<const f32x4 *>(m + ((2 * tt) * 64 + lane) * 16);
-    const f32x4 w = *reinterpret_cast<const f32x4 *>(m + ((2 * tt + 1) * 64 + lane) * 16);
-    p.f = Frag8<false>{{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w}};
-}
-__device__ __forceinline__ void store_mat(char *m, int tt, int lane, const Pair<true> &p) {
-    *reinterpret_cast<u32x4 *>(m + ((2 * tt) * 64 + lane) * 16) = u32x4{p.hi.p[0], p.hi.p[1], p.hi.p[2], p.hi.p[3]};
-    *reinterpret_cast<u32x4 *>(m + ((2 * tt + 1) * 64 + lane) * 16) = u32x4{p.lo.p[0], p.lo.p[1], p.lo.p[2], p.lo.p[3]};
-}
-__device__ __forceinline__ void store_mat(char *m, int tt, int lane, const Pair<false> &p) {
-    *reinterpret_cast<f32x4 *>(m + ((2 * tt) * 64 + lane) * 16) = f32x4{p.f.f[0], p.f.f[1], p.f.f[2], p.f.f[3]};
-    *reinterpret_cast<f32x4 *>(m + ((2 * tt + 1) * 64 + lane) * 16) = f32x4{p.f.f[4], p.f.f[5], p.f.f[6], p.f.f[7]};
+template <bool BF>
+__device__ __forceinline__ void store_mat(char *m, int tt, int lane, const Pair<BF> &p) {
+    u32x4 u, w;
+    __builtin_memcpy(&u, &p, 16);
+    __builtin_memcpy(&w, reinterpret_cast<const char *>(&p) + 16, 16);
+    *reinterpret_cast<u32x4 *>(m + ((2 * tt) * 64 + lane) * 16) = u;
+    *reinterpret_cast<u32x4 *>(m + ((2 * tt + 1) * 64 + lane) * 16) = w;
 }
 template <bool BF>
 __device__ __forceinline__ float mat_entry(const char *mat, int tt, int m, int g, int j) {
@@ -343,10 +303,10 @@ __device__ __forceinline__ bool finite(const Pair<true> &p) {
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p.hi.p[i]), __builtin_bit_cast(bf16x2, 0u), z, false);
+        z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p.p[0].p[i]), __builtin_bit_cast(bf16x2, 0u), z, false);
     return __builtin_amdgcn_ballot_w64(z != 0.f) == 0;
 }
-__device__ __forceinline__ bool finite(const Pair<false> &p) { return all_finite(p.f.f); }
+__device__ __forceinline__ bool finite(const Pair<false> &p) { return all_finite(p.p[0].f); }
 // acc[token][column] += sum over sources j of M[token][j] x_j[column], x in the lanes of their columns. REV: sources from
 // the token on, else up to it.
 template <bool BF, bool REV>
@@ -492,9 +452,9 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
         }
     }
     const int row0 = RK::row_at(lane), tile0 = RK::tile_at(lane), col0 = RV::col_at(lane, wave);
-    Pair<BF> sf[KC];  // the state as an operand
+    Pair<BF> sf[KC][1];  // the state as an operand
 #pragma unroll
-    for (int kc = 0; kc < KC; ++kc) sf[kc] = pair_of<BF>(st[2 * kc], st[2 * kc + 1]);
+    for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
     for (int cc = 0; cc < nch; ++cc) {
         const int c = chunk_of(cc), b = cc & (NB - 1);
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
@@ -521,29 +481,29 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 
         // ---- products with the state: K S, and S^T q. The operands are asked for ahead of the products.
         f32x4 x[2] = {zero4(), zero4()}, y[2] = {zero4(), zero4()};
-        Frag8<BF> kf[KC][2], qf[KC][2];
+        Exact<BF> kf[KC][2], qf[KC][2];
         Pair<BF> mat[2];
         float vx[8], r[8], z[8], w[8];
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) kf[kc][tt] = RK::row_frag(sk + 16 * tt * RK::RB, row0, kc);
+            for (int tt = 0; tt < 2; ++tt) kf[kc][tt].p[0] = RK::row_frag(sk + 16 * tt * RK::RB, row0, kc);
         const Frag8<BF> vf = RV::col_frag(sv, col0);
         weights(REV ? kLeave : kEnter, w);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) load_mat(sr + (REV ? kMatPT : kMatN) * kMatBytes, tt, lane, mat[tt]);
+        for (int tt = 0; tt < 2; ++tt) mat[tt] = load_mat<BF>(sr + (REV ? kMatPT : kMatN) * kMatBytes, tt, lane);
         if constexpr (MODE == kForward)
 #pragma unroll
             for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) qf[kc][tt] = RK::row_frag(sq_ + 16 * tt * RK::RB, row0, kc);
+                for (int tt = 0; tt < 2; ++tt) qf[kc][tt].p[0] = RK::row_frag(sq_ + 16 * tt * RK::RB, row0, kc);
         KDA_ORDER;
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) mm2(x, kf[kc], sf[kc]);
+        for (int kc = 0; kc < KC; ++kc) mmx(x, kf[kc], sf[kc]);
         KDA_ORDER;
         if constexpr (MODE == kForward)
 #pragma unroll
-            for (int kc = 0; kc < KC; ++kc) mm2(y, sf[kc], qf[kc]);
+            for (int kc = 0; kc < KC; ++kc) mmx(y, sf[kc], qf[kc]);
         KDA_ORDER;
         widen(vf, vx);
         mfma_fence(x[0], x[1]);
@@ -557,8 +517,8 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
             for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] *= w[i];
             const bool fine = all_finite(vx);
             if (fine) {
-                const Frag8<BF> f[2] = {vf, vf};
-                mm2(x, mat, f);
+                const Exact<BF> f[1] = {{{vf}}};
+                mmx(x, mat, f);
             } else {
                 mix_rows<BF, true>(x, vx, sr + kMatPT * kMatBytes, lane);
             }
@@ -566,12 +526,12 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = x[i >> 2][i & 3];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) load_mat(sr + kMatNT * kMatBytes, tt, lane, mat[tt]);
+            for (int tt = 0; tt < 2; ++tt) mat[tt] = load_mat<BF>(sr + kMatNT * kMatBytes, tt, lane);
         }
         {
-            Pair<BF> rp;
-            set_pair(rp, r);
-            mm2(x, mat, rp);
+            Pair<BF> rp[1];
+            set_multi(rp[0], r);
+            mmx(x, mat, rp);
         }
         KDA_ORDER;
         // the update's operands, while those products run
@@ -586,16 +546,16 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 y[tt] *= wt[kEnterScaled * C + 16 * tt + li];
-                load_mat(sr + kMatP * kMatBytes, tt, lane, mat[tt]);
+                mat[tt] = load_mat<BF>(sr + kMatP * kMatBytes, tt, lane);
             }
         }
         KDA_ORDER;
         mfma_fence(x[0], x[1]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
-        Pair<BF> zp;
-        set_pair(zp, z);
-        if (!finite(zp)) {  // a source that is not shows in its own row
+        Pair<BF> zp[1];
+        set_multi(zp[0], z);
+        if (!finite(zp[0])) {  // a source that is not shows in its own row
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = r[i];
             mix_rows<BF, REV>(x, r, sr + (REV ? kMatNT : kMatN) * kMatBytes, lane);
@@ -603,23 +563,28 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
             for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
             if constexpr (MODE == kForward) {
                 mix_cols<BF>(y, z, sr + kMatP * kMatBytes, lane);
-                zp = Pair<BF>{};
+                zp[0] = Pair<BF>{};
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) mat[tt] = Pair<BF>{};
             } else if constexpr (BF) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split_bf16(z[2 * i], z[2 * i + 1], zp.hi.p[i], zp.lo.p[i]);
+                for (int i = 0; i < 4; ++i) split_bf16(z[2 * i], z[2 * i + 1], zp[0].p[0].p[i], zp[0].p[1].p[i]);
             }
         }
         if constexpr (MODE == kForward) {
-            mm2(y, zp, mat);
+            mmx(y, zp, mat);
         } else {
             // ---- z or dw by columns: [V][32], the parts one after the other
-            char *rows = A.rows + ((sq.first + c) * A.c.H + h) * (int64_t)V * (C * 4);
+            char *rows = A.rows + ((sq.first + c) * A.c.H + h) * (int64_t)V * (C * (BF ? 2 * A.parts : 4));
             if constexpr (BF) {
                 char *p = rows + (col + li) * (C * 2) + 16 * g;
-                *reinterpret_cast<u32x4 *>(p) = u32x4{zp.hi.p[0], zp.hi.p[1], zp.hi.p[2], zp.hi.p[3]};
-                *reinterpret_cast<u32x4 *>(p + V * (C * 2)) = u32x4{zp.lo.p[0], zp.lo.p[1], zp.lo.p[2], zp.lo.p[3]};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) __builtin_memcpy(p + n * V * (C * 2), &zp[0].p[n], 16);
+                if (A.parts == 3) {
+                    Multi<true, 3> all;
+                    set_multi(all, z);
+                    __builtin_memcpy(p + 2 * V * (C * 2), &all.p[2], 16);
+                }
             } else {
                 char *p = rows + (col + li) * (C * 4) + 16 * g;
                 *reinterpret_cast<f32x4 *>(p) = f32x4{z[0], z[1], z[2], z[3]};
@@ -632,15 +597,15 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
             for (int i = 0; i < 8; ++i) w[i] *= z[i];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
-            Frag8<BF> f[kParts<BF>];
-            set_parts(f, w);
+            Multi<BF, 3> f;
+            set_multi(f, w);
             constexpr int KG = KT < 4 ? KT : 4;  // products of different tiles follow each other
 #pragma unroll
             for (int k0 = 0; k0 < KT; k0 += KG)
 #pragma unroll
-                for (int p = 0; p < kParts<BF>; ++p)
+                for (int p = 0; p < (BF ? 3 : 1); ++p)
 #pragma unroll
-                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], f[p]);
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], f.p[p]);
         } else {
             float wq[8], wk[8], be[8];
             weights(kEnterScaled, wq);
@@ -654,9 +619,9 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
             }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
-            Frag8<BF> f[kParts<BF>], e[kParts<BF>];
-            set_parts(f, wq);
-            set_parts(e, wk);
+            Multi<BF, 3> f, e;
+            set_multi(f, wq);
+            set_multi(e, wk);
             constexpr int KG = KT < 4 ? KT : 4;
 #pragma unroll
             for (int k0 = 0; k0 < KT; k0 += KG) {
@@ -664,13 +629,13 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 #pragma unroll
                 for (int j = 0; j < KG; ++j) a[j] = RK::tile_frag(sq_, tile0, k0 + j);
 #pragma unroll
-                for (int p = 0; p < kParts<BF>; ++p)
+                for (int p = 0; p < (BF ? 3 : 1); ++p)
 #pragma unroll
-                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], a[j], f[p]);
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], a[j], f.p[p]);
 #pragma unroll
-                for (int p = 0; p < kParts<BF>; ++p)
+                for (int p = 0; p < (BF ? 3 : 1); ++p)
 #pragma unroll
-                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], e[p]);
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], e.p[p]);
             }
             const auto out = __builtin_amdgcn_make_buffer_rsrc(po, 0, (tokens_of(c) - 1) * lv + V * EB, 0x00027000);
             po += step_v;
@@ -697,7 +662,7 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
         }
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][KT]>(st));
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) sf[kc] = pair_of<BF>(st[2 * kc], st[2 * kc + 1]);
+        for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
     }
     if (A.s_end) put_state(A.s_end + nh * sstate);
 }

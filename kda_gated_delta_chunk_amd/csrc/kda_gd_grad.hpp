@@ -19,9 +19,9 @@ namespace gd {
 // A tile of V channels x 32 tokens in LDS, from rows of the states' passes: 16 bytes of a row are the tokens of a lane
 // group's slots. bf16: the two halves (tiles of 16 tokens) in planes of their own, rows of 32 bytes ordered so that the
 // eight rows of a transposing read, and the sixteen of a row read, fall on different banks.
-template <bool BF, int V> struct Tile;
-template <int V> struct Tile<true, V> {
-    static constexpr int PLANE = V * 32, PART = 2 * PLANE, PARTS = 2;
+template <bool BF, int V, int NP> struct Tile;
+template <int V, int NP> struct Tile<true, V, NP> {
+    static constexpr int PLANE = V * 32, PART = 2 * PLANE;
     static __device__ __forceinline__ int at(int row, int g) {
         const int line = (row & 3) | (row & 24) >> 1 | (row & 4) << 2 | (row & ~31);
         return line * 32 + ((g ^ ((row >> 3) & 2)) << 3);
@@ -39,44 +39,50 @@ template <int V> struct Tile<true, V> {
         const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + PLANE);
         return Frag8<true>{{a.x, a.y, b.x, b.y}};
     }
-    static __device__ __forceinline__ Pair<true> cols_pair(const char *t, int at, int vc, int tt) {
-        return Pair<true>{cols(t, at, vc, tt), cols(t + PART, at, vc, tt)};
+    static __device__ __forceinline__ Multi<true, NP> all_cols(const char *t, int at, int vc, int tt) {
+        Multi<true, NP> m;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) m.p[n] = cols(t + n * PART, at, vc, tt);
+        return m;
     }
-    static __device__ __forceinline__ Pair<true> rows_pair(const char *t, int at, int vt) {
-        return Pair<true>{rows(t, at, vt), rows(t + PART, at, vt)};
+    static __device__ __forceinline__ Multi<true, NP> all_rows(const char *t, int at, int vt) {
+        Multi<true, NP> m;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) m.p[n] = rows(t + n * PART, at, vt);
+        return m;
     }
 };
-template <int V> struct Tile<false, V> {
+template <int V, int NP> struct Tile<false, V, NP> {
     using R = Rw<false, 32>;
-    static constexpr int PART = R::bytes(V), PARTS = 1;
+    static constexpr int PART = R::bytes(V);
     static __device__ __forceinline__ int cols_at(int lane) { return R::col_at(lane, 0); }
     static __device__ __forceinline__ int rows_at(int lane) { return R::row_at(lane); }
-    static __device__ __forceinline__ Pair<false> cols_pair(const char *t, int at, int vc, int tt) {
-        return Pair<false>{R::col_frag(t + 32 * vc * R::RB + 64 * tt, at)};
+    static __device__ __forceinline__ Multi<false, NP> all_cols(const char *t, int at, int vc, int tt) {
+        return {{R::col_frag(t + 32 * vc * R::RB + 64 * tt, at)}};
     }
-    static __device__ __forceinline__ Pair<false> rows_pair(const char *t, int at, int vt) {
-        return Pair<false>{R::row_frag(t + 16 * vt * R::RB, at, 0)};
+    static __device__ __forceinline__ Multi<false, NP> all_rows(const char *t, int at, int vt) {
+        return {{R::row_frag(t + 16 * vt * R::RB, at, 0)}};
     }
 };
-// On its way there: V * 128 bytes (both parts), 16 a load.
-template <bool BF, int V, int NT>
+// On its way there: all parts, 16 bytes a load.
+template <bool BF, int V, int NP, int NT>
 struct TileIn {
-    static constexpr int NL = V * 8 / NT > 0 ? V * 8 / NT : 1;
-    static_assert(V * 8 % NT == 0 || NT % (V * 8) == 0, "whole rounds");
+    using T = Tile<BF, V, NP>;
+    static constexpr int UNITS = V * (BF ? 4 * NP : 8), NL = (UNITS + NT - 1) / NT;
     u32x4 w[NL];
     int to[NL];
     uint32_t from[NL];
     __device__ __forceinline__ void init(int tid) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int u = (i * NT + tid) % (V * 8);
+            const int u = i * NT + tid < UNITS ? i * NT + tid : UNITS - 1;  // lanes left over bring the last once more
             from[i] = u * 16;
-            if constexpr (BF) to[i] = u / (V * 4) * Tile<true, V>::PART + Tile<true, V>::at(u / 4 % V, u & 3);
+            if constexpr (BF) to[i] = u / (V * 4) * T::PART + T::at(u / 4 % V, u & 3);
             else to[i] = Rw<false, 32>::slot(u / 8, u & 7);
         }
     }
     __device__ __forceinline__ void take(const char *p) {
-        const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, V * 128, 0x00027000);
+        const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, UNITS * 16, 0x00027000);
 #pragma unroll
         for (int i = 0; i < NL; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b128(b, from[i], 0, 0);
     }
@@ -85,39 +91,50 @@ struct TileIn {
         for (int i = 0; i < NL; ++i)
             if constexpr (BF) {
                 *reinterpret_cast<uint2 *>(t + to[i]) = make_uint2(w[i].x, w[i].y);
-                *reinterpret_cast<uint2 *>(t + to[i] + Tile<true, V>::PLANE) = make_uint2(w[i].z, w[i].w);
+                *reinterpret_cast<uint2 *>(t + to[i] + T::PLANE) = make_uint2(w[i].z, w[i].w);
             } else {
                 *reinterpret_cast<u32x4 *>(t + to[i]) = w[i];
             }
     }
 };
 
-template <bool BF, int K, int V>
+// The sum of the pieces of a product over a long axis.
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&x)[1]) { return x[0]; }
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&x)[2]) { return x[0] + x[1]; }
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&x)[4]) { return (x[0] + x[1]) + (x[2] + x[3]); }
+__device__ __forceinline__ void fence_each(f32x4 (&x)[1]) { mfma_fence(x[0]); }
+__device__ __forceinline__ void fence_each(f32x4 (&x)[2]) { mfma_fence(x[0], x[1]); }
+__device__ __forceinline__ void fence_each(f32x4 (&x)[4]) { mfma_fence(x[0], x[1], x[2], x[3]); }
+
+template <bool BF, int K, int V, int NP>
 struct GradLds {
-    static constexpr int C = kChunkTokens, NP = BF ? 2 : 1, NW = K / 16;
-    static constexpr int T_ = Tile<BF, V>::PART, M_ = Rw<BF, C>::bytes(C);  // a part of a tile, of a matrix
+    static constexpr int C = kChunkTokens, NM = BF ? 2 : 1, NW = K / 16;
+    static constexpr int T_ = (BF ? NP : 1) * Tile<BF, V, NP>::PART, M_ = Rw<BF, C>::bytes(C);  // a tile; a part of a matrix
     static constexpr int K_ = Rw<BF, K>::bytes(C), O_ = Rw<BF, V>::bytes(C);
-    static constexpr int dout = 0, z = dout + O_, dw = z + NP * T_, k = dw + NP * T_, q = k + K_, m1 = q + K_,
-                         m2 = m1 + NP * M_, wt = m2 + NP * M_, u = wt + kWeights * C * 4,
-                         db = u + NW * C * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
+    static constexpr int dout = 0, z = dout + O_, dw = z + T_, k = dw + T_, q = k + K_, m1 = q + K_,
+                         m2 = m1 + NM * M_, wt = m2 + NM * M_, u = wt + kWeights * C * 4, pairs = u + NW * C * 4,
+                         db = pairs + 2 * NW * C * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
 };
 
 // One segment of a (sequence, head); a wavefront 16 columns of K, all V rows of the transposed states in its registers.
-// YF: dq and dk in fp32 per v head.
-template <bool BF, int K, int V, bool YF>
+// YF: dq and dk in fp32 per v head. NP: parts of computed operands; GF: the gates' gradients in fp32.
+template <bool BF, int K, int V, bool YF, int NP>
 __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A) {
-    using L = GradLds<BF, K, V>;
+    using L = GradLds<BF, K, V, NP>;
     using RK = Rw<BF, K>;
     using RV = Rw<BF, V>;
     using RC = Rw<BF, kChunkTokens>;
-    using TV = Tile<BF, V>;
-    constexpr int NW = K / 16, NT = NW * 64, VT = V / 16, VC = V / 32, C = kChunkTokens, NP = L::NP;
-    constexpr int EB = BF ? 2 : 4;
+    using TV = Tile<BF, V, NP>;
+    constexpr int NW = L::NW, NT = NW * 64, VT = V / 16, VC = V / 32, KC = K / 32;
+    constexpr int C = kChunkTokens, EB = BF ? 2 : 4;
+    constexpr bool GF = !BF || NP == 3;
+    using Op = Multi<BF, NP>;
     __shared__ __align__(16) char smem[L::bytes];
     char *const s_do = smem + L::dout, *const s_z = smem + L::z, *const s_dw = smem + L::dw, *const s_k = smem + L::k,
          *const s_q = smem + L::q, *const s_m1 = smem + L::m1, *const s_m2 = smem + L::m2;
     float *const s_wt = reinterpret_cast<float *>(smem + L::wt), *const s_red = reinterpret_cast<float *>(smem + L::red);
     float(*const s_u)[C] = reinterpret_cast<float(*)[C]>(smem + L::u);
+    float(*const s_pairs)[C] = reinterpret_cast<float(*)[C]>(smem + L::pairs);
     float *const s_db = reinterpret_cast<float *>(smem + L::db);
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
@@ -127,31 +144,31 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     if (slot >= A.c.segs) return;
     const int64_t n = find_seq<true>(A.c, slot, lane);
     const Seq sq = seq_of(A.c, n);
-    const int64_t len = sq.t1 - sq.t0;
-    const int all = (int)((len + C - 1) / C);  // the sequence's chunks
+    const int len = (int)(sq.t1 - sq.t0);  // under 2^31
+    const int all = (int)(((int64_t)len + C - 1) / C);  // the sequence's chunks
     if (slot < sq.seg || (slot - sq.seg) * kSegmentChunks >= all) return;
     const int c0 = (int)(slot - sq.seg) * kSegmentChunks, c1 = c0 + kSegmentChunks < all ? c0 + kSegmentChunks : all;
-    const int nch = c1 - c0, col = wave * 16;
+    const int nch = c1 - c0, col = wave * 16;  // this wavefront's first column
     const int64_t sstate = (int64_t)K * V, nh = n * A.c.H + h;
 
     // a state [K][V] in memory as tiles of its transpose
-    auto add_state = [&](const float *s, f32x4 (&st)[VT]) __attribute__((always_inline)) {
+    auto get_state = [&](const float *s, f32x4 (&st)[VT]) __attribute__((always_inline)) {
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt)
             st[vt] = s ? *reinterpret_cast<const f32x4 *>(s + (int64_t)(col + li) * V + RV::state_row(vt, g)) : zero4();
     };
     f32x4 st[VT];
-    add_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
+    get_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
     hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
 
     const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (V * EB);
     const char *pk = reinterpret_cast<const char *>(A.k) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
     const char *pq = reinterpret_cast<const char *>(A.q) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
     const char *pd = reinterpret_cast<const char *>(A.dout) + (sq.t0 * A.c.H + h) * (V * EB);
-    const int64_t tile = (int64_t)V * (C * 4);
+    constexpr int64_t tile = (int64_t)V * C * (BF ? 2 * NP : 4);
     RowsIn<BF, K, C, NT> rk, rq;
     RowsIn<BF, V, C, NT> rd;
-    TileIn<BF, V, NT> rz, rw;
+    TileIn<BF, V, NP, NT> rz, rw;
     rk.init(tid, lk);
     rq.init(tid, lk);
     rd.init(tid, lv);
@@ -160,7 +177,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     u32x4 rwt;
     auto take = [&](int c) __attribute__((always_inline)) {
         const int64_t t = (int64_t)c * C, at = (sq.first + c) * A.c.H + h;
-        const int m = (int)(len - t < C ? len - t : C);
+        const int m = len - (int)t < C ? len - (int)t : C;
         rk.take(pk + t * lk, m);
         rq.take(pq + t * lk, m);
         rd.take(pd + t * lv, m);
@@ -174,23 +191,20 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         rd.put(s_do);
         rz.put(s_z);
         rw.put(s_dw);
-        if (tid < 64) *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(s_wt) + tid * 16) = rwt;
+        if (wave == 0) *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(s_wt) + tid * 16) = rwt;
     };
-    const int rowv0 = RV::row_at(lane), rowc0 = RC::row_at(lane), colk0 = RK::col_at(lane, wave), tilev0 = RV::tile_at(lane);
+    const int rowv0 = RV::row_at(lane), rowk0 = RK::row_at(lane), rowc0 = RC::row_at(lane), tilev0 = RV::tile_at(lane);
     const int tcols0 = TV::cols_at(lane), trows0 = TV::rows_at(lane);
+    const int colk0 = RK::col_at(lane, wave);
     auto tile_cols = [&](const char *s, int vc, int tt) __attribute__((always_inline)) {
-        return TV::cols_pair(s, tcols0, vc, tt);
+        return TV::all_cols(s, tcols0, vc, tt);
     };
-    auto tile_rows = [&](const char *s, int vt) __attribute__((always_inline)) { return TV::rows_pair(s, trows0, vt); };
+    auto tile_rows = [&](const char *s, int vt) __attribute__((always_inline)) { return TV::all_rows(s, trows0, vt); };
     // The matrices of the pairs' weights: sixteen bytes of a row are the tokens of a lane group's slots, as in a tile.
     auto mat_row = [&](const char *s, int tt) __attribute__((always_inline)) {
         Pair<BF> p;
-        if constexpr (BF) {
-            p.hi = RC::row_frag(s + 16 * tt * RC::RB, rowc0, 0);
-            p.lo = RC::row_frag(s + L::M_ + 16 * tt * RC::RB, rowc0, 0);
-        } else {
-            p.f = RC::row_frag(s + 16 * tt * RC::RB, rowc0, 0);
-        }
+#pragma unroll
+        for (int n = 0; n < L::NM; ++n) p.p[n] = RC::row_frag(s + n * L::M_ + 16 * tt * RC::RB, rowc0, 0);
         return p;
     };
     auto put_mat = [&](char *s, int row, int ts, const f32x4 &w) __attribute__((always_inline)) {  // sources 16 ts + 4g ..
@@ -214,7 +228,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         }
     };
     auto clear_mats = [&]() __attribute__((always_inline)) {  // the tiles across the diagonal are read, never computed
-        for (int i = tid; i < 2 * NP * L::M_ / 16; i += NT) reinterpret_cast<uint4 *>(s_m1)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < 2 * L::NM * L::M_ / 16; i += NT) reinterpret_cast<uint4 *>(s_m1)[i] = make_uint4(0, 0, 0, 0);
     };
     auto weights = [&](int which, float (&w)[8]) __attribute__((always_inline)) {
         *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(s_wt + which * C + token_of(0, g));
@@ -229,7 +243,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         for (int i = 0; i < 4; ++i)
             e[i] = __builtin_amdgcn_exp2f(later ? (sh[i] - th) + (sl[i] - tl) : (th - sh[i]) + (tl - sl[i]));
     };
-    // a token's dot of rows x with a result y (columns 4g + i of token 16 tt + l % 16), over this wavefront's columns
+    // a token's dot of rows x with a result y (columns 4g + i of token 16 tt + l % 16) over this wavefront's columns
     auto dot = [&](const char *x, int tt, const f32x4 &y) __attribute__((always_inline)) {
         float r[4];
         RK::load_quad(x, 16 * tt + li, col + 4 * g, r);
@@ -238,22 +252,24 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         for (int i = 0; i < 4; ++i) d = fmaf(r[i], y[i], d);
         return d;
     };
-    auto store = [&](void *p, int64_t t, const f32x4 &y, bool live) __attribute__((always_inline)) {
-        if (!live) return;
-        const int64_t at = (t * A.c.H + h) * K + col + 4 * g;
+    auto put_dot = [&](int tt, float d) __attribute__((always_inline)) {
+        d += __shfl_xor(d, 16);
+        d += __shfl_xor(d, 32);
+        if (g == 0) s_u[wave][16 * tt + li] = d;
+    };
+    auto at_of = [&](int64_t t) __attribute__((always_inline)) { return (t * A.c.H + h) * K + col + 4 * g; };
+    auto store = [&](void *p, int64_t at, const f32x4 &y) __attribute__((always_inline)) {
         if constexpr (BF && !YF)
             *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + at) =
                 make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
         else
             *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p) + at) = y;
     };
-
-    // y += the first matrix times the rows at s (f, x: this wavefront's columns of them); see all_finite
-    auto mix = [&](f32x4 (&y)[2], const Frag8<BF> &f, const float (&x)[8], const char *s, bool later, int m)
-                   __attribute__((always_inline)) {
+    // y += the first matrix times the rows at s (f: this wavefront's columns of them); see all_finite
+    auto mix = [&](f32x4 (&y)[2], const Exact<BF> (&f)[1], const float (&x)[8], const Pair<BF> (&mat)[2], const char *s,
+                   bool later, int m) __attribute__((always_inline)) {
         if (all_finite(x)) {
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], f, mat_row(s_m1, tt));
+            mmx(y, f, mat);
             return;
         }
 #pragma unroll 1
@@ -276,33 +292,50 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     clear_mats();
     for (int c = c0; c < c1; ++c) {
         const int64_t tc = sq.t0 + (int64_t)c * C;
-        const int m = (int)(sq.t1 - tc < C ? sq.t1 - tc : C);
+        const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
         __syncthreads();  // the last chunk's rows and matrices are read
         put();
-        if (c + 1 < c1) take(c + 1);
-        else take(c);  // the walk back begins with the last one
+        take(c + 1 < c1 ? c + 1 : c);  // the walk back begins with the last one
+        if (lane < C) s_pairs[2 * wave][lane] = s_pairs[2 * wave + 1][lane] = 0.f;
         __syncthreads();
         // ---- the pairs' weights: lane holds sources i = 16 ts + 4g .. of token r = 16 tt + l % 16
         for (int p = wave; p < 6; p += NW) {
             const int which = p >= 3, x = which ? p - 3 : p, tt = x > 0, ts = x > 1;
-            f32x4 acc = zero4(), e;
+            f32x4 part[VC], acc, prod = zero4(), e;
             const int r = 16 * tt + li, i0 = 16 * ts + 4 * g;
+            Op z[VC];
 #pragma unroll
             for (int vc = 0; vc < VC; ++vc) {
-                const Pair<BF> z = tile_cols(s_z, vc, ts);
-                if (which) acc = mm(acc, z, tile_cols(s_dw, vc, tt));
-                else acc = mm(acc, z, RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc));
+                part[vc] = zero4();
+                z[vc] = tile_cols(s_z, vc, ts);
             }
+            if (which) {
+                Op w[VC];
+#pragma unroll
+                for (int vc = 0; vc < VC; ++vc) w[vc] = tile_cols(s_dw, vc, tt);
+                mmx(part, z, w);
+            } else {
+                Exact<BF> d[VC];
+#pragma unroll
+                for (int vc = 0; vc < VC; ++vc) d[vc].p[0] = RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc);
+                mmx(part, z, d);
+            }
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc)
+                prod = mma32(prod, RK::row_frag(s_k + 16 * ts * RK::RB, rowk0, kc),
+                             RK::row_frag((which ? s_k : s_q) + 16 * tt * RK::RB, rowk0, kc));
             decays(r, i0, false, e);
             const f32x4 be = *reinterpret_cast<const f32x4 *>(s_wt + kBeta * C + i0);
             const float f = which ? -s_wt[kBeta * C + r] : A.scale;
-            mfma_fence(acc);
+            fence_each(part);
+            acc = sum_of(part);
+            mfma_fence(prod);
             if (which && tt == ts && r < m) {  // M's diagonal
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i0 + i == r) {
                         const int64_t at = (tc + r) * A.c.H + h;
-                        if (BF && !A.gates_fp32) IO<true>::st(reinterpret_cast<uint16_t *>(A.dbeta), at, acc[i]);
+                        if (!GF) IO<true>::st(reinterpret_cast<uint16_t *>(A.dbeta), at, acc[i]);
                         else reinterpret_cast<float *>(A.dbeta)[at] = acc[i];
                     }
             }
@@ -310,17 +343,34 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             for (int i = 0; i < 4; ++i)
                 acc[i] = (which ? i0 + i < r : i0 + i <= r) && r < m ? f * acc[i] * e[i] * be[i] : 0.f;
             put_mat(which ? s_m2 : s_m1, r, ts, acc);
+            // pairs of the log-decays' gradient: + at the row, - at the source
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float X = i0 + i < r ? acc[i] * prod[i] : 0.f;
+                sum += X;
+                const float all16 = row_scan16(X);  // the source's sum, in its last lane
+                if (li == 15) s_pairs[2 * wave][i0 + i] -= all16;
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (g == 0) s_pairs[2 * wave + 1][r] += sum;
+            __builtin_amdgcn_wave_barrier();
         }
         // ---- what the state gives
         f32x4 y1[2] = {zero4(), zero4()}, y2[2] = {zero4(), zero4()};
 #pragma unroll
         for (int vc = 0; vc < VC; ++vc) {
-            const Pair<BF> s = pair_of<BF>(st[2 * vc], st[2 * vc + 1]);
+            Exact<BF> d[2];
+            Op w[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                y1[tt] = mm(y1[tt], s, RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc));
-                y2[tt] = mm(y2[tt], s, tile_cols(s_dw, vc, tt));
+                d[tt].p[0] = RV::row_frag(s_do + 16 * tt * RV::RB, rowv0, vc);
+                w[tt] = tile_cols(s_dw, vc, tt);
             }
+            const Op s[1] = {multi_of<BF, NP>(st[2 * vc], st[2 * vc + 1])};
+            mmx(y1, s, d);
+            mmx(y2, s, w);
         }
         mfma_fence(y1[0], y1[1], y2[0], y2[1]);
 #pragma unroll
@@ -328,52 +378,52 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             const int t = 16 * tt + li;
             y1[tt] *= s_wt[kEnterScaled * C + t];
             y2[tt] *= -s_wt[kEnter * C + t] * s_wt[kBeta * C + t];
-        }
-        __syncthreads();
-        const Frag8<BF> kf = RK::col_frag(s_k, colk0);
-        float kx[8];
-        widen(kf, kx);
-        mix(y1, kf, kx, s_k, false, m);
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y2[tt] = mm(y2[tt], kf, mat_row(s_m2, tt));
-        // ---- the state's update
-        const float total = s_wt[kTotal * C];
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) st[vt] *= total;
-        {
-            float w[8];
-            weights(kLeaveBeta, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= kx[i];
-            Pair<BF> kp;
-            set_pair(kp, w);
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) st[vt] = mm(st[vt], tile_rows(s_z, vt), kp);
-        }
-        // ---- results
-        mfma_fence(y1[0], y1[1], y2[0], y2[1]);
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            const int t = 16 * tt + li;
-            store(A.dq, tc + t, y1[tt], t < m);
-            if (t < m) *reinterpret_cast<f32x4 *>(A.dk_part + ((tc + t) * A.c.H + h) * K + col + 4 * g) = y2[tt];
-            float d = dot(s_q, tt, y1[tt]) + dot(s_k, tt, y2[tt]);
-            d += __shfl_xor(d, 16);
-            d += __shfl_xor(d, 32);
-            if (g == 0) s_u[wave][t] = d;
+            put_dot(tt, dot(s_q, tt, y1[tt]) + dot(s_k, tt, y2[tt]));
         }
         __syncthreads();
         if (tid < C) {
             float d = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
+            for (int w = 0; w < NW; ++w) d += s_u[w][tid] + (s_pairs[2 * w][tid] + s_pairs[2 * w + 1][tid]);
             s_db[(c - c0) * C + tid] = tid < m ? d : 0.f;
         }
+        Pair<BF> mat1[2], mat2[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            mat1[tt] = mat_row(s_m1, tt);
+            mat2[tt] = mat_row(s_m2, tt);
+        }
+        const Exact<BF> kf[1] = {{{RK::col_frag(s_k, colk0)}}};
+        float kx[8], w[8];
+        widen(kf[0].p[0], kx);
+        mix(y1, kf, kx, mat1, s_k, false, m);
+        mmx(y2, kf, mat2);
+        // ---- the state's update
+        weights(kLeaveBeta, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= kx[i];
+        Op kp;
+        set_multi(kp, w);
+        const float total = s_wt[kTotal * C];
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+            st[vt] *= total;
+            st[vt] = mmx(st[vt], tile_rows(s_z, vt), kp);
+        }
+        // ---- results
+        mfma_fence(y1[0], y1[1], y2[0], y2[1]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+            if (16 * tt + li < m) {
+                const int64_t at = at_of(tc + 16 * tt + li);
+                store(A.dq, at, y1[tt]);
+                *reinterpret_cast<f32x4 *>(A.dk_part + at) = y2[tt];
+            }
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
     }
     // ---- what the border behind the segment passes on
     f32x4 gt[VT];
-    add_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
+    get_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
     float border = 0.f;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
@@ -389,26 +439,42 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     clear_mats();
     for (int c = c1 - 1; c >= c0; --c) {
         const int64_t tc = sq.t0 + (int64_t)c * C;
-        const int m = (int)(sq.t1 - tc < C ? sq.t1 - tc : C);
+        const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
         __syncthreads();
         put();
         if (c > c0) take(c - 1);
+        f32x4 read[2];  // what the walk forward left for dk
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+            if (16 * tt + li < m) read[tt] = *reinterpret_cast<const f32x4 *>(A.dk_part + at_of(tc + 16 * tt + li));
         __syncthreads();
         // ---- the pairs' weights the other way round: lane holds tokens j = 16 ts + 4g .. that see token r = 16 tt + l % 16
         for (int p = wave; p < 6; p += NW) {
             const int which = p >= 3, x = which ? p - 3 : p, ts = x > 0, tt = x > 1;
-            f32x4 acc = zero4(), e;
+            f32x4 part[VC], acc, e;
             const int r = 16 * tt + li, j0 = 16 * ts + 4 * g;
+            Op z[VC];
 #pragma unroll
             for (int vc = 0; vc < VC; ++vc) {
-                const Pair<BF> z = tile_cols(s_z, vc, tt);
-                if (which) acc = mm(acc, tile_cols(s_dw, vc, ts), z);
-                else acc = mm(acc, RV::row_frag(s_do + 16 * ts * RV::RB, rowv0, vc), z);
+                part[vc] = zero4();
+                z[vc] = tile_cols(s_z, vc, tt);
+            }
+            if (which) {
+                Op w[VC];
+#pragma unroll
+                for (int vc = 0; vc < VC; ++vc) w[vc] = tile_cols(s_dw, vc, ts);
+                mmx(part, w, z);
+            } else {
+                Exact<BF> d[VC];
+#pragma unroll
+                for (int vc = 0; vc < VC; ++vc) d[vc].p[0] = RV::row_frag(s_do + 16 * ts * RV::RB, rowv0, vc);
+                mmx(part, d, z);
             }
             decays(r, j0, true, e);
             const f32x4 be = *reinterpret_cast<const f32x4 *>(s_wt + kBeta * C + j0);
             const float f = s_wt[kBeta * C + r];
-            mfma_fence(acc);
+            fence_each(part);
+            acc = sum_of(part);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 acc[i] = (which ? j0 + i > r : j0 + i >= r) && j0 + i < m ? f * acc[i] * e[i] * (which ? -be[i] : A.scale) : 0.f;
@@ -417,25 +483,39 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         f32x4 y[2] = {zero4(), zero4()};
 #pragma unroll
         for (int vc = 0; vc < VC; ++vc) {
-            const Pair<BF> s = pair_of<BF>(gt[2 * vc], gt[2 * vc + 1]);
+            Op z[2];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], s, tile_cols(s_z, vc, tt));
+            for (int tt = 0; tt < 2; ++tt) z[tt] = tile_cols(s_z, vc, tt);
+            const Op s[1] = {multi_of<BF, NP>(gt[2 * vc], gt[2 * vc + 1])};
+            mmx(y, s, z);
         }
         mfma_fence(y[0], y[1]);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y[tt] *= s_wt[kLeaveBeta * C + 16 * tt + li];
+        for (int tt = 0; tt < 2; ++tt) {
+            y[tt] *= s_wt[kLeaveBeta * C + 16 * tt + li];
+            put_dot(tt, dot(s_k, tt, y[tt]));
+        }
         __syncthreads();
-        const Frag8<BF> kf = RK::col_frag(s_k, colk0), qf = RK::col_frag(s_q, colk0);
+        if (tid < m) {
+            float d = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
+            s_db[(c - c0) * C + tid] -= d;
+        }
+        Pair<BF> mat1[2], mat2[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            mat1[tt] = mat_row(s_m1, tt);
+            mat2[tt] = mat_row(s_m2, tt);
+        }
+        const Exact<BF> kf[1] = {{{RK::col_frag(s_k, colk0)}}}, qf[1] = {{{RK::col_frag(s_q, colk0)}}};
         float qx[8], kx[8];
-        widen(qf, qx);
-        widen(kf, kx);
-        mix(y, qf, qx, s_q, true, m);
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y[tt] = mm(y[tt], kf, mat_row(s_m2, tt));
+        widen(qf[0].p[0], qx);
+        widen(kf[0].p[0], kx);
+        mix(y, qf, qx, mat1, s_q, true, m);
+        mmx(y, kf, mat2);
         // ---- the state gradient's update
-        const float total = s_wt[kTotal * C];
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) gt[vt] *= total;
+        Op qp, kp;
         {
             float w[8], e[8], be[8];
             weights(kEnterScaled, w);
@@ -446,40 +526,28 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
                 w[i] *= qx[i];
                 e[i] *= -be[i] * kx[i];
             }
-            Pair<BF> qp, kp;
-            set_pair(qp, w);
-            set_pair(kp, e);
+            set_multi(qp, w);
+            set_multi(kp, e);
+        }
+        const float total = s_wt[kTotal * C];
 #pragma unroll
-            for (int vt = 0; vt < VT; ++vt) {
-                gt[vt] = mm(gt[vt], RV::tile_frag(s_do, tilev0, vt), qp);
-                gt[vt] = mm(gt[vt], tile_rows(s_dw, vt), kp);
-            }
+        for (int vt = 0; vt < VT; ++vt) {
+            gt[vt] *= total;
+            const Exact<BF> d = {{RV::tile_frag(s_do, tilev0, vt)}};
+            gt[vt] = mmx(gt[vt], d, qp);
+            gt[vt] = mmx(gt[vt], tile_rows(s_dw, vt), kp);
         }
         mfma_fence(y[0], y[1]);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            const int t = 16 * tt + li;
-            float d = dot(s_k, tt, y[tt]);
-            if (t < m) y[tt] += *reinterpret_cast<const f32x4 *>(A.dk_part + ((tc + t) * A.c.H + h) * K + col + 4 * g);
-            store(A.dk, tc + t, y[tt], t < m);
-            d += __shfl_xor(d, 16);
-            d += __shfl_xor(d, 32);
-            if (g == 0) s_u[wave][t] = d;
-        }
-        __syncthreads();
-        if (tid < C && tid < m) {
-            float d = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
-            s_db[(c - c0) * C + tid] -= d;
-        }
+        for (int tt = 0; tt < 2; ++tt)
+            if (16 * tt + li < m) store(A.dk, at_of(tc + 16 * tt + li), y[tt] + read[tt]);
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(gt));
     }
     __syncthreads();
     // ---- dg: the sums from a token to the border, in fp64
     if (wave == 0) {
         constexpr int PER = kSegmentChunks * C / 64;
-        double own[PER], sum = 0.0, later = 0.0;
+        double own[PER], sum = 0.0;
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i) {
             const int t = lane * PER + i;
@@ -492,38 +560,37 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             const double x = __shfl_down(upto, d);
             if (lane + d < 64) upto += x;
         }
-        later = upto - sum;
-        double b = 0.0;
+        double b = upto - sum;
 #pragma unroll
         for (int w = 0; w < NW; ++w) b += s_red[w];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int64_t t = sq.t0 + (int64_t)c0 * C + lane * PER + i;
-            const float x = (float)(own[i] + later + b);
             if (t < sq.t1 && lane * PER + i < nch * C) {
-                if (BF && !A.gates_fp32) IO<true>::st(reinterpret_cast<uint16_t *>(A.dg), t * A.c.H + h, x);
+                const float x = (float)(own[i] + b);
+                if (!GF) IO<true>::st(reinterpret_cast<uint16_t *>(A.dg), t * A.c.H + h, x);
                 else reinterpret_cast<float *>(A.dg)[t * A.c.H + h] = x;
             }
         }
     }
 }
 
-template <bool BF, int K, int V, bool YF>
+template <bool BF, int K, int V, bool YF, int NP>
 hipError_t launch_grad(const GradArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((kda_gd_grad_kernel<BF, K, V, YF>), hd::wide_grid(a.c.segs * a.c.H), dim3(K * 4), 0, st, a);
+    hipLaunchKernelGGL((kda_gd_grad_kernel<BF, K, V, YF, NP>), hd::wide_grid(a.c.segs * a.c.H), dim3(K * 4), 0, st, a);
     return hipGetLastError();
 }
-template <bool BF, int K, bool YF>
+template <bool BF, int K, bool YF, int NP>
 hipError_t grad_by_v(const GradArgs &a, int V, hipStream_t st) {
-    return V == 32   ? launch_grad<BF, K, 32, YF>(a, st)
-           : V == 64 ? launch_grad<BF, K, 64, YF>(a, st)
-                     : launch_grad<BF, K, 128, YF>(a, st);
+    return V == 32   ? launch_grad<BF, K, 32, YF, NP>(a, st)
+           : V == 64 ? launch_grad<BF, K, 64, YF, NP>(a, st)
+                     : launch_grad<BF, K, 128, YF, NP>(a, st);
 }
-template <bool BF, bool YF>
+template <bool BF, bool YF, int NP>
 hipError_t grad_by_k(const GradArgs &a, int K, int V, hipStream_t st) {
-    return K == 32   ? grad_by_v<BF, 32, YF>(a, V, st)
-           : K == 64 ? grad_by_v<BF, 64, YF>(a, V, st)
-                     : grad_by_v<BF, 128, YF>(a, V, st);
+    return K == 32   ? grad_by_v<BF, 32, YF, NP>(a, V, st)
+           : K == 64 ? grad_by_v<BF, 64, YF, NP>(a, V, st)
+                     : grad_by_v<BF, 128, YF, NP>(a, V, st);
 }
 
 }  // namespace gd

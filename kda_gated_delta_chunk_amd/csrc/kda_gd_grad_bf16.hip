@@ -4,7 +4,7 @@
 namespace kda {
 namespace gd {
 hipError_t grad_pass_bf16(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st) {
-    return y_fp32 ? grad_by_k<true, true>(a, K, V, st) : grad_by_k<true, false>(a, K, V, st);
+    return y_fp32 ? grad_by_k<true, true, 2>(a, K, V, st) : grad_by_k<true, false, 2>(a, K, V, st);
 }
 }  // namespace gd
 }  // namespace kda

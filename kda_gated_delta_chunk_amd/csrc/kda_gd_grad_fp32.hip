@@ -3,6 +3,6 @@
 
 namespace kda {
 namespace gd {
-hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st) { return grad_by_k<false, true>(a, K, V, st); }
+hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st) { return grad_by_k<false, true, 2>(a, K, V, st); }
 }  // namespace gd
 }  // namespace kda
