@@ -589,9 +589,9 @@ kda_status_t kda_gd_chunk_fwd(const void *q, const void *k, const void *v, const
  * Nothing from a forward call is needed; the result is deterministic. Rows of
  * tokens outside every sequence are not written. A non-finite value reaches,
  * in its own head and sequence, what depends on it: a v dq and dk from its
- * token on, a q or d_o dk and dv up to its token, a k dq from its token on and
- * dk and dv up to it, a g or beta these and the rest of its 32-token chunk;
- * and any of them may spoil every dg and dbeta.
+ * token on, a q or d_o dk and dv up to its token (d_o also its dq), a k dq from
+ * its token on, dv up to it and every dk, a g or beta all of these; and any of
+ * them may spoil every dg and dbeta.
  */
 kda_status_t kda_gd_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
                               const float *S0, const int32_t *cu_seqlens, const void *d_o, const float *dS_final,

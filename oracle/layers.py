@@ -131,3 +131,36 @@ def norm_backward(dy, x, w=None, b=None, z=None, eps=1e-5, center=True):
         dx = dx - d.sum(-1, keepdim=True) / C
     out["dx"] = r * dx
     return out
+
+
+def rotate_axes(x, freqs, axes, positions, layout="half", inverse=False, scale=1.0):
+    """rotate() with several axes, pair by pair: pair j turns by positions[axes[j]]."""
+    y, P = f64(x).clone(), freqs.numel()
+    for j in range(P):
+        angle = f64(positions)[int(axes[j])][..., None] * f64(freqs)[j] * (-1.0 if inverse else 1.0)
+        one, two = (j, j + P) if layout == "half" else (2 * j, 2 * j + 1)
+        a, b = f64(x)[..., one], f64(x)[..., two]
+        y[..., one] = scale * (a * torch.cos(angle) - b * torch.sin(angle))
+        y[..., two] = scale * (a * torch.sin(angle) + b * torch.cos(angle))
+    return y
+
+
+def save8(x):
+    """(codes, scales) of a checkpoint in 8 bits, block by block: the exact quotients are formed in whole numbers where
+    they could be a tie (127 x is exact in fp64)."""
+    x = f64(x)
+    codes, scales = torch.zeros_like(x), []
+    for c in range(0, x.shape[-1], 128):
+        b = x[..., c:c + 128]
+        top = b.abs().amax(-1, keepdim=True)
+        codes[..., c:c + 128] = torch.where(top > 0, torch.round(127 * b / top.clamp(min=1e-300)), 0.0)
+        scales.append(top / 127)
+    return codes.to(torch.int8), torch.cat(scales, -1)
+
+
+def restore8(codes, scales):
+    """The values in fp64, unrounded."""
+    x = f64(codes)
+    for i in range(scales.shape[-1]):
+        x[..., 128 * i:128 * i + 128] *= f64(scales)[..., i, None]
+    return x
