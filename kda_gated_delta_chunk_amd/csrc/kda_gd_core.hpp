@@ -361,7 +361,7 @@ struct StateLds {
 // One (sequence, head), columns vt * VT .. of the state, a wavefront 16 of them: all K rows as fp32 accumulators, which
 // are at once operands of the products with the state, so it never leaves the registers.
 template <bool BF, int K, int VT, int MODE>
-__global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs A, int V) {
+__global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs A, int V) {
     using L = StateLds<BF, K, VT, MODE>;
     using RK = Rw<BF, K>;
     using RV = Rw<BF, VT>;
@@ -383,6 +383,62 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
     const int len = (int)(sq.t1 - sq.t0);  // under 2^31
     const int nch = (int)(((int64_t)len + C - 1) / C);
     const int col = vt * VT + wave * 16;  // this wavefront's first column
+
+    // ---- the second half of the wavefronts: rows on their way to LDS
+    if (wave >= NW) {
+        const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (uint32_t)(V * EB);
+        constexpr int RECB = L::R_;
+        RowsIn<BF, K, C, NT> rk, rq;
+        RowsIn<BF, VT, C, NT> rv;
+        BytesIn<RECB, NT> rr;
+        rk.init(tid - NT, lk);
+        rq.init(tid - NT, lk);
+        rv.init(tid - NT, lv);
+        rr.init(tid - NT);
+        // the next chunk to be asked for, and where it lies
+        const int64_t c_first = REV ? nch - 1 : 0, step = REV ? -1 : 1;
+        const char *pk = reinterpret_cast<const char *>(A.k) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
+        const char *pq = reinterpret_cast<const char *>(A.q) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
+        const char *pv = reinterpret_cast<const char *>(A.v) + (((sq.t0 + c_first * C) * A.c.H + h) * V + vt * VT) * EB;
+        const char *prec = A.c.rec + ((sq.first + c_first) * A.c.H + h) * RECB;
+        const int64_t step_k = step * C * lk, step_v = step * C * lv, step_r = step * A.c.H * RECB;
+        auto take = [&](int i) __attribute__((always_inline)) {
+            const int c = REV ? nch - 1 - i : i, m = len - c * C < C ? len - c * C : C;
+            rk.take(pk, m);
+            if constexpr (MODE != kErrors) rq.take(pq, m);
+            rv.take(pv, m);
+            rr.take(prec);
+            pk += step_k;
+            if constexpr (MODE != kErrors) pq += step_k;
+            pv += step_v;
+            prec += step_r;
+        };
+        auto put = [&](int b) __attribute__((always_inline)) {
+            rk.put(smem + L::k + b * L::K_);
+            if constexpr (MODE != kErrors) rq.put(smem + L::q + b * L::K_);
+            rv.put(smem + L::v + b * L::V_);
+            rr.put(smem + L::rec + b * L::R_);
+        };
+        if (nch > 0) {
+            take(0);
+            if constexpr (NB == 2) {
+                put(0);
+                if (nch > 1) take(1);
+            }
+        }
+        for (int cc = 0; cc < nch; ++cc) {
+            __syncthreads();
+            if constexpr (NB == 1) {
+                put(0);
+                if (cc + 1 < nch) take(cc + 1);
+                __syncthreads();
+            } else if (cc + 1 < nch) {
+                put((cc + 1) & 1);
+                if (cc + 2 < nch) take(cc + 2);
+            }
+        }
+        return;
+    }
 
     // ---- the state at its start
     f32x4 st[KT];
@@ -407,65 +463,18 @@ __global__ __launch_bounds__(VT * 4, 2) void kda_gd_state_kernel(const StateArgs
 
     hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][KT]>(st));  // the loads end here: no waits for them in the loop
 
-    // ---- the rows' ways
-    const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (uint32_t)(V * EB);
-    constexpr int RECB = L::R_;
-    RowsIn<BF, K, C, NT> rk, rq;
-    RowsIn<BF, VT, C, NT> rv;
-    BytesIn<RECB, NT> rr;
-    rk.init(tid, lk);
-    rq.init(tid, lk);
-    rv.init(tid, lv);
-    rr.init(tid);
-    // the next chunk to be asked for, and where it lies
-    const int64_t c_first = REV ? nch - 1 : 0, step = REV ? -1 : 1;
-    const char *pk = reinterpret_cast<const char *>(A.k) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
-    const char *pq = reinterpret_cast<const char *>(A.q) + ((sq.t0 + c_first * C) * A.c.Hk + h / group) * (K * EB);
-    const char *pv = reinterpret_cast<const char *>(A.v) + (((sq.t0 + c_first * C) * A.c.H + h) * V + vt * VT) * EB;
-    const char *prec = A.c.rec + ((sq.first + c_first) * A.c.H + h) * RECB;
-    char *po = reinterpret_cast<char *>(A.o) + ((sq.t0 + c_first * C) * A.c.H + h) * V * EB;
-    const int64_t step_k = step * C * lk, step_v = step * C * lv, step_r = step * A.c.H * RECB;
+    const uint32_t lv = (uint32_t)A.c.H * (uint32_t)(V * EB);
+    const int64_t step_v = (REV ? -1 : 1) * (int64_t)C * lv;
+    char *po = reinterpret_cast<char *>(A.o) + ((sq.t0 + (REV ? nch - 1 : 0) * (int64_t)C) * A.c.H + h) * V * EB;
     auto tokens_of = [&](int c) __attribute__((always_inline)) { return len - c * C < C ? len - c * C : C; };
-    auto take = [&](int c) __attribute__((always_inline)) {
-        const int m = tokens_of(c);
-        rk.take(pk, m);
-        if constexpr (MODE != kErrors) rq.take(pq, m);
-        rv.take(pv, m);
-        rr.take(prec);
-        pk += step_k;
-        if constexpr (MODE != kErrors) pq += step_k;
-        pv += step_v;
-        prec += step_r;
-    };
-    auto put = [&](int b) __attribute__((always_inline)) {
-        rk.put(smem + L::k + b * L::K_);
-        if constexpr (MODE != kErrors) rq.put(smem + L::q + b * L::K_);
-        rv.put(smem + L::v + b * L::V_);
-        rr.put(smem + L::rec + b * L::R_);
-    };
-    auto chunk_of = [&](int i) __attribute__((always_inline)) { return REV ? nch - 1 - i : i; };
-    if (nch > 0) {
-        take(chunk_of(0));
-        if constexpr (NB == 2) {
-            put(0);
-            if (nch > 1) take(chunk_of(1));
-        }
-    }
     const int row0 = RK::row_at(lane), tile0 = RK::tile_at(lane), col0 = RV::col_at(lane, wave);
     Pair<BF> sf[KC][1];  // the state as an operand
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
     for (int cc = 0; cc < nch; ++cc) {
-        const int c = chunk_of(cc), b = cc & (NB - 1);
+        const int c = REV ? nch - 1 - cc : cc, b = cc & (NB - 1);
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
-        if constexpr (NB == 1) {
-            put(0);
-            if (cc + 1 < nch) take(chunk_of(cc + 1));
-            __syncthreads();
-        } else if (cc + 1 < nch) {
-            put(b ^ 1);
-            if (cc + 2 < nch) take(chunk_of(cc + 2));
-        }
+        if constexpr (NB == 1) __syncthreads();
         const char *sk = smem + L::k + b * L::K_, *sv = smem + L::v + b * L::V_, *sr = smem + L::rec + b * L::R_;
         const char *sq_ = smem + L::q + b * L::K_;
         (void)sq_;

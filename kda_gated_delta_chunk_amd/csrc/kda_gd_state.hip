@@ -8,7 +8,7 @@ template <bool BF, int K, int VT, int MODE>
 hipError_t launch(const StateArgs &a, int V, hipStream_t st) {
     const int64_t items = (int64_t)a.c.N * a.c.H;
     hipLaunchKernelGGL((kda_gd_state_kernel<BF, K, VT, MODE>), hd::wide_grid((items + 7) / 8 * 8 * a.tiles),
-                       dim3(VT * 4), 0, st, a, V);
+                       dim3(VT * 8), 0, st, a, V);
     return hipGetLastError();
 }
 template <bool BF, int K, int VT>
