@@ -120,8 +120,11 @@ __device__ __forceinline__ int token_of(int tt, int g) { return 16 * tt + 4 * g;
 __device__ __forceinline__ int slot_token(int g, int j) { return token_of(j >> 2, g) + (j & 3); }
 
 // ------------------------------------------------------------------ rows in LDS
-// NCOL elements a row. bf16: the 16-byte slots of a row are permuted by an exclusive or with its index, so that 16 rows
-// at one slot (the lanes of a row read) and 8 rows at two adjacent ones (of a transposing read) fall on different banks.
+// NCOL elements a row. bf16: the 16-byte slots of a row are permuted by an exclusive or with bits of its index. The LDS
+// serves a 16-byte read in four steps of sixteen lanes, and the steps that matter take lanes 0-3, 12-15 and 20-27 and
+// lanes 4-11, 16-19 and 28-31: eight rows at one slot and the other eight at the slot beside it, which the row's bits 2 and
+// 3 keep on different banks (counting the lanes in order instead had every read of rows take 8 cycles, not 4). An 8-byte
+// transposing read takes 32 lanes a step: 8 rows at two adjacent slots.
 // fp32: rows padded by 16 bytes to the same end. Channels: slots 0-7 of a 32-deep product are channels 32c + 8g + j (bf16,
 // one 16-byte read) or 4g + i and 16 + 4g + i (fp32), and a state's tile kt has its rows in the same order.
 template <bool BF, int NCOL> struct Rw;
@@ -129,8 +132,8 @@ template <int NCOL> struct Rw<true, NCOL> {
     static constexpr int NS = NCOL / 8, RB = NCOL * 2;
     static constexpr int bytes(int rows) { return rows * RB; }
     static __device__ __forceinline__ int swz(int row) {
-        const int line = NCOL == 128 ? row & 7 : NCOL == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
-        return (line << 1) | ((row >> 3) & 1);
+        const int high = NCOL == 128 ? (row & 3) << 2 : NCOL == 64 ? (row & 2) << 1 : 0;
+        return high | (((row >> 1) ^ row) & 4) >> 1 | ((row >> 3) & 1);
     }
     static __device__ __forceinline__ int slot(int row, int s) { return row * RB + ((s ^ swz(row)) << 4); }
     static __device__ __forceinline__ int state_row(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
