@@ -18,10 +18,12 @@ namespace gd {
 
 // A tile of V channels x 32 tokens in LDS, from rows of the states' passes: 16 bytes of a row are the tokens of a lane
 // group's slots. bf16: the two halves (tiles of 16 tokens) in planes of their own, rows of 32 bytes ordered so that the
-// eight rows of a transposing read, and the sixteen of a row read, fall on different banks.
+// eight rows of a transposing read, and the sixteen of a row read, fall on different banks. (The planes are not a multiple
+// of 512 bytes apart: the compiler would join a lane's reads of both into one instruction, whose halves then meet on the
+// same banks, 8 cycles for 4.)
 template <bool BF, int V, int NP> struct Tile;
 template <int V, int NP> struct Tile<true, V, NP> {
-    static constexpr int PLANE = V * 32, PART = 2 * PLANE;
+    static constexpr int PLANE = V * 32 + 64, PART = 2 * PLANE;
     static __device__ __forceinline__ int at(int row, int g) {
         const int line = (row & 3) | (row & 24) >> 1 | (row & 4) << 2 | (row & ~31);
         return line * 32 + ((g ^ ((row >> 3) & 2)) << 3);
@@ -106,14 +108,32 @@ __device__ __forceinline__ void fence_each(f32x4 (&x)[1]) { mfma_fence(x[0]); }
 __device__ __forceinline__ void fence_each(f32x4 (&x)[2]) { mfma_fence(x[0], x[1]); }
 __device__ __forceinline__ void fence_each(f32x4 (&x)[4]) { mfma_fence(x[0], x[1], x[2], x[3]); }
 
+// The sum over a wavefront's four groups of 16 lanes, in all of them. A swap exchanges the odd groups (or the upper pair) of
+// its first operand with the even ones (the lower pair) of its second.
+__device__ __forceinline__ float sum_groups(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a0 = a[0], a1 = a[1];
+    const uint32_t s = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1));
+    const auto b = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+    const uint32_t b0 = b[0], b1 = b[1];
+    return __builtin_bit_cast(float, b0) + __builtin_bit_cast(float, b1);
+}
+
 template <bool BF, int K, int V, int NP>
 struct GradLds {
     static constexpr int C = kChunkTokens, NM = BF ? 2 : 1, NW = K / 16;
     static constexpr int T_ = (BF ? NP : 1) * Tile<BF, V, NP>::PART, M_ = Rw<BF, C>::bytes(C);  // a tile; a part of a matrix
     static constexpr int K_ = Rw<BF, K>::bytes(C), O_ = Rw<BF, V>::bytes(C);
-    static constexpr int dout = 0, z = dout + O_, dw = z + T_, k = dw + T_, q = k + K_, m1 = q + K_,
-                         m2 = m1 + NM * M_, wt = m2 + NM * M_, u = wt + kWeights * C * 4, pairs = u + NW * C * 4,
-                         db = pairs + 2 * NW * C * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
+    // A chunk's rows, twice where there is room for one workgroup that fills the compute unit: the next chunk's come while
+    // this one's are read. (Of smaller workgroups several run side by side instead.)
+    static constexpr int dout = 0, z = dout + O_, dw = z + T_, k = dw + T_, q = k + K_, wt = q + K_,
+                         ROWS = wt + kWeights * C * 4;
+    static constexpr int REST = 2 * NM * M_ + kSegmentChunks * (NW * C + 12 * 16 + C) * 4 + NW * 4;
+    static constexpr int NB = NW == 8 && 2 * ROWS + REST <= 160 * 1024 ? 2 : 1;
+    static constexpr int m1 = NB * ROWS, m2 = m1 + NM * M_, u = m2 + NM * M_, pairs = u + kSegmentChunks * NW * C * 4,
+                         db = pairs + kSegmentChunks * 12 * 16 * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
+    static_assert(bytes == NB * ROWS + REST && bytes <= 160 * 1024, "a compute unit's memory");
 };
 
 // One segment of a (sequence, head); a wavefront 16 columns of K, all V rows of the transposed states in its registers.
@@ -130,12 +150,24 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     constexpr bool GF = !BF || NP == 3;
     using Op = Multi<BF, NP>;
     __shared__ __align__(16) char smem[L::bytes];
-    char *const s_do = smem + L::dout, *const s_z = smem + L::z, *const s_dw = smem + L::dw, *const s_k = smem + L::k,
-         *const s_q = smem + L::q, *const s_m1 = smem + L::m1, *const s_m2 = smem + L::m2;
-    float *const s_wt = reinterpret_cast<float *>(smem + L::wt), *const s_red = reinterpret_cast<float *>(smem + L::red);
-    float(*const s_u)[C] = reinterpret_cast<float(*)[C]>(smem + L::u);
-    float(*const s_pairs)[C] = reinterpret_cast<float(*)[C]>(smem + L::pairs);
+    char *const s_m1 = smem + L::m1, *const s_m2 = smem + L::m2;
+    float *const s_red = reinterpret_cast<float *>(smem + L::red);
+    // the log-decays' gradient by chunk: tokens' dots by wavefront, pairs' sums by job (of rows, of sources), all of them
+    float(*const s_u)[NW][C] = reinterpret_cast<float(*)[NW][C]>(smem + L::u);
+    float(*const s_pairs)[12][16] = reinterpret_cast<float(*)[12][16]>(smem + L::pairs);
     float *const s_db = reinterpret_cast<float *>(smem + L::db);
+    // the rows in use
+    char *s_do, *s_z, *s_dw, *s_k, *s_q;
+    float *s_wt;
+    auto rows_of = [&](int i) __attribute__((always_inline)) {
+        char *const p = smem + (i & (L::NB - 1)) * L::ROWS;
+        s_do = p + L::dout;
+        s_z = p + L::z;
+        s_dw = p + L::dw;
+        s_k = p + L::k;
+        s_q = p + L::q;
+        s_wt = reinterpret_cast<float *>(p + L::wt);
+    };
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
               li = lane & 15;
@@ -157,10 +189,6 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         for (int vt = 0; vt < VT; ++vt)
             st[vt] = s ? *reinterpret_cast<const f32x4 *>(s + (int64_t)(col + li) * V + RV::state_row(vt, g)) : zero4();
     };
-    f32x4 st[VT];
-    get_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
-    hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
-
     const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (V * EB);
     const char *pk = reinterpret_cast<const char *>(A.k) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
     const char *pq = reinterpret_cast<const char *>(A.q) + (sq.t0 * A.c.Hk + h / group) * (K * EB);
@@ -175,7 +203,8 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     rz.init(tid);
     rw.init(tid);
     u32x4 rwt;
-    auto take = [&](int c) __attribute__((always_inline)) {
+    auto take = [&](int i) __attribute__((always_inline)) {
+        const int c = c0 + i;
         const int64_t t = (int64_t)c * C, at = (sq.first + c) * A.c.H + h;
         const int m = len - (int)t < C ? len - (int)t : C;
         rk.take(pk + t * lk, m);
@@ -185,14 +214,20 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         rw.take(A.dw + at * tile);
         rwt = *reinterpret_cast<const u32x4 *>(A.c.rec + at * rec_bytes(true) + rec_weights(true) + (tid & 63) * 16);
     };
-    auto put = [&]() __attribute__((always_inline)) {
-        rk.put(s_k);
-        rq.put(s_q);
-        rd.put(s_do);
-        rz.put(s_z);
-        rw.put(s_dw);
-        if (wave == 0) *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(s_wt) + tid * 16) = rwt;
+    auto put = [&](int i) __attribute__((always_inline)) {
+        char *const p = smem + (i & (L::NB - 1)) * L::ROWS;
+        rk.put(p + L::k);
+        rq.put(p + L::q);
+        rd.put(p + L::dout);
+        rz.put(p + L::z);
+        rw.put(p + L::dw);
+        if (wave == 0) *reinterpret_cast<u32x4 *>(p + L::wt + tid * 16) = rwt;
     };
+    take(0);
+    f32x4 st[VT];
+    get_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
+    hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
+
     const int rowv0 = RV::row_at(lane), rowk0 = RK::row_at(lane), rowc0 = RC::row_at(lane), tilev0 = RV::tile_at(lane);
     const int tcols0 = TV::cols_at(lane), trows0 = TV::rows_at(lane);
     const int colk0 = RK::col_at(lane, wave);
@@ -246,16 +281,13 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     // a token's dot of rows x with a result y (columns 4g + i of token 16 tt + l % 16) over this wavefront's columns
     auto dot = [&](const char *x, int tt, const f32x4 &y) __attribute__((always_inline)) {
         float r[4];
-        RK::load_quad(x, 16 * tt + li, col + 4 * g, r);
+        int row = 16 * tt + li;
+        asm("" : "+v"(row));  // one read for both tiles would meet itself on the same banks
+        RK::load_quad(x, row, col + 4 * g, r);
         float d = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) d = fmaf(r[i], y[i], d);
         return d;
-    };
-    auto put_dot = [&](int tt, float d) __attribute__((always_inline)) {
-        d += __shfl_xor(d, 16);
-        d += __shfl_xor(d, 32);
-        if (g == 0) s_u[wave][16 * tt + li] = d;
     };
     auto at_of = [&](int64_t t) __attribute__((always_inline)) { return (t * A.c.H + h) * K + col + 4 * g; };
     auto store = [&](void *p, int64_t at, const f32x4 &y) __attribute__((always_inline)) {
@@ -288,16 +320,25 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     };
 
     // ================================================================ forward in time
-    take(c0);
     clear_mats();
-    for (int c = c0; c < c1; ++c) {
-        const int64_t tc = sq.t0 + (int64_t)c * C;
+    if constexpr (L::NB == 2) {
+        put(0);
+        if (nch > 1) take(1);
+    }
+    f32x4 gt[VT];
+    for (int i = 0; i < nch; ++i) {
+        const int64_t tc = sq.t0 + (int64_t)(c0 + i) * C;
         const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
-        __syncthreads();  // the last chunk's rows and matrices are read
-        put();
-        take(c + 1 < c1 ? c + 1 : c);  // the walk back begins with the last one
-        if (lane < C) s_pairs[2 * wave][lane] = s_pairs[2 * wave + 1][lane] = 0.f;
-        __syncthreads();
+        rows_of(i);
+        __syncthreads();  // the last chunk's rows and matrices are read (NB = 2: and this one's rows are there)
+        if constexpr (L::NB == 1) {
+            put(i);
+            if (i + 1 < nch) take(i + 1);
+            else if (nch > 1) take(nch - 2);  // the walk back begins with the chunk that is here
+            __syncthreads();
+        }
+        if (i == nch - 1)  // behind the segment, for the walk back
+            get_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
         // ---- the pairs' weights: lane holds sources i = 16 ts + 4g .. of token r = 16 tt + l % 16
         for (int p = wave; p < 6; p += NW) {
             const int which = p >= 3, x = which ? p - 3 : p, tt = x > 0, ts = x > 1;
@@ -345,17 +386,23 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             put_mat(which ? s_m2 : s_m1, r, ts, acc);
             // pairs of the log-decays' gradient: + at the row, - at the source
             float sum = 0.f;
+            f32x4 by_source;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float X = i0 + i < r ? acc[i] * prod[i] : 0.f;
+            for (int n = 0; n < 4; ++n) {
+                const float X = i0 + n < r ? acc[n] * prod[n] : 0.f;
                 sum += X;
-                const float all16 = row_scan16(X);  // the source's sum, in its last lane
-                if (li == 15) s_pairs[2 * wave][i0 + i] -= all16;
+                by_source[n] = row_scan16(X);  // the source's sum, in its last lane
             }
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (g == 0) s_pairs[2 * wave + 1][r] += sum;
-            __builtin_amdgcn_wave_barrier();
+            if (li == 15) *reinterpret_cast<f32x4 *>(&s_pairs[i][2 * p + 1][4 * g]) = by_source;
+            sum = sum_groups(sum);
+            if (g == 0) s_pairs[i][2 * p][li] = sum;
+        }
+        if constexpr (L::NB == 2) {
+            if (i + 1 < nch) {
+                put(i + 1);
+                if (i + 2 < nch) take(i + 2);
+                else if (nch > 2) take(nch - 3);  // the walk back finds the last two chunks here
+            }
         }
         // ---- what the state gives
         f32x4 y1[2] = {zero4(), zero4()}, y2[2] = {zero4(), zero4()};
@@ -373,20 +420,15 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             mmx(y2, s, w);
         }
         mfma_fence(y1[0], y1[1], y2[0], y2[1]);
+        float dots[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
             const int t = 16 * tt + li;
             y1[tt] *= s_wt[kEnterScaled * C + t];
             y2[tt] *= -s_wt[kEnter * C + t] * s_wt[kBeta * C + t];
-            put_dot(tt, dot(s_q, tt, y1[tt]) + dot(s_k, tt, y2[tt]));
+            dots[tt] = dot(s_q, tt, y1[tt]) + dot(s_k, tt, y2[tt]);
         }
         __syncthreads();
-        if (tid < C) {
-            float d = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) d += s_u[w][tid] + (s_pairs[2 * w][tid] + s_pairs[2 * w + 1][tid]);
-            s_db[(c - c0) * C + tid] = tid < m ? d : 0.f;
-        }
         Pair<BF> mat1[2], mat2[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
@@ -404,6 +446,11 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         for (int i = 0; i < 8; ++i) w[i] *= kx[i];
         Op kp;
         set_multi(kp, w);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const float d = sum_groups(dots[tt]);
+            if (g == 0) s_u[i][wave][16 * tt + li] = d;
+        }
         const float total = s_wt[kTotal * C];
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
@@ -422,8 +469,6 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
     }
     // ---- what the border behind the segment passes on
-    f32x4 gt[VT];
-    get_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
     float border = 0.f;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
@@ -437,17 +482,20 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     // ================================================================ backward in time
     __syncthreads();
     clear_mats();
-    for (int c = c1 - 1; c >= c0; --c) {
-        const int64_t tc = sq.t0 + (int64_t)c * C;
+    for (int i = nch - 1; i >= 0; --i) {
+        const int64_t tc = sq.t0 + (int64_t)(c0 + i) * C;
         const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
+        rows_of(i);
         __syncthreads();
-        put();
-        if (c > c0) take(c - 1);
+        if (L::NB == 1 && i < nch - 1) {
+            put(i);
+            if (i > 0) take(i - 1);
+            __syncthreads();
+        }
         f32x4 read[2];  // what the walk forward left for dk
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
             if (16 * tt + li < m) read[tt] = *reinterpret_cast<const f32x4 *>(A.dk_part + at_of(tc + 16 * tt + li));
-        __syncthreads();
         // ---- the pairs' weights the other way round: lane holds tokens j = 16 ts + 4g .. that see token r = 16 tt + l % 16
         for (int p = wave; p < 6; p += NW) {
             const int which = p >= 3, x = which ? p - 3 : p, ts = x > 0, tt = x > 1;
@@ -480,6 +528,11 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
                 acc[i] = (which ? j0 + i > r : j0 + i >= r) && j0 + i < m ? f * acc[i] * e[i] * (which ? -be[i] : A.scale) : 0.f;
             put_mat(which ? s_m2 : s_m1, r, ts, acc);
         }
+        if constexpr (L::NB == 2)
+            if (i > 0 && i < nch - 1) {
+                put(i - 1);
+                if (i > 1) take(i - 2);
+            }
         f32x4 y[2] = {zero4(), zero4()};
 #pragma unroll
         for (int vc = 0; vc < VC; ++vc) {
@@ -490,18 +543,13 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             mmx(y, s, z);
         }
         mfma_fence(y[0], y[1]);
+        float dots[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
             y[tt] *= s_wt[kLeaveBeta * C + 16 * tt + li];
-            put_dot(tt, dot(s_k, tt, y[tt]));
+            dots[tt] = dot(s_k, tt, y[tt]);
         }
         __syncthreads();
-        if (tid < m) {
-            float d = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) d += s_u[w][tid];
-            s_db[(c - c0) * C + tid] -= d;
-        }
         Pair<BF> mat1[2], mat2[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
@@ -529,6 +577,11 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             set_multi(qp, w);
             set_multi(kp, e);
         }
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const float d = sum_groups(dots[tt]);
+            if (g == 0) s_u[i][wave][16 * tt + li] -= d;
+        }
         const float total = s_wt[kTotal * C];
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
@@ -542,6 +595,20 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         for (int tt = 0; tt < 2; ++tt)
             if (16 * tt + li < m) store(A.dk, at_of(tc + 16 * tt + li), y[tt] + read[tt]);
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(gt));
+    }
+    __syncthreads();
+    for (int t = tid; t < nch * C; t += NT) {
+        const int i = t / C, r = t % C;
+        float d = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) d += s_u[i][w][r];
+        // jobs 3x + (0, 1, 2): rows of tiles 0, 1, 1, sources of tiles 0, 0, 1
+#pragma unroll
+        for (int x = 0; x < 6; x += 3) {
+            const float *s = &s_pairs[i][2 * x][r & 15];
+            d += r < 16 ? s[0] - (s[16] + s[48]) : s[32] + (s[64] - s[80]);
+        }
+        s_db[t] = sq.t0 + (int64_t)c0 * C + t < sq.t1 ? d : 0.f;
     }
     __syncthreads();
     // ---- dg: the sums from a token to the border, in fp64
