@@ -10,8 +10,8 @@ namespace {
 // One workgroup: clamps cu_seqlens into [0, T], makes it non-decreasing (a running maximum) and numbers the chunks and
 // segments, 1024 sequences at a time. T < 2^31.
 __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T,
-                                                            Seq *__restrict__ seqs) {
-    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16];
+                                                            Seq *__restrict__ seqs, int32_t *__restrict__ order) {
+    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16], s_all[1024];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     auto entry = [&](int64_t i) -> uint32_t {
         const int32_t x = cu[i];
@@ -46,7 +46,15 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
             if (lane >= d) uc += x, us += y;
         }
         if (lane == 63) s_chunks[wave] = uc, s_segs[wave] = us;
+        s_all[t] = chunks;
         __syncthreads();
+        // the longest first, of equal ones the first: one that starts late would run on alone
+        if (n < N) {
+            const int all = N - base < 1024 ? (int)(N - base) : 1024;
+            int before_it = 0;
+            for (int j = 0; j < all; ++j) before_it += s_all[j] > chunks || (s_all[j] == chunks && j < t);
+            order[base + before_it] = (int32_t)n;
+        }
         uint32_t ac = 0, as = 0;
         for (int w = 0; w < 16; ++w) {
             if (w < wave) uc += s_chunks[w], us += s_segs[w];
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(256) void kda_gd_group_kernel(const Common cm, cons
 
 // ------------------------------------------------------------------ workspace
 struct Layout {
-    size_t seqs, rec, z, dw, seed_s, seed_g, dk_part, dq, dk, total;
+    size_t seqs, order, rec, z, dw, seed_s, seed_g, dk_part, dq, dk, total;
 };
 struct Sizes {
     int64_t slots, segs;
@@ -324,7 +332,10 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
         return here;
     };
     const size_t ch = (size_t)s.slots * H;
-    if (packed) l.seqs = take((size_t)N * sizeof(Seq));
+    if (packed) {
+        l.seqs = take((size_t)N * sizeof(Seq));
+        l.order = take((size_t)N * 4);
+    }
     l.rec = take(ch * rec_bytes(bwd));
     if (bwd) {
         l.z = take(ch * V * kChunkTokens * tile_bytes);
@@ -364,6 +375,7 @@ Call prepare(const GdArgs &a, bool bwd) {
     x.l = layout(s, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd, tile_bytes(a.io_bf16, a.gates_fp32));
     x.ws = reinterpret_cast<char *>(a.workspace);
     x.c.seqs = packed ? reinterpret_cast<const Seq *>(x.ws + x.l.seqs) : nullptr;
+    x.c.order = packed ? reinterpret_cast<const int32_t *>(x.ws + x.l.order) : nullptr;
     x.c.T = a.T;
     x.c.ntok = a.B * a.T;
     x.c.slots = s.slots;
@@ -396,7 +408,7 @@ hipError_t prep_k(const GdArgs &a, const Common &c, bool bwd, hipStream_t st) {
 hipError_t make_records(const GdArgs &a, const Call &x, bool bwd, hipStream_t st) {
     if (x.c.seqs) {
         hipLaunchKernelGGL(kda_gd_table_kernel, dim3(1), dim3(1024), 0, st, a.cu_seqlens, a.num_seqs, (uint32_t)a.T,
-                           const_cast<Seq *>(x.c.seqs));
+                           const_cast<Seq *>(x.c.seqs), const_cast<int32_t *>(x.c.order));
         KDA_TRY(hipGetLastError());
     }
     if (a.T == 0) return hipSuccess;
@@ -430,7 +442,7 @@ hipError_t launch_gd_fwd(const GdArgs &a, hipStream_t st) {
     s.s_end = a.S_final;
     s.o = a.o;
     s.tiles = a.V / state_tile(a.V);
-    return state_pass(a.io_bf16, kForward, s, a.K, a.V, st);
+    return forward_pass(a.io_bf16, s, a.K, a.V, st);
 }
 
 hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
@@ -444,13 +456,12 @@ hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
     s.k = a.k;
     s.tiles = a.V / state_tile(a.V);
     s.parts = tile_parts(a.io_bf16, a.gates_fp32);
-    if (a.T > 0) {  // forward in time: the errors z, and the states at the segments' starts
-        s.v = a.v;
-        s.s_init = a.S0;
-        s.rows = at(x.l.z);
-        s.seed = reinterpret_cast<float *>(at(x.l.seed_s));
-        KDA_TRY(state_pass(a.io_bf16, kErrors, s, a.K, a.V, st));
-    }
+    // forward in time: the errors z, and the states at the segments' starts
+    StateArgs e = s;
+    e.v = a.v;
+    e.s_init = a.S0;
+    e.rows = at(x.l.z);
+    e.seed = reinterpret_cast<float *>(at(x.l.seed_s));
     // backward in time: dv, the writes' gradients, and the state's at the segments' ends
     s.v = a.dout;
     s.s_init = a.dS_final;
@@ -458,7 +469,7 @@ hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
     s.o = a.dv;
     s.rows = at(x.l.dw);
     s.seed = reinterpret_cast<float *>(at(x.l.seed_g));
-    KDA_TRY(state_pass(a.io_bf16, kReverse, s, a.K, a.V, st));
+    KDA_TRY(backward_passes(a.io_bf16, s, e, a.K, a.V, st));
     if (a.T == 0) return hipSuccess;
     const bool grouped = a.H != a.Hk;
     GradArgs g{};

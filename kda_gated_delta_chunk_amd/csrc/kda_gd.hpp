@@ -64,6 +64,7 @@ constexpr int rec_weights(bool bwd) { return (bwd ? 3 : 2) * kMatBytes; }
 
 struct Common {
     const Seq *seqs;   // or null: rows of T tokens
+    const int32_t *order;  // the sequences, the longest first (of each 1024), or null
     int64_t T, ntok, slots, segs;  // slots, segs: chunks and segments of all sequences (upper bounds when packed)
     int32_t nch, nseg;  // per row (not packed)
     int32_t N, H, Hk;
@@ -96,7 +97,8 @@ struct GradArgs {
 constexpr int state_tile(int V) { return V < 64 ? V : 64; }
 
 enum Mode { kForward, kErrors, kReverse };  // outputs; the errors and states for the gradients; the state's gradients
-hipError_t state_pass(bool bf16, Mode mode, const StateArgs &a, int K, int V, hipStream_t st);
+hipError_t forward_pass(bool bf16, const StateArgs &a, int K, int V, hipStream_t st);
+hipError_t backward_passes(bool bf16, const StateArgs &reverse, const StateArgs &errors, int K, int V, hipStream_t st);
 hipError_t grad_pass_bf16(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
 hipError_t grad_pass_bf16_gates_fp32(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
 hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st);

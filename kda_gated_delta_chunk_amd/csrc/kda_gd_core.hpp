@@ -364,36 +364,35 @@ struct StateLds {
 // One (sequence, head), columns vt * VT .. of the state, a wavefront 16 of them: all K rows as fp32 accumulators, which
 // are at once operands of the products with the state, so it never leaves the registers.
 template <bool BF, int K, int VT, int MODE>
-__global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs A, int V) {
+__device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t blk, char *smem) {
     using L = StateLds<BF, K, VT, MODE>;
     using RK = Rw<BF, K>;
     using RV = Rw<BF, VT>;
-    constexpr int NW = VT / 16, NT = NW * 64, KT = K / 16, KC = K / 32, C = kChunkTokens, NB = L::NB;
+    constexpr int NW = VT / 16, NT = NW * 64, NS = NT / 2, KT = K / 16, KC = K / 32, C = kChunkTokens, NB = L::NB;
     constexpr int EB = BF ? 2 : 4;
     constexpr bool REV = MODE == kReverse;
-    __shared__ __align__(16) char smem[L::bytes];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
               li = lane & 15;
-    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
     // the tiles of a head 8 workgroups apart: the same XCD, whose L2 then holds the rows they share
     const int64_t grp = blk / (8 * A.tiles);
     const int in = (int)(blk - grp * 8 * A.tiles), vt = in >> 3;
-    const int64_t item = grp * 8 + (in & 7), n = item / A.c.H;
-    const int h = (int)(item - n * A.c.H), group = A.c.H / A.c.Hk;
-    if (n >= A.c.N) return;
+    const int64_t item = grp * 8 + (in & 7), nth = item / A.c.H;
+    const int h = (int)(item - nth * A.c.H), group = A.c.H / A.c.Hk;
+    if (nth >= A.c.N) return;
+    const int64_t n = A.c.order ? A.c.order[nth] : nth;
     const Seq sq = seq_of(A.c, n);
     const int len = (int)(sq.t1 - sq.t0);  // under 2^31
     const int nch = (int)(((int64_t)len + C - 1) / C);
     const int col = vt * VT + wave * 16;  // this wavefront's first column
 
-    // ---- the second half of the wavefronts: rows on their way to LDS
+    // ---- the last third of the wavefronts: rows on their way to LDS
     if (wave >= NW) {
         const uint32_t lk = (uint32_t)A.c.Hk * (K * EB), lv = (uint32_t)A.c.H * (uint32_t)(V * EB);
         constexpr int RECB = L::R_;
-        RowsIn<BF, K, C, NT> rk, rq;
-        RowsIn<BF, VT, C, NT> rv;
-        BytesIn<RECB, NT> rr;
+        RowsIn<BF, K, C, NS> rk, rq;
+        RowsIn<BF, VT, C, NS> rv;
+        BytesIn<RECB, NS> rr;
         rk.init(tid - NT, lk);
         rq.init(tid - NT, lk);
         rv.init(tid - NT, lv);
@@ -502,6 +501,10 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
             for (int tt = 0; tt < 2; ++tt) kf[kc][tt].p[0] = RK::row_frag(sk + 16 * tt * RK::RB, row0, kc);
         const Frag8<BF> vf = RV::col_frag(sv, col0);
         weights(REV ? kLeave : kEnter, w);
+        KDA_ORDER;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) mmx(x, kf[kc], sf[kc]);
+        KDA_ORDER;
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) mat[tt] = load_mat<BF>(sr + (REV ? kMatPT : kMatN) * kMatBytes, tt, lane);
         if constexpr (MODE == kForward)
@@ -509,13 +512,6 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
             for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) qf[kc][tt].p[0] = RK::row_frag(sq_ + 16 * tt * RK::RB, row0, kc);
-        KDA_ORDER;
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc) mmx(x, kf[kc], sf[kc]);
-        KDA_ORDER;
-        if constexpr (MODE == kForward)
-#pragma unroll
-            for (int kc = 0; kc < KC; ++kc) mmx(y, sf[kc], qf[kc]);
         KDA_ORDER;
         widen(vf, vx);
         mfma_fence(x[0], x[1]);
@@ -545,6 +541,9 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
             set_multi(rp[0], r);
             mmx(x, mat, rp);
         }
+        if constexpr (MODE == kForward)
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc) mmx(y, sf[kc], qf[kc]);
         KDA_ORDER;
         // the update's operands, while those products run
         Frag8<BF> kt_f[KT];
@@ -619,21 +618,18 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
 #pragma unroll
                     for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], f.p[p]);
         } else {
-            float wq[8], wk[8], be[8];
+            float wq[8], be[8];
             weights(kEnterScaled, wq);
-            weights(kEnter, wk);
             weights(kBeta, be);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 z[i] *= be[i];  // dL/dz, which is dL/dv
                 wq[i] *= vx[i];
-                wk[i] *= -z[i];
             }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) st[kt] *= total;
-            Multi<BF, 3> f, e;
+            Multi<BF, 3> f;
             set_multi(f, wq);
-            set_multi(e, wk);
             constexpr int KG = KT < 4 ? KT : 4;
 #pragma unroll
             for (int k0 = 0; k0 < KT; k0 += KG) {
@@ -644,11 +640,18 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
                 for (int p = 0; p < (BF ? 3 : 1); ++p)
 #pragma unroll
                     for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], a[j], f.p[p]);
+            }
+            KDA_ORDER;
+            weights(kEnter, wq);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wq[i] *= -z[i];
+            set_multi(f, wq);
+#pragma unroll
+            for (int k0 = 0; k0 < KT; k0 += KG)
 #pragma unroll
                 for (int p = 0; p < (BF ? 3 : 1); ++p)
 #pragma unroll
-                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], e.p[p]);
-            }
+                    for (int j = 0; j < KG; ++j) st[k0 + j] = mma32(st[k0 + j], kt_f[k0 + j], f.p[p]);
             const auto out = __builtin_amdgcn_make_buffer_rsrc(po, 0, (tokens_of(c) - 1) * lv + V * EB, 0x00027000);
             po += step_v;
 #pragma unroll
@@ -677,6 +680,20 @@ __global__ __launch_bounds__(VT * 8, 2) void kda_gd_state_kernel(const StateArgs
         for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
     }
     if (A.s_end) put_state(A.s_end + nh * sstate);
+}
+
+template <bool BF, int K, int VT>
+__global__ __launch_bounds__(VT * 6, 3) void kda_gd_state_kernel(const StateArgs A, int V) {
+    __shared__ __align__(16) char smem[StateLds<BF, K, VT, kForward>::bytes];
+    state_pass<BF, K, VT, kForward>(A, V, blockIdx.x + (int64_t)blockIdx.y * gridDim.x, smem);
+}
+// The backward call's two passes wait for nothing of each other's: one launch, the longer one's workgroups first.
+template <bool BF, int K, int VT>
+__global__ __launch_bounds__(VT * 6, 3) void kda_gd_states_kernel(const StateArgs R, const StateArgs E, int V, int64_t blocks) {
+    __shared__ __align__(16) char smem[StateLds<BF, K, VT, kReverse>::bytes];
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    if (blk < blocks) state_pass<BF, K, VT, kReverse>(R, V, blk, smem);
+    else state_pass<BF, K, VT, kErrors>(E, V, blk - blocks, smem);
 }
 
 }  // namespace gd
