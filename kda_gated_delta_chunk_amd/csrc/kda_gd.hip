@@ -441,7 +441,6 @@ hipError_t launch_gd_fwd(const GdArgs &a, hipStream_t st) {
     s.s_init = a.S0;
     s.s_end = a.S_final;
     s.o = a.o;
-    s.tiles = a.V / state_tile(a.V);
     return forward_pass(a.io_bf16, s, a.K, a.V, st);
 }
 
@@ -454,7 +453,6 @@ hipError_t launch_gd_bwd(const GdArgs &a, hipStream_t st) {
     s.c = x.c;
     s.q = a.q;
     s.k = a.k;
-    s.tiles = a.V / state_tile(a.V);
     s.parts = tile_parts(a.io_bf16, a.gates_fp32);
     // forward in time: the errors z, and the states at the segments' starts
     StateArgs e = s;

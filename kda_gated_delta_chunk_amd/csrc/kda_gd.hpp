@@ -94,11 +94,9 @@ struct GradArgs {
     float scale;
 };
 
-constexpr int state_tile(int V) { return V < 64 ? V : 64; }
-
 enum Mode { kForward, kErrors, kReverse };  // outputs; the errors and states for the gradients; the state's gradients
 hipError_t forward_pass(bool bf16, const StateArgs &a, int K, int V, hipStream_t st);
-hipError_t backward_passes(bool bf16, const StateArgs &reverse, const StateArgs &errors, int K, int V, hipStream_t st);
+hipError_t backward_passes(bool bf16, const StateArgs &reverse, StateArgs errors, int K, int V, hipStream_t st);
 hipError_t grad_pass_bf16(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
 hipError_t grad_pass_bf16_gates_fp32(const GradArgs &a, int K, int V, bool y_fp32, hipStream_t st);
 hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st);

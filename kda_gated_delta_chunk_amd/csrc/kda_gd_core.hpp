@@ -683,13 +683,13 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
 }
 
 template <bool BF, int K, int VT>
-__global__ __launch_bounds__(VT * 6, 3) void kda_gd_state_kernel(const StateArgs A, int V) {
+__global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_state_kernel(const StateArgs A, int V) {
     __shared__ __align__(16) char smem[StateLds<BF, K, VT, kForward>::bytes];
     state_pass<BF, K, VT, kForward>(A, V, blockIdx.x + (int64_t)blockIdx.y * gridDim.x, smem);
 }
 // The backward call's two passes wait for nothing of each other's: one launch, the longer one's workgroups first.
 template <bool BF, int K, int VT>
-__global__ __launch_bounds__(VT * 6, 3) void kda_gd_states_kernel(const StateArgs R, const StateArgs E, int V, int64_t blocks) {
+__global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_states_kernel(const StateArgs R, const StateArgs E, int V, int64_t blocks) {
     __shared__ __align__(16) char smem[StateLds<BF, K, VT, kReverse>::bytes];
     const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
     if (blk < blocks) state_pass<BF, K, VT, kReverse>(R, V, blk, smem);

@@ -5,7 +5,9 @@ namespace kda {
 namespace gd {
 namespace {
 template <bool BF, int K, int VT>
-hipError_t launch(const StateArgs &a, const StateArgs *e, int V, hipStream_t st) {
+hipError_t launch(StateArgs a, StateArgs *e, int V, hipStream_t st) {
+    a.tiles = V / VT;
+    if (e) e->tiles = a.tiles;
     const int64_t blocks = ((int64_t)a.c.N * a.c.H + 7) / 8 * 8 * a.tiles;
     if (e)
         hipLaunchKernelGGL((kda_gd_states_kernel<BF, K, VT>), hd::wide_grid(2 * blocks), dim3(VT * 6), 0, st, a, *e, V, blocks);
@@ -13,12 +15,21 @@ hipError_t launch(const StateArgs &a, const StateArgs *e, int V, hipStream_t st)
         hipLaunchKernelGGL((kda_gd_state_kernel<BF, K, VT>), hd::wide_grid(blocks), dim3(VT * 6), 0, st, a, V);
     return hipGetLastError();
 }
+// Tiles of 64 columns occupy a compute unit each. Where there are more of them than compute units, the two of a head share
+// one: their products overlap, and they read the same rows (4096 tokens of 256 heads: 318 us for 401; of 64 heads 184 us
+// and 300). Packed sequences are balanced as they come, which takes several pieces for every compute unit (16 of 17011 tokens,
+// 32 heads: 251 us for 226).
 template <bool BF, int K>
-hipError_t by_tile(const StateArgs &a, const StateArgs *e, int V, hipStream_t st) {
-    return state_tile(V) == 32 ? launch<BF, K, 32>(a, e, V, st) : launch<BF, K, 64>(a, e, V, st);
+hipError_t by_tile(const StateArgs &a, StateArgs *e, int V, hipStream_t st) {
+    constexpr int64_t kUnits = 256;
+    const int64_t items = (int64_t)a.c.N * a.c.H * (e ? 2 : 1);
+    const bool many = a.c.seqs ? items >= 4 * kUnits : 2 * items > kUnits;
+    return V == 32              ? launch<BF, K, 32>(a, e, V, st)
+           : V == 64 || !many   ? launch<BF, K, 64>(a, e, V, st)
+                                : launch<BF, K, 128>(a, e, V, st);
 }
 template <bool BF>
-hipError_t by_k(const StateArgs &a, const StateArgs *e, int K, int V, hipStream_t st) {
+hipError_t by_k(const StateArgs &a, StateArgs *e, int K, int V, hipStream_t st) {
     return K == 32   ? by_tile<BF, 32>(a, e, V, st)
            : K == 64 ? by_tile<BF, 64>(a, e, V, st)
                      : by_tile<BF, 128>(a, e, V, st);
@@ -28,7 +39,7 @@ hipError_t by_k(const StateArgs &a, const StateArgs *e, int K, int V, hipStream_
 hipError_t forward_pass(bool bf16, const StateArgs &a, int K, int V, hipStream_t st) {
     return bf16 ? by_k<true>(a, nullptr, K, V, st) : by_k<false>(a, nullptr, K, V, st);
 }
-hipError_t backward_passes(bool bf16, const StateArgs &reverse, const StateArgs &errors, int K, int V, hipStream_t st) {
+hipError_t backward_passes(bool bf16, const StateArgs &reverse, StateArgs errors, int K, int V, hipStream_t st) {
     return bf16 ? by_k<true>(reverse, &errors, K, V, st) : by_k<false>(reverse, &errors, K, V, st);
 }
 }  // namespace gd
