@@ -9,7 +9,7 @@ namespace {
 // ------------------------------------------------------------------ packed sequences
 // One workgroup: clamps cu_seqlens into [0, T], makes it non-decreasing (a running maximum) and numbers the chunks and
 // segments, 1024 sequences at a time. T < 2^31.
-__global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T,
+__global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T, uint32_t seg_chunks,
                                                             Seq *__restrict__ seqs, int32_t *__restrict__ order) {
     __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16], s_all[1024];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
             if (x > top) top = x;
         }
         const uint32_t chunks = (end - before + (kChunkTokens - 1)) / kChunkTokens;
-        const uint32_t segs = (chunks + (kSegmentChunks - 1)) / kSegmentChunks;
+        const uint32_t segs = (chunks + (seg_chunks - 1)) / seg_chunks;
         uint32_t uc = chunks, us = segs;  // sums up to this sequence
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -311,15 +311,26 @@ struct Layout {
 };
 struct Sizes {
     int64_t slots, segs;
-    int32_t nch, nseg;
+    int32_t nch, nseg, seg;
 };
-Sizes sizes(int64_t B, int64_t T, int32_t N, bool packed) {
+// The segments' length by the heads alone, so that a sequence's gradients are the same bits in every batch: about two
+// workgroups of the gradients' kernel for every place on the card that a sequence of 4096 tokens finds. A segment's start and
+// end cost about as much as 1.2 of its chunks and its states' way through memory (4096 x 96 heads: 533 us of 16 chunks, 554 of
+// 8), a long one leaves compute units idle (1531 tokens x 12 heads of 64 channels: 282 us of 16 chunks, 146 of 8, 84 of 2).
+int32_t segment_chunks(int32_t H, int32_t K) {
+    int32_t seg = segment_most(K);
+    while (seg > 2 && (int64_t)seg * 512 > (int64_t)H * K) seg >>= 1;
+    return seg;
+}
+Sizes sizes(int64_t B, int64_t T, int32_t N, int32_t H, int32_t K, bool packed) {
     Sizes s;
-    const int64_t nch = (T + kChunkTokens - 1) / kChunkTokens, nseg = (nch + kSegmentChunks - 1) / kSegmentChunks;
+    const int64_t nch = (T + kChunkTokens - 1) / kChunkTokens;
+    s.seg = segment_chunks(H, K);
+    const int64_t nseg = (nch + s.seg - 1) / s.seg;
     s.nch = (int32_t)(nch ? nch : 1);
     s.nseg = (int32_t)(nseg ? nseg : 1);
     s.slots = packed ? T / kChunkTokens + N : B * nch;
-    s.segs = packed ? T / (kChunkTokens * kSegmentChunks) + N : B * nseg;
+    s.segs = packed ? T / (kChunkTokens * s.seg) + N : B * nseg;
     return s;
 }
 Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t N, bool packed, bool bwd,
@@ -371,7 +382,7 @@ struct Call {
 Call prepare(const GdArgs &a, bool bwd) {
     Call x{};
     const bool packed = a.cu_seqlens != nullptr;
-    const Sizes s = sizes(a.B, a.T, a.num_seqs, packed);
+    const Sizes s = sizes(a.B, a.T, a.num_seqs, a.H, a.K, packed);
     x.l = layout(s, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd, tile_bytes(a.io_bf16, a.gates_fp32));
     x.ws = reinterpret_cast<char *>(a.workspace);
     x.c.seqs = packed ? reinterpret_cast<const Seq *>(x.ws + x.l.seqs) : nullptr;
@@ -382,6 +393,7 @@ Call prepare(const GdArgs &a, bool bwd) {
     x.c.segs = s.segs;
     x.c.nch = s.nch;
     x.c.nseg = s.nseg;
+    x.c.seg = s.seg;
     x.c.N = a.num_seqs;
     x.c.H = a.H;
     x.c.Hk = a.Hk;
@@ -408,7 +420,7 @@ hipError_t prep_k(const GdArgs &a, const Common &c, bool bwd, hipStream_t st) {
 hipError_t make_records(const GdArgs &a, const Call &x, bool bwd, hipStream_t st) {
     if (x.c.seqs) {
         hipLaunchKernelGGL(kda_gd_table_kernel, dim3(1), dim3(1024), 0, st, a.cu_seqlens, a.num_seqs, (uint32_t)a.T,
-                           const_cast<Seq *>(x.c.seqs), const_cast<int32_t *>(x.c.order));
+                           (uint32_t)x.c.seg, const_cast<Seq *>(x.c.seqs), const_cast<int32_t *>(x.c.order));
         KDA_TRY(hipGetLastError());
     }
     if (a.T == 0) return hipSuccess;
@@ -421,11 +433,11 @@ hipError_t make_records(const GdArgs &a, const Call &x, bool bwd, hipStream_t st
 
 size_t gd_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool) {
-    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, false, 0).total;
+    return gd::layout(gd::sizes(B, T, num_seqs, H, K, packed), B * T, H, Hk, K, V, num_seqs, packed, false, 0).total;
 }
 size_t gd_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t num_seqs,
                               bool packed, bool io_bf16) {
-    return gd::layout(gd::sizes(B, T, num_seqs, packed), B * T, H, Hk, K, V, num_seqs, packed, true,
+    return gd::layout(gd::sizes(B, T, num_seqs, H, K, packed), B * T, H, Hk, K, V, num_seqs, packed, true,
                       gd::tile_bytes(io_bf16, true)).total;
 }
 

@@ -46,7 +46,8 @@ hipError_t launch_gd_decode(const GdDecodeArgs &a, hipStream_t st);
 namespace gd {
 
 constexpr int kChunkTokens = 32;
-constexpr int kSegmentChunks = 8;  // chunks of a workgroup of the gradients' kernel
+// Chunks of a workgroup of the gradients' kernel: a power of two from 2 up to this (Common::seg).
+constexpr int segment_most(int K) { return K == 128 ? 16 : 8; }
 
 // A sequence: its tokens in the flattened [B * T], the number of its first chunk and of its first segment among all.
 struct Seq {
@@ -67,6 +68,7 @@ struct Common {
     const int32_t *order;  // the sequences, the longest first (of each 1024), or null
     int64_t T, ntok, slots, segs;  // slots, segs: chunks and segments of all sequences (upper bounds when packed)
     int32_t nch, nseg;  // per row (not packed)
+    int32_t seg;        // chunks of a segment
     int32_t N, H, Hk;
     char *rec;          // [slots][H] records
 };

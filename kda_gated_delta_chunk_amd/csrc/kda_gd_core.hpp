@@ -485,10 +485,10 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
             *reinterpret_cast<f32x4 *>(w) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of(0, g));
             *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of(1, g));
         };
-        if (MODE == kErrors && c > 0 && c % kSegmentChunks == 0)
-            put_state(A.seed + ((sq.seg + c / kSegmentChunks) * A.c.H + h) * sstate);
-        if (MODE == kReverse && c + 1 < nch && (c + 1) % kSegmentChunks == 0)
-            put_state(A.seed + ((sq.seg + c / kSegmentChunks) * A.c.H + h) * sstate);
+        if (MODE == kErrors && c > 0 && (c & (A.c.seg - 1)) == 0)
+            put_state(A.seed + ((sq.seg + c / A.c.seg) * A.c.H + h) * sstate);
+        if (MODE == kReverse && c + 1 < nch && ((c + 1) & (A.c.seg - 1)) == 0)
+            put_state(A.seed + ((sq.seg + c / A.c.seg) * A.c.H + h) * sstate);
 
         // ---- products with the state: K S, and S^T q. The operands are asked for ahead of the products.
         f32x4 x[2] = {zero4(), zero4()}, y[2] = {zero4(), zero4()};

@@ -129,10 +129,11 @@ struct GradLds {
     // this one's are read. (Of smaller workgroups several run side by side instead.)
     static constexpr int dout = 0, z = dout + O_, dw = z + T_, k = dw + T_, q = k + K_, wt = q + K_,
                          ROWS = wt + kWeights * C * 4;
-    static constexpr int REST = 2 * NM * M_ + kSegmentChunks * (NW * C + 12 * 16 + C) * 4 + NW * 4;
+    static constexpr int MOST = segment_most(K);
+    static constexpr int REST = 2 * NM * M_ + MOST * (NW * C + 12 * 16 + C) * 4 + NW * 4;
     static constexpr int NB = NW == 8 && 2 * ROWS + REST <= 160 * 1024 ? 2 : 1;
-    static constexpr int m1 = NB * ROWS, m2 = m1 + NM * M_, u = m2 + NM * M_, pairs = u + kSegmentChunks * NW * C * 4,
-                         db = pairs + kSegmentChunks * 12 * 16 * 4, red = db + kSegmentChunks * C * 4, bytes = red + NW * 4;
+    static constexpr int m1 = NB * ROWS, m2 = m1 + NM * M_, u = m2 + NM * M_, pairs = u + MOST * NW * C * 4,
+                         db = pairs + MOST * 12 * 16 * 4, red = db + MOST * C * 4, bytes = red + NW * 4;
     static_assert(bytes == NB * ROWS + REST && bytes <= 160 * 1024, "a compute unit's memory");
 };
 
@@ -178,8 +179,8 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     const Seq sq = seq_of(A.c, n);
     const int len = (int)(sq.t1 - sq.t0);  // under 2^31
     const int all = (int)(((int64_t)len + C - 1) / C);  // the sequence's chunks
-    if (slot < sq.seg || (slot - sq.seg) * kSegmentChunks >= all) return;
-    const int c0 = (int)(slot - sq.seg) * kSegmentChunks, c1 = c0 + kSegmentChunks < all ? c0 + kSegmentChunks : all;
+    if (slot < sq.seg || (slot - sq.seg) * A.c.seg >= all) return;
+    const int c0 = (int)(slot - sq.seg) * A.c.seg, c1 = c0 + A.c.seg < all ? c0 + A.c.seg : all;
     const int nch = c1 - c0, col = wave * 16;  // this wavefront's first column
     const int64_t sstate = (int64_t)K * V, nh = n * A.c.H + h;
 
@@ -613,7 +614,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     __syncthreads();
     // ---- dg: the sums from a token to the border, in fp64
     if (wave == 0) {
-        constexpr int PER = kSegmentChunks * C / 64;
+        constexpr int PER = L::MOST * C / 64;
         double own[PER], sum = 0.0;
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i) {
