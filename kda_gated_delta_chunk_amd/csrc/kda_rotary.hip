@@ -159,15 +159,18 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
     Row r = {};
     int64_t t = (int64_t)blockIdx.x * tok_par + tsub;
     take(t, hsub, r);
+    int32_t at[AXES ? E : 1] = {};  // the token's positions, asked for while the one before it is turned
+    auto positions_of = [&](int64_t t) __attribute__((always_inline)) {
+        if (AXES && pairs && t < tokens)
+#pragma unroll
+            for (int i = 0; i < (AXES ? E : 1); ++i) at[i] = positions[line[i] + t];
+    };
+    positions_of(t);
     for (; t < tokens; t += step) {
         float cs[E], sn[E];
         if (pairs) {
             int64_t pos = 0;
-            int32_t at[AXES ? E : 1];
-            if constexpr (AXES) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) at[i] = positions[line[i] + t];
-            } else {
+            if constexpr (!AXES) {
                 pos = positions ? (int64_t)positions[t]
                     : tokens <= 0xffffffffll ? (int64_t)((uint32_t)t % (uint32_t)T) : t % T;
             }
@@ -180,6 +183,7 @@ __global__ __launch_bounds__(256) void kda_rotary_kernel(const void *qp, const v
                 if (undefined >> i & 1) sn[i] = cs[i] = __builtin_nanf("");
             }
         }
+        positions_of(t + step);
         for (int h = hsub; h < Hq + Hk; h += heads_par) {
             Row next = {};
             const bool more = h + heads_par < Hq + Hk;
@@ -201,6 +205,11 @@ hipError_t launch_i(const RotaryArgs &a, hipStream_t st) {
     int heads_par = 256 / units;  // D <= 512: at most 256 units
     if (heads_par > H) heads_par = H;
     if (heads_par < 1) heads_par = 1;
+    // With axes of their own a thread's angles cost as much as the rows that it turns by them: where 1024 workgroups are left,
+    // a thread turns several heads of a token (2 x 8191 tokens of 40 heads of 128 channels: 97 us with 32 heads side by side,
+    // 77 with 8, 72 with 4: 4.7 TB/s).
+    if (AXES)
+        while (heads_par > 4 && a.tokens * units * (heads_par / 2) >= 256 * 1024) heads_par /= 2;
     int tok_par = 256 / (units * heads_par);
     if (tok_par < 1) tok_par = 1;
     int64_t wgs = (a.tokens + tok_par - 1) / tok_par;
