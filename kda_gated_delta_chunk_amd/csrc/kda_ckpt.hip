@@ -30,6 +30,17 @@ struct Quantizer {
 };
 __device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// The largest over LPB lanes next to each other, in all of them: quads by their permutations, then the other quad and the
+// other eight by mirrors.
+template <int LPB>
+__device__ __forceinline__ uint32_t largest_of(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xb1, 0xf, 0xf, true));
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4e, 0xf, 0xf, true));
+    if constexpr (LPB >= 8) m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xf, 0xf, true));
+    if constexpr (LPB >= 16) m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xf, 0xf, true));
+    return m;
+}
+
 // LPB lanes a block, eight adjacent values each (C a multiple of 8) or the values lane, lane + LPB, ...; a workgroup
 // takes 256 / LPB blocks at a time.
 template <bool BF, bool VEC, int LPB>
@@ -61,8 +72,7 @@ __global__ __launch_bounds__(256) void kda_ckpt_save_kernel(const void *__restri
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) m = max(m, size_bits(x[i]));
-#pragma unroll
-        for (int d = 1; d < LPB; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        m = largest_of<LPB>(m);
         const float top = __uint_as_float(m);
         const bool bad = m >= 0x7f800000u;
         int8_t out[V];
@@ -91,7 +101,7 @@ __global__ __launch_bounds__(256) void kda_ckpt_restore_kernel(const int8_t *__r
     using E = typename IO<BF>::T;
     const int64_t stride = (int64_t)gridDim.x * 256;
     for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < runs; r += stride) {
-        const int64_t row = r / runs_per_row;
+        const int64_t row = runs_per_row == kCkptBlock / V ? r / (kCkptBlock / V) : r / runs_per_row;
         const int c = (int)(r - row * runs_per_row) * V;
         const float step = scales[row * nb + c / kCkptBlock];
         if constexpr (V == 8) {
@@ -133,17 +143,27 @@ hipError_t restore_v(const CkptArgs &a, int nb, hipStream_t st) {
     return hipGetLastError();
 }
 int blocks_of(int32_t C) { return (int)(((int64_t)C + kCkptBlock - 1) / kCkptBlock); }
+// Rows of whole blocks are as many rows of one block.
+CkptArgs by_blocks(CkptArgs a) {
+    if (a.C % kCkptBlock == 0) {
+        a.rows *= a.C / kCkptBlock;
+        a.C = kCkptBlock;
+    }
+    return a;
+}
 
 }  // namespace
 
-hipError_t launch_ckpt_save(const CkptArgs &a, hipStream_t st) {
-    if (a.rows == 0) return hipSuccess;
+hipError_t launch_ckpt_save(const CkptArgs &args, hipStream_t st) {
+    if (args.rows == 0) return hipSuccess;
+    const CkptArgs a = by_blocks(args);
     const int nb = blocks_of(a.C);
     if (a.io_bf16) return a.C % 8 == 0 ? save_c<true, true>(a, nb, st) : save_c<true, false>(a, nb, st);
     return a.C % 8 == 0 ? save_c<false, true>(a, nb, st) : save_c<false, false>(a, nb, st);
 }
-hipError_t launch_ckpt_restore(const CkptArgs &a, hipStream_t st) {
-    if (a.rows == 0) return hipSuccess;
+hipError_t launch_ckpt_restore(const CkptArgs &args, hipStream_t st) {
+    if (args.rows == 0) return hipSuccess;
+    const CkptArgs a = by_blocks(args);
     const int nb = blocks_of(a.C);
     if (a.io_bf16) return a.C % 8 == 0 ? restore_v<true, 8>(a, nb, st) : restore_v<true, 1>(a, nb, st);
     return a.C % 8 == 0 ? restore_v<false, 8>(a, nb, st) : restore_v<false, 1>(a, nb, st);
