@@ -8,12 +8,14 @@ namespace {
 
 // ------------------------------------------------------------------ packed sequences
 // One workgroup: clamps cu_seqlens into [0, T], makes it non-decreasing (a running maximum), numbers the chunks and
-// segments, and orders the sequences by length, 1024 of them at a time. T < 2^31. (4 us; without the order the state pass
-// over 16 sequences of 17011 tokens, 32 heads, took 275 us, not 227.)
+// segments, and orders up to 1024 sequences by length: one that starts late would run on alone (more of them balance by
+// their number). T < 2^31. (4 us; without the order the state pass over 16 sequences of 17011 tokens, 32 heads, took 275
+// us, not 227.)
 __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T,
                                                             uint32_t seg_chunks, Seq *__restrict__ seqs,
                                                             int32_t *__restrict__ order) {
-    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16], s_all[1024];
+    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16];
+    __shared__ __align__(16) uint32_t s_all[1024];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     auto entry = [&](int64_t i) -> uint32_t {
         const int32_t x = cu[i];
@@ -50,12 +52,16 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
         if (lane == 63) s_chunks[wave] = uc, s_segs[wave] = us;
         s_all[t] = chunks;
         __syncthreads();
-        // the longest first, of equal ones the first: one that starts late would run on alone
-        if (n < N) {
-            const int all = N - base < 1024 ? (int)(N - base) : 1024;
-            int before_it = 0;
-            for (int j = 0; j < all; ++j) before_it += s_all[j] > chunks || (s_all[j] == chunks && j < t);
-            order[base + before_it] = (int32_t)n;
+        if (N > 1024) {
+            if (n < N) order[n] = (int32_t)n;
+        } else if (n < N) {  // the longest first, of equal ones the first; lengths behind the last are 0 and come last
+            int ahead = 0;
+            for (int j = 0; j < N; j += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(s_all + j);
+                ahead += (x.x > chunks || (x.x == chunks && j < t)) + (x.y > chunks || (x.y == chunks && j + 1 < t)) +
+                         (x.z > chunks || (x.z == chunks && j + 2 < t)) + (x.w > chunks || (x.w == chunks && j + 3 < t));
+            }
+            order[ahead] = (int32_t)n;
         }
         uint32_t ac = 0, as = 0;
         for (int w = 0; w < 16; ++w) {

@@ -65,7 +65,7 @@ constexpr int rec_weights(bool bwd) { return (bwd ? 3 : 2) * kMatBytes; }
 
 struct Common {
     const Seq *seqs;   // or null: rows of T tokens
-    const int32_t *order;  // the sequences, the longest first (of each 1024), or null
+    const int32_t *order;  // the sequences in the order of their workgroups, or null
     int64_t T, ntok, slots, segs;  // slots, segs: chunks and segments of all sequences (upper bounds when packed)
     int32_t nch, nseg;  // per row (not packed)
     int32_t seg;        // chunks of a segment

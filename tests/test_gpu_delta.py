@@ -426,6 +426,69 @@ def test_gradients_at_long_offsets():
         assert torch.equal(r["dS0"][n + 1], r1["dS0"][0])
 
 
+@pytest.mark.parametrize("io,K", [("bf16", 128), ("bf16", 32), ("fp32", 128), ("fp32", 64)])
+def test_many_heads_share_compute_units(io, K):
+    """Where there are more column tiles than compute units both of a head go to one workgroup: the same bits as of a call of
+    few heads (two chunks, so that the gradients' segments are the same)."""
+    H, Hk, V = 260, 130, 128
+    x = inputs(1, 45, H, Hk, K, V, io, 97)
+    o, S = kda.gd_chunk_fwd(*(x[n] for n in ARGS), S0=x["S0"], scale=0.3)
+    r = kda.gd_chunk_bwd(*(x[n] for n in ARGS), x["do"], S0=x["S0"], dS_final=x["dS"], scale=0.3)
+    for h in (0, 126, 256):
+        few = {n: t[:, :, h // 2:h // 2 + 2] if n in ("q", "k") else t[:, h:h + 4] if n in ("S0", "dS") else t[:, :, h:h + 4]
+               for n, t in x.items()}
+        few = {n: t.contiguous() for n, t in few.items()}
+        o1, S1 = kda.gd_chunk_fwd(*(few[n] for n in ARGS), S0=few["S0"], scale=0.3)
+        r1 = kda.gd_chunk_bwd(*(few[n] for n in ARGS), few["do"], S0=few["S0"], dS_final=few["dS"], scale=0.3)
+        assert torch.equal(o[:, :, h:h + 4], o1) and torch.equal(S[:, h:h + 4], S1)
+        for n in ("dv", "dg", "dbeta"):
+            assert torch.equal(r[n][:, :, h:h + 4], r1[n]), n
+        for n in ("dq", "dk"):
+            assert torch.equal(r[n][:, :, h // 2:h // 2 + 2], r1[n]), n
+        assert torch.equal(r["dS0"][:, h:h + 4], r1["dS0"])
+
+
+def test_many_packed_sequences_share_compute_units():
+    """The same for packed ones, whose workgroups start in the order of their lengths: each as if it were alone."""
+    H, K, V, N = 32, 64, 128, 41
+    gen = torch.Generator().manual_seed(12)
+    lengths = torch.randint(0, 90, (N,), generator=gen)
+    lengths[5] = lengths[17] = 0
+    lengths[23] = 700
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lengths.cumsum(0)]).to(torch.int32)
+    T = int(cu[-1])
+    x = inputs(1, T, H, H // 2, K, V, "bf16", 98, gates="fp32", N=N)
+    dev = cu.cuda()
+    o, S = kda.gd_chunk_fwd(*(x[n] for n in ARGS), S0=x["S0"], cu_seqlens=dev)
+    r = kda.gd_chunk_bwd(*(x[n] for n in ARGS), x["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=dev)
+    assert torch.equal(S[5], x["S0"][5]) and torch.equal(r["dS0"][17], x["dS"][17])
+    for n in (0, 6, 23, 40):
+        a, b = int(cu[n]), int(cu[n + 1])
+        one = [x[m][:, a:b].contiguous() for m in ARGS + ("do",)]
+        S0, dS = x["S0"][n:n + 1].contiguous(), x["dS"][n:n + 1].contiguous()
+        o1, S1 = kda.gd_chunk_fwd(*one[:5], S0=S0)
+        r1 = kda.gd_chunk_bwd(*one, S0=S0, dS_final=dS)
+        assert torch.equal(o[:, a:b], o1) and torch.equal(S[n:n + 1], S1)
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(r[m][:, a:b], r1[m]), m
+        assert torch.equal(r["dS0"][n:n + 1], r1["dS0"])
+
+
+@pytest.mark.parametrize("N", [1023, 1024, 1025, 2500])
+def test_many_short_sequences(N):
+    """Packed sequences of two tokens equal the rows of a batch, bit for bit, also where the table takes several turns."""
+    x = inputs(N, 2, 2, 1, 32, 64, "bf16", 99)
+    flat = {n: x[n].reshape((1, 2 * N) + x[n].shape[2:]) for n in ARGS + ("do",)}
+    cu = torch.arange(0, 2 * N + 1, 2, dtype=torch.int32, device="cuda")
+    o, S = kda.gd_chunk_fwd(*(x[n] for n in ARGS), S0=x["S0"])
+    po, pS = kda.gd_chunk_fwd(*(flat[n] for n in ARGS), S0=x["S0"], cu_seqlens=cu)
+    assert torch.equal(po.reshape(o.shape), o) and torch.equal(pS, S)
+    r = kda.gd_chunk_bwd(*(x[n] for n in ARGS), x["do"], S0=x["S0"], dS_final=x["dS"])
+    pr = kda.gd_chunk_bwd(*(flat[n] for n in ARGS), flat["do"], S0=x["S0"], dS_final=x["dS"], cu_seqlens=cu)
+    for n in r:
+        assert torch.equal(pr[n].reshape(r[n].shape), r[n]), n
+
+
 def test_refusals():
     x = inputs(1, 8, 4, 2, 32, 32, "bf16", 93)
     q, k, v, g, beta = (x[n] for n in ARGS)
