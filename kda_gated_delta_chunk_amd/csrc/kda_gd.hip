@@ -80,8 +80,8 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
 // ------------------------------------------------------------------ the chunks' records
 // One wavefront per (chunk, q/k head): the products k_r.k_i and q_r.k_i once, then for every v head that shares them the
 // decays, A and its inverse. The inverse by blocks of 16: by substitution over all 32 rows the registers that hold them
-// spilled (464 us for the 70 below). It is formed in fp32; as operands its matrices leave in two bf16 parts (2^-17 of an
-// entry), which with the states' is what dbeta of fp32 gates is off by (2.6e-6 of its size, dg 1e-6).
+// spilled (464 us for the 70 below). It is formed in fp32; as operands the matrices leave in two bf16 parts (2^-17 of an
+// entry), for the gradients of fp32 gates in three: with two dbeta was off by 2.6e-6 of its size, with three by 2.4e-7.
 // HBM bounds it: 4096 tokens of 96 heads of 128 channels, bf16, move 328 MB in 69 us (4.8 TB/s), backward 377 MB in 79.
 constexpr int kPitch = kChunkTokens + 4;
 template <bool BF, bool GF, int K, bool BWD>
@@ -262,7 +262,19 @@ __global__ __launch_bounds__(64) void kda_gd_prep_kernel(const Common cm, const 
                     __syncthreads();
                 }
         }
-        // ---- as operands
+        // ---- as operands (bf16 beside fp32 gates: what two parts leave of an entry lies by itself)
+        auto put = [&](int which, int tt, const float (&x)[8]) __attribute__((always_inline)) {
+            if constexpr (BF && GF && BWD) {
+                Multi<true, 3> f;
+                set_multi(f, x);
+                store_mat(rec + which * kMatBytes, tt, lane, Pair<true>{{f.p[0], f.p[1]}});
+                __builtin_memcpy(cm.third + (((slot * cm.H + h) * 3 + which) * 2 + tt) * (kThirdBytes / 2) + lane * 16, &f.p[2], 16);
+            } else {
+                Pair<BF> f;
+                set_multi(f, x);
+                store_mat(rec + which * kMatBytes, tt, lane, f);
+            }
+        };
         auto rows = [&](const float (&m)[C][kPitch], int r, float (&x)[8]) __attribute__((always_inline)) {
             *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(&m[r][token_of(0, g)]);
             *reinterpret_cast<f32x4 *>(x + 4) = *reinterpret_cast<const f32x4 *>(&m[r][token_of(1, g)]);
@@ -274,21 +286,16 @@ __global__ __launch_bounds__(64) void kda_gd_prep_kernel(const Common cm, const 
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
             float x[8];
-            Pair<BF> f;
             rows(s_a[0], 16 * tt + li, x);
-            set_multi(f, x);
-            store_mat(rec + kMatN * kMatBytes, tt, lane, f);
+            put(kMatN, tt, x);
             if constexpr (!BWD) {
                 rows(s_p, 16 * tt + li, x);
-                set_multi(f, x);
-                store_mat(rec + kMatP * kMatBytes, tt, lane, f);
+                put(kMatP, tt, x);
             } else {
                 cols(s_a[BWD], 16 * tt + li, x);
-                set_multi(f, x);
-                store_mat(rec + kMatNT * kMatBytes, tt, lane, f);
+                put(kMatNT, tt, x);
                 cols(s_p, 16 * tt + li, x);
-                set_multi(f, x);
-                store_mat(rec + kMatPT * kMatBytes, tt, lane, f);
+                put(kMatPT, tt, x);
             }
         }
     }
@@ -318,7 +325,7 @@ __global__ __launch_bounds__(256) void kda_gd_group_kernel(const Common cm, cons
 
 // ------------------------------------------------------------------ workspace
 struct Layout {
-    size_t seqs, order, rec, z, dw, seed_s, seed_g, dk_part, dq, dk, total;
+    size_t seqs, order, rec, third, z, dw, seed_s, seed_g, dk_part, dq, dk, total;
 };
 struct Sizes {
     int64_t slots, segs;
@@ -360,6 +367,7 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
     }
     l.rec = take(ch * rec_bytes(bwd));
     if (bwd) {
+        l.third = take(tile_bytes > 4 ? ch * 3 * kThirdBytes : 0);
         l.z = take(ch * V * kChunkTokens * tile_bytes);
         l.dw = take(ch * V * kChunkTokens * tile_bytes);
         l.seed_s = take((size_t)s.segs * H * K * V * 4);
@@ -409,6 +417,7 @@ Call prepare(const GdArgs &a, bool bwd) {
     x.c.H = a.H;
     x.c.Hk = a.Hk;
     x.c.rec = x.ws + x.l.rec;
+    x.c.third = bwd && tile_parts(a.io_bf16, a.gates_fp32) == 3 ? x.ws + x.l.third : nullptr;
     return x;
 }
 

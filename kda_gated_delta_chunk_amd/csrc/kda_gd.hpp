@@ -58,7 +58,7 @@ struct Seq {
 // which a wavefront's lanes read them as operands: [16-row tile][half][lane][16 bytes], the halves a bf16 pair's parts
 // or the first and last four of eight fp32 slots.
 enum Mat { kMatN = 0, kMatP = 1, kMatNT = 1, kMatPT = 2 };  // forward: N, P; backward: N, its transpose, P's
-constexpr int kMatBytes = 4096;
+constexpr int kMatBytes = 4096, kThirdBytes = 2048;
 enum Weight { kEnter, kEnterScaled, kLeave, kLeaveBeta, kBeta, kSumHi, kSumLo, kTotal, kWeights };
 constexpr int rec_bytes(bool bwd) { return (bwd ? 3 : 2) * kMatBytes + kWeights * kChunkTokens * 4; }
 constexpr int rec_weights(bool bwd) { return (bwd ? 3 : 2) * kMatBytes; }
@@ -71,6 +71,7 @@ struct Common {
     int32_t seg;        // chunks of a segment
     int32_t N, H, Hk;
     char *rec;          // [slots][H] records
+    char *third;        // backward, bf16 I/O beside fp32 gates: third parts of the records' matrices, in their order; or null
 };
 
 struct StateArgs {

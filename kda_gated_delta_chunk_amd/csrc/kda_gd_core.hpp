@@ -365,14 +365,15 @@ struct StateLds {
 // are at once operands of the products with the state, so it never leaves the registers. A third of the wavefronts bring
 // the rows, a chunk ahead in LDS and another on its way: done by the rest beside their products it took 700 cycles a chunk.
 // bf16: products of inputs are exact, the state and computed operands go in as two bf16 parts, what is added to the state
-// as three (the state after 4096 tokens is off by 5e-7 of its size, an output by what its own rounding gives).
+// as three (the state after 4096 tokens is off by 5e-7 of its size, an output by what its own rounding gives). NP = 3, the
+// gradients beside fp32 gates: all of them three (4100 tokens of 32 heads: 177 us for 157).
 //
 // Bound by one wavefront's way through a chunk, whose steps wait for one another: forward 68 matrix instructions (1088
 // cycles), about 230 vector ones (1100), 40 reads of an LDS that three others read as well (870): 3300 cycles, 170 us for
 // 4096 tokens of one head, 195 for 96 (410 + 100 MB, 2.6 TB/s; matrix instructions run in 32% of the cycles of the units in
 // use, LDS in 29%). Other orders of the products, the next chunk's first operands read ahead of the barrier, the state's parts
 // formed between the update's products: all within 3%. Backward, both passes of 96 heads 411 us (1.4 GB, 3.4 TB/s).
-template <bool BF, int K, int VT, int MODE>
+template <bool BF, int K, int VT, int MODE, int NP>
 __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t blk, char *smem) {
     using L = StateLds<BF, K, VT, MODE>;
     using RK = Rw<BF, K>;
@@ -479,9 +480,21 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
     char *po = reinterpret_cast<char *>(A.o) + ((sq.t0 + (REV ? nch - 1 : 0) * (int64_t)C) * A.c.H + h) * V * EB;
     auto tokens_of = [&](int c) __attribute__((always_inline)) { return len - c * C < C ? len - c * C : C; };
     const int row0 = RK::row_at(lane), tile0 = RK::tile_at(lane), col0 = RV::col_at(lane, wave);
-    Pair<BF> sf[KC][1];  // the state as an operand
+    Multi<BF, NP> sf[KC][1];  // the state as an operand
 #pragma unroll
-    for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
+    for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, NP>(st[2 * kc], st[2 * kc + 1]);
+    Frag8<BF> next[REV ? 2 : 1][2];  // the next chunk's third parts of P's transpose and N's, or of N
+    auto thirds = [&](int c) __attribute__((always_inline)) {
+        if constexpr (BF && NP == 3)
+#pragma unroll
+            for (int n = 0; n < (REV ? 2 : 1); ++n)
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+                    __builtin_memcpy(&next[n][tt],
+                                     A.c.third + (((sq.first + c) * A.c.H + h) * 3 + (REV ? kMatPT - n : kMatN)) * kThirdBytes +
+                                         tt * (kThirdBytes / 2) + lane * 16, 16);
+    };
+    if (nch > 0) thirds(REV ? nch - 1 : 0);
     for (int cc = 0; cc < nch; ++cc) {
         const int c = REV ? nch - 1 - cc : cc, b = cc & (NB - 1);
         __syncthreads();  // nobody reads the last chunk's rows any more (NB = 2: and this one's are there)
@@ -499,10 +512,24 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
         if (MODE == kReverse && c + 1 < nch && ((c + 1) & (A.c.seg - 1)) == 0)
             put_state(A.seed + ((sq.seg + c / A.c.seg) * A.c.H + h) * sstate);
 
+        Frag8<BF> third[REV ? 2 : 1][2];
+        if constexpr (BF && NP == 3) {
+#pragma unroll
+            for (int n = 0; n < (REV ? 2 : 1); ++n)
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) third[n][tt] = next[n][tt];
+            if (cc + 1 < nch) thirds(REV ? c - 1 : c + 1);
+        }
+        auto mat_of = [&](Multi<BF, NP> &m, int which, int tt) __attribute__((always_inline)) {
+            const Pair<BF> p = load_mat<BF>(sr + which * kMatBytes, tt, lane);
+            __builtin_memcpy(&m, &p, sizeof(p));
+            if constexpr (BF && NP == 3) m.p[2] = third[REV && which == kMatNT][tt];
+        };
+
         // ---- products with the state: K S, and S^T q. The operands are asked for ahead of the products.
         f32x4 x[2] = {zero4(), zero4()}, y[2] = {zero4(), zero4()};
         Exact<BF> kf[KC][2], qf[KC][2];
-        Pair<BF> mat[2];
+        Multi<BF, NP> mat[2];
         float vx[8], r[8], z[8], w[8];
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc)
@@ -515,7 +542,7 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
         for (int kc = 0; kc < KC; ++kc) mmx(x, kf[kc], sf[kc]);
         KDA_ORDER;
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) mat[tt] = load_mat<BF>(sr + (REV ? kMatPT : kMatN) * kMatBytes, tt, lane);
+        for (int tt = 0; tt < 2; ++tt) mat_of(mat[tt], REV ? kMatPT : kMatN, tt);
         if constexpr (MODE == kForward)
 #pragma unroll
             for (int kc = 0; kc < KC; ++kc)
@@ -543,10 +570,10 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = x[i >> 2][i & 3];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) mat[tt] = load_mat<BF>(sr + kMatNT * kMatBytes, tt, lane);
+            for (int tt = 0; tt < 2; ++tt) mat_of(mat[tt], kMatNT, tt);
         }
         {
-            Pair<BF> rp[1];
+            Multi<BF, NP> rp[1];
             set_multi(rp[0], r);
             mmx(x, mat, rp);
         }
@@ -566,7 +593,7 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 y[tt] *= wt[kEnterScaled * C + 16 * tt + li];
-                mat[tt] = load_mat<BF>(sr + kMatP * kMatBytes, tt, lane);
+                mat_of(mat[tt], kMatP, tt);
             }
         }
         KDA_ORDER;
@@ -585,7 +612,7 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
                 mix_cols<BF>(y, z, sr + kMatP * kMatBytes, lane);
                 zp[0] = Pair<BF>{};
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) mat[tt] = Pair<BF>{};
+                for (int tt = 0; tt < 2; ++tt) mat[tt] = Multi<BF, NP>{};
             } else if constexpr (BF) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split_bf16(z[2 * i], z[2 * i + 1], zp[0].p[0].p[i], zp[0].p[1].p[i]);
@@ -686,7 +713,7 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
         }
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][KT]>(st));
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, 2>(st[2 * kc], st[2 * kc + 1]);
+        for (int kc = 0; kc < KC; ++kc) sf[kc][0] = multi_of<BF, NP>(st[2 * kc], st[2 * kc + 1]);
     }
     if (A.s_end) put_state(A.s_end + nh * sstate);
 }
@@ -694,15 +721,15 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
 template <bool BF, int K, int VT>
 __global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_state_kernel(const StateArgs A, int V) {
     __shared__ __align__(16) char smem[StateLds<BF, K, VT, kForward>::bytes];
-    state_pass<BF, K, VT, kForward>(A, V, blockIdx.x + (int64_t)blockIdx.y * gridDim.x, smem);
+    state_pass<BF, K, VT, kForward, 2>(A, V, blockIdx.x + (int64_t)blockIdx.y * gridDim.x, smem);
 }
 // The backward call's two passes wait for nothing of each other's: one launch, the longer one's workgroups first.
-template <bool BF, int K, int VT>
+template <bool BF, int K, int VT, int NP>
 __global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_states_kernel(const StateArgs R, const StateArgs E, int V, int64_t blocks) {
     __shared__ __align__(16) char smem[StateLds<BF, K, VT, kReverse>::bytes];
     const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
-    if (blk < blocks) state_pass<BF, K, VT, kReverse>(R, V, blk, smem);
-    else state_pass<BF, K, VT, kErrors>(E, V, blk - blocks, smem);
+    if (blk < blocks) state_pass<BF, K, VT, kReverse, NP>(R, V, blk, smem);
+    else state_pass<BF, K, VT, kErrors, NP>(E, V, blk - blocks, smem);
 }
 
 }  // namespace gd

@@ -9,21 +9,26 @@ hipError_t launch(StateArgs a, StateArgs *e, int V, hipStream_t st) {
     a.tiles = V / VT;
     if (e) e->tiles = a.tiles;
     const int64_t blocks = ((int64_t)a.c.N * a.c.H + 7) / 8 * 8 * a.tiles;
-    if (e)
-        hipLaunchKernelGGL((kda_gd_states_kernel<BF, K, VT>), hd::wide_grid(2 * blocks), dim3(VT * 6), 0, st, a, *e, V, blocks);
+    const dim3 grid = hd::wide_grid(e ? 2 * blocks : blocks);
+    if (e && a.c.third)
+        hipLaunchKernelGGL((kda_gd_states_kernel<BF, K, VT, BF && !(K == 128 && VT == 128) ? 3 : 2>), grid, dim3(VT * 6), 0, st,
+                           a, *e, V, blocks);
+    else if (e)
+        hipLaunchKernelGGL((kda_gd_states_kernel<BF, K, VT, 2>), grid, dim3(VT * 6), 0, st, a, *e, V, blocks);
     else
-        hipLaunchKernelGGL((kda_gd_state_kernel<BF, K, VT>), hd::wide_grid(blocks), dim3(VT * 6), 0, st, a, V);
+        hipLaunchKernelGGL((kda_gd_state_kernel<BF, K, VT>), grid, dim3(VT * 6), 0, st, a, V);
     return hipGetLastError();
 }
 // Tiles of 64 columns occupy a compute unit each. Where there are more of them than compute units, the two of a head share
 // one: their products overlap, and they read the same rows (4096 tokens of 256 heads: 318 us for 401; of 64 heads 184 us
 // and 300). Packed sequences are balanced as they come, which takes several pieces for every compute unit (16 of 17011 tokens,
-// 32 heads: 251 us for 226).
+// 32 heads: 251 us for 226). With three parts and K = 128 the registers of both tiles' wavefronts spill (backward passes of
+// 4096 tokens of 96 heads: 907 us for 531): one tile then.
 template <bool BF, int K>
 hipError_t by_tile(const StateArgs &a, StateArgs *e, int V, hipStream_t st) {
     constexpr int64_t kUnits = 256;
     const int64_t items = (int64_t)a.c.N * a.c.H * (e ? 2 : 1);
-    const bool many = a.c.seqs ? items >= 4 * kUnits : 2 * items > kUnits;
+    const bool fits = !(K == 128 && a.c.third), many = fits && (a.c.seqs ? items >= 4 * kUnits : 2 * items > kUnits);
     return V == 32              ? launch<BF, K, 32>(a, e, V, st)
            : V == 64 || !many   ? launch<BF, K, 64>(a, e, V, st)
                                 : launch<BF, K, 128>(a, e, V, st);
