@@ -335,7 +335,11 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         put(0);
         if (nch > 1) take(1);
     }
+    // the gradient behind the segment: for the walk back, asked for before the last chunk where registers are left
     f32x4 gt[VT];
+    constexpr bool EARLY = NP == 2;
+    const float *const behind =
+        c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr;
     for (int i = 0; i < nch; ++i) {
         const int64_t tc = sq.t0 + (int64_t)(c0 + i) * C;
         const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
@@ -347,8 +351,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
             else if (nch > 1) take(nch - 2);  // the walk back begins with the chunk that is here
             __syncthreads();
         }
-        if (i == nch - 1)  // behind the segment, for the walk back
-            get_state(c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr, gt);
+        if (EARLY && i == nch - 1) get_state(behind, gt);
         // ---- the pairs' weights: lane holds sources i = 16 ts + 4g .. of token r = 16 tt + l % 16
         for (int p = wave; p < 6; p += NW) {
             const int which = p >= 3, x = which ? p - 3 : p, tt = x > 0, ts = x > 1;
@@ -479,6 +482,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
         hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
     }
     // ---- what the border behind the segment passes on
+    if (!EARLY) get_state(behind, gt);
     float border = 0.f;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
