@@ -61,7 +61,8 @@ __global__ __launch_bounds__(256) void kda_ckpt_save_kernel(const void *__restri
             if (lane * V < n) {
                 u32x4 w[BF ? 1 : 2];
 #pragma unroll
-                for (int i = 0; i < (BF ? 1 : 2); ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + lane * V) + i);
+                for (int i = 0; i < (BF ? 1 : 2); ++i)
+                    w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + lane * V) + i);
                 __builtin_memcpy(e, w, sizeof(e));
             }
 #pragma unroll

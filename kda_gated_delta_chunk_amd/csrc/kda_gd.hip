@@ -268,7 +268,8 @@ __global__ __launch_bounds__(64) void kda_gd_prep_kernel(const Common cm, const 
                 Multi<true, 3> f;
                 set_multi(f, x);
                 store_mat(rec + which * kMatBytes, tt, lane, Pair<true>{{f.p[0], f.p[1]}});
-                __builtin_memcpy(cm.third + (((slot * cm.H + h) * 3 + which) * 2 + tt) * (kThirdBytes / 2) + lane * 16, &f.p[2], 16);
+                __builtin_memcpy(cm.third + (((slot * cm.H + h) * 3 + which) * 2 + tt) * (kThirdBytes / 2) + lane * 16,
+                                 &f.p[2], 16);
             } else {
                 Pair<BF> f;
                 set_multi(f, x);

@@ -22,8 +22,6 @@ namespace kda {
 namespace gd {
 
 using hd::lane_value;
-using hd::Rows;
-using hd::Stage;
 using hd::u32x2;
 using hd::u32x4;
 
@@ -725,7 +723,9 @@ __global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_state_kern
 }
 // The backward call's two passes wait for nothing of each other's: one launch, the longer one's workgroups first.
 template <bool BF, int K, int VT, int NP>
-__global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_states_kernel(const StateArgs R, const StateArgs E, int V, int64_t blocks) {
+__global__ __launch_bounds__(VT * 6, (VT == 128 ? 3 : 2)) void kda_gd_states_kernel(const StateArgs R,
+                                                                                          const StateArgs E, int V,
+                                                                                          int64_t blocks) {
     __shared__ __align__(16) char smem[StateLds<BF, K, VT, kReverse>::bytes];
     const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
     if (blk < blocks) state_pass<BF, K, VT, kReverse, NP>(R, V, blk, smem);

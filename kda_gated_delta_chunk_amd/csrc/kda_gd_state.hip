@@ -29,9 +29,9 @@ hipError_t by_tile(const StateArgs &a, StateArgs *e, int V, hipStream_t st) {
     constexpr int64_t kUnits = 256;
     const int64_t items = (int64_t)a.c.N * a.c.H * (e ? 2 : 1);
     const bool fits = !(K == 128 && a.c.third), many = fits && (a.c.seqs ? items >= 4 * kUnits : 2 * items > kUnits);
-    return V == 32              ? launch<BF, K, 32>(a, e, V, st)
-           : V == 64 || !many   ? launch<BF, K, 64>(a, e, V, st)
-                                : launch<BF, K, 128>(a, e, V, st);
+    return V == 32            ? launch<BF, K, 32>(a, e, V, st)
+           : V == 64 || !many ? launch<BF, K, 64>(a, e, V, st)
+                              : launch<BF, K, 128>(a, e, V, st);
 }
 template <bool BF>
 hipError_t by_k(const StateArgs &a, StateArgs *e, int K, int V, hipStream_t st) {
