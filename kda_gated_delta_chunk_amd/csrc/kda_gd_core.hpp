@@ -600,7 +600,8 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
         for (int i = 0; i < 8; ++i) z[i] = x[i >> 2][i & 3];
         Pair<BF> zp[1];
         set_multi(zp[0], z);
-        if (!finite(zp[0])) {  // a source that is not shows in its own row
+        const bool fine_z = finite(zp[0]);
+        if (!fine_z) {  // a source that is not shows in its own row
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = r[i];
             mix_rows<BF, REV>(x, r, sr + (REV ? kMatNT : kMatN) * kMatBytes, lane);
@@ -627,7 +628,15 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
                 for (int n = 0; n < 2; ++n) __builtin_memcpy(p + n * V * (C * 2), &zp[0].p[n], 16);
                 if (A.parts == 3) {
                     Multi<true, 3> all;
-                    set_multi(all, z);
+                    if (fine_z) {
+                        set_multi(all, z);
+                    } else {  // a token's parts by themselves: the gradients read them token by token
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t hi = zp[0].p[0].p[i], lo = zp[0].p[1].p[i];
+                            all.p[2].p[i] = pack_bf16(z[2 * i] - bf_lo(hi) - bf_lo(lo), z[2 * i + 1] - bf_hi(hi) - bf_hi(lo));
+                        }
+                    }
                     __builtin_memcpy(p + 2 * V * (C * 2), &all.p[2], 16);
                 }
             } else {
