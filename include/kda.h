@@ -678,7 +678,10 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weig
  * channels (the last of a row may be fewer):
  *   scale = max |x| / 127,   code = 127 x / max |x| to the nearest whole
  *   number, ties to even,    value = code * scale, rounded to `io`
- * A value is off by at most half a scale. Channels that are all zero have
+ * in fp32 (a scale whose 127-fold would pass fp32's largest value is the one
+ * below it: finite values come back finite). Before its rounding to `io` a
+ * value is off by at most half a scale, and the roundings of fp32, less than
+ * 2^-14 of a scale. Channels that are all zero have
  * scale 0; a block that holds an infinity or a NaN has scale NaN and comes
  * back as NaN; one whose largest value is below 2^-119 loses precision to the
  * range of its scale.

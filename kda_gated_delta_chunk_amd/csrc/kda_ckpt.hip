@@ -1,7 +1,8 @@
 // Activation checkpoints in 8 bits, for gfx950: along every row 128 values share a step, their largest size's 127th part,
 //   step = max |x| / 127,  code = the nearest whole number to 127 x / max |x| (ties to even),  x ~ code * step.
-// A value is off by at most half a step, 2^-8 of the block's largest (uniform steps: for values of one scale the error
-// is a quarter of what 8-bit floating point leaves). A block that holds an infinity or a NaN comes back as NaN.
+// A value is off by at most half a step, 2^-8 of the block's largest, before it is rounded to its type (uniform steps: for
+// values of one scale the error is a quarter of what 8-bit floating point leaves). A block that holds an infinity or a NaN
+// comes back as NaN.
 //
 // The kernels only move bytes: x once and one byte a value. A group of lanes owns a block, eight values each, so the
 // largest is found across lanes and every load and store is 8 to 32 bytes wide. 8192 x 4096 values of bf16, 102 MB either
@@ -16,6 +17,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 // 127 x / top to the nearest: the quotient by the reciprocal, then what it leaves of the dividend (exact) divided once
 // more, which brings a quotient that is a half exactly there. The dividend is scaled so that nothing over- or underflows.
+// 127 x is exact for bf16 and rounded once for fp32, where a quotient within 2^-16 of a half can go either way.
 struct Quantizer {
     float top, inv, scale;
     __device__ __forceinline__ explicit Quantizer(float largest) {
@@ -91,7 +93,11 @@ __global__ __launch_bounds__(256) void kda_ckpt_save_kernel(const void *__restri
             for (int i = 0; i < V; ++i)
                 if (lane + i * LPB < n) o[lane + i * LPB] = out[i];
         }
-        if (lane == 0) scales[b] = bad ? __builtin_nanf("") : top / 127.f;
+        // The quotient may round up: where 127 of it would pass the largest value of fp32, the scale below it (off by less
+        // than one step of fp32, so that 127 of it stay under the largest).
+        float scale = top / 127.f;
+        if (scale * 127.f > __FLT_MAX__) scale = __uint_as_float(__float_as_uint(scale) - 1);
+        if (lane == 0) scales[b] = bad ? __builtin_nanf("") : scale;
     }
 }
 

@@ -103,8 +103,9 @@ def _need8(c, name, shape, dev):
 
 def checkpoint8(x, out=None):
     """x [..., C] (bf16 or fp32) as a Checkpoint8: codes = 127 x / max |x| to the nearest whole number (ties to even),
-    scales = max |x| / 127, the maximum over 128 adjacent values of the last axis. A value is off by at most half a
-    scale; a block with an infinity or a NaN comes back as NaN. ``out`` may hold a Checkpoint8 to write into."""
+    scales = max |x| / 127, the maximum over 128 adjacent values of the last axis. Before it is rounded to x's dtype a
+    value is off by at most half a scale; a block with an infinity or a NaN comes back as NaN. ``out`` may hold a
+    Checkpoint8 to write into."""
     lib = _lib.load()
     dev, io = _cuda(x), _io_code(x.dtype)
     if x.dim() < 1 or x.shape[-1] < 1:
