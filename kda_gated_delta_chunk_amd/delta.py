@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import _io_code, _lib, _ptr
-from .layers import _call, _cuda, _hd_seqs, _need, _restored, _result, _states, _workspace
+from .layers import _call, _cuda, _hd_seqs, _int32, _need, _restored, _result, _states, _workspace
 
 __all__ = ["gd_chunk_fwd", "gd_chunk_bwd", "gd_decode_step", "gd_workspace_bytes", "gd_bwd_workspace_bytes"]
 
@@ -40,6 +40,8 @@ def _inputs(q, k, v, g, beta, lead):
     _need(q, "q", lead + (Hk, K), dt, dev)
     _need(k, "k", lead + (Hk, K), dt, dev)
     _need(v, "v", lead + (H, V), dt, dev)
+    if (H * V | Hk * K) >> 31:
+        _int32(H, Hk, K, V)
     gt = torch.float32 if g.dtype is torch.float32 else dt
     _need(g, "g", lead + (H,), gt, dev)
     _need(beta, "beta", lead + (H,), gt, dev)

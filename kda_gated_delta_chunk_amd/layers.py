@@ -47,6 +47,12 @@ def _cuda(t):
     return t.device
 
 
+def _int32(*sizes):
+    """Sizes that go into the library as 32-bit numbers: ctypes would pass on the low bits of larger ones."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes %s: at most 2^31 - 1" % (sizes,))
+
+
 def _workspace(workspace, need: int, dev, what: str, *sizes):
     if need == 0:
         raise KDAError(2, what % sizes)
@@ -110,6 +116,7 @@ def checkpoint8(x, out=None):
     dev, io = _cuda(x), _io_code(x.dtype)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x has shape %s, expected at least one value in a row" % (tuple(x.shape),))
+    _int32(x.shape[-1])
     _need(x, "x", x.shape, x.dtype, dev)
     if out is None:
         out = Checkpoint8(torch.empty(x.shape, dtype=torch.int8, device=dev),
@@ -129,6 +136,7 @@ def restore8(c, out=None):
     dev, io, shape = _cuda(c.codes), _io_code(c.dtype), c.codes.shape
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("codes has shape %s, expected at least one value in a row" % (tuple(shape),))
+    _int32(shape[-1])
     _need8(c, "c", shape, dev)
     if out is None:
         out = torch.empty(shape, dtype=c.dtype, device=dev)
@@ -171,6 +179,8 @@ def _hd_inputs(q, k, v, g, lead):
     _need(q, "q", lead + (Hk, K), dt, dev)
     _need(k, "k", lead + (Hk, K), dt, dev)
     _need(v, "v", lead + (H, V), dt, dev)
+    if (H * V | Hk * K) >> 31:
+        _int32(H, Hk, K, V)
     if g.dim() == 1:
         _need(g, "g", (H,), torch.float32, dev)
         return H, Hk, K, V, dt, _lib.KDA_DECAY_PER_HEAD
@@ -184,6 +194,7 @@ def _hd_seqs(q, cu_seqlens):
     if cu_seqlens is None:
         return q.shape[0]
     _need(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, q.device)
+    _int32(cu_seqlens.numel())
     return cu_seqlens.numel() - 1
 
 
@@ -336,6 +347,8 @@ def rotary(q, freqs, k=None, positions=None, layout: str = "half", inverse: bool
         raise ValueError("k_out without k")
     if positions is not None:
         _need(positions, "positions", lead, torch.int32, dev)
+    if ((Hq + Hk) * D + freqs.numel()) >> 30:
+        _int32(Hq, Hk, D, 2 * freqs.numel())
     out = _result(out, "out", q)
     _call(dev, lib.kda_rotary, _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), _ptr(out), _ptr(k_out),
           math.prod(lead), lead[-1], Hq, Hk, D, 2 * freqs.numel(), io, _lib.ROTARY_LAYOUTS[layout], int(bool(inverse)),
@@ -391,6 +404,8 @@ def rotary_axes(q, freqs, axes, positions, k=None, layout: str = "half", inverse
         k_out = _result(k_out, "k_out", k)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if ((Hq + Hk) * D + freqs.numel()) >> 30 or A >> 31:
+        _int32(A, Hq, Hk, D, 2 * freqs.numel())
     out = _result(out, "out", q)
     _call(dev, lib.kda_rotary_axes, _ptr(q), _ptr(k), _ptr(freqs), _ptr(axes), _ptr(positions), _ptr(out), _ptr(k_out),
           math.prod(lead), A, Hq, Hk, D, 2 * freqs.numel(), io, _lib.ROTARY_LAYOUTS[layout], int(bool(inverse)), scale)
@@ -415,6 +430,8 @@ def _norm_args(x, weight, bias, o_gate):
                 _need(t, name, shape, torch.float32, dev)
     if o_gate is not None:
         _need(o_gate, "o_gate", x.shape, x.dtype, dev)
+    if groups * C >> 31:
+        _int32(groups, C)
     return math.prod(x.shape[:-1]), max(groups, 1), C
 
 
