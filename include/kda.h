@@ -548,8 +548,8 @@ kda_status_t kda_hd_decode_step(const void *q, const void *k, const void *v, con
 
 /*
  * Workspace bytes of kda_gd_chunk_fwd and kda_gd_chunk_bwd (arguments as
- * there; packed: whether cu_seqlens is given, 0 or 1). 0 for sizes that are
- * not supported.
+ * there; packed: whether cu_seqlens is given, 0 or 1), for gates of either
+ * type. 0 for sizes that are not supported.
  */
 size_t kda_gd_chunk_fwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
                                         int32_t num_seqs, int32_t packed, kda_dtype_t io);

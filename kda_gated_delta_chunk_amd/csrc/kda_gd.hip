@@ -7,21 +7,21 @@ namespace gd {
 namespace {
 
 // ------------------------------------------------------------------ packed sequences
-// One workgroup: clamps cu_seqlens into [0, T], makes it non-decreasing (a running maximum), numbers the chunks and
-// segments, and orders up to 1024 sequences by length: one that starts late would run on alone (more of them balance by
+// One workgroup: clamps cu_seqlens into [0, T], makes it non-decreasing (a running maximum), numbers the chunks, segments and
+// borders between them, and orders up to 1024 sequences by length: one that starts late would run on alone (more of them balance by
 // their number). T < 2^31. (4 us; without the order the state pass over 16 sequences of 17011 tokens, 32 heads, took 275
 // us, not 227.)
 __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__restrict__ cu, int32_t N, uint32_t T,
-                                                            uint32_t seg_chunks, Seq *__restrict__ seqs,
+                                                            uint32_t seg_chunks, Packed *__restrict__ seqs,
                                                             int32_t *__restrict__ order) {
-    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16];
+    __shared__ uint32_t s_max[16], s_chunks[16], s_segs[16], s_borders[16];
     __shared__ __align__(16) uint32_t s_all[1024];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     auto entry = [&](int64_t i) -> uint32_t {
         const int32_t x = cu[i];
         return x < 0 ? 0 : (uint32_t)x > T ? T : (uint32_t)x;
     };
-    uint32_t top = entry(0), first = 0, seg = 0;
+    uint32_t top = entry(0), first = 0, seg = 0, border = 0;
     for (int64_t base = 0; base < N; base += 1024) {
         const int64_t n = base + t;
         uint32_t end = n < N ? entry(n + 1) : 0;
@@ -43,13 +43,14 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
         }
         const uint32_t chunks = (end - before + (kChunkTokens - 1)) / kChunkTokens;
         const uint32_t segs = (chunks + (seg_chunks - 1)) / seg_chunks;
-        uint32_t uc = chunks, us = segs;  // sums up to this sequence
+        const uint32_t borders = segs ? segs - 1 : 0;
+        uint32_t uc = chunks, us = segs, ub = borders;  // sums up to this sequence
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t x = __shfl_up(uc, d), y = __shfl_up(us, d);
-            if (lane >= d) uc += x, us += y;
+            const uint32_t x = __shfl_up(uc, d), y = __shfl_up(us, d), z = __shfl_up(ub, d);
+            if (lane >= d) uc += x, us += y, ub += z;
         }
-        if (lane == 63) s_chunks[wave] = uc, s_segs[wave] = us;
+        if (lane == 63) s_chunks[wave] = uc, s_segs[wave] = us, s_borders[wave] = ub;
         s_all[t] = chunks;
         __syncthreads();
         if (N > 1024) {
@@ -63,16 +64,19 @@ __global__ __launch_bounds__(1024) void kda_gd_table_kernel(const int32_t *__res
             }
             order[ahead] = (int32_t)n;
         }
-        uint32_t ac = 0, as = 0;
+        uint32_t ac = 0, as = 0, ab = 0;
         for (int w = 0; w < 16; ++w) {
-            if (w < wave) uc += s_chunks[w], us += s_segs[w];
+            if (w < wave) uc += s_chunks[w], us += s_segs[w], ub += s_borders[w];
             ac += s_chunks[w];
             as += s_segs[w];
+            ab += s_borders[w];
         }
         if (n < N)
-            seqs[n] = Seq{(int64_t)before, (int64_t)end, (int64_t)(first + uc - chunks), (int64_t)(seg + us - segs)};
+            seqs[n] = Packed{(int64_t)before, (int64_t)end, (int64_t)(first + uc - chunks), (int32_t)(seg + us - segs),
+                             (int32_t)(border + ub - borders)};
         first += ac;
         seg += as;
+        border += ab;
         __syncthreads();
     }
 }
@@ -329,7 +333,7 @@ struct Layout {
     size_t seqs, order, rec, third, z, dw, seed_s, seed_g, dk_part, dq, dk, total;
 };
 struct Sizes {
-    int64_t slots, segs;
+    int64_t slots, segs, borders;
     int32_t nch, nseg, seg;
 };
 // The segments' length by the heads alone, so that a sequence's gradients are the same bits in every batch: about two
@@ -350,6 +354,7 @@ Sizes sizes(int64_t B, int64_t T, int32_t N, int32_t H, int32_t K, bool packed) 
     s.nseg = (int32_t)(nseg ? nseg : 1);
     s.slots = packed ? T / kChunkTokens + N : B * nch;
     s.segs = packed ? T / (kChunkTokens * s.seg) + N : B * nseg;
+    s.borders = packed ? T / (kChunkTokens * s.seg) : B * (s.nseg - 1);  // a sequence of L tokens has (L - 1) / a segment's
     return s;
 }
 Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t N, bool packed, bool bwd,
@@ -363,7 +368,7 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
     };
     const size_t ch = (size_t)s.slots * H;
     if (packed) {
-        l.seqs = take((size_t)N * sizeof(Seq));
+        l.seqs = take((size_t)N * sizeof(Packed));
         l.order = take((size_t)N * 4);
     }
     l.rec = take(ch * rec_bytes(bwd));
@@ -371,8 +376,8 @@ Layout layout(const Sizes &s, int64_t ntok, int32_t H, int32_t Hk, int32_t K, in
         l.third = take(tile_bytes > 4 ? ch * 3 * kThirdBytes : 0);
         l.z = take(ch * V * kChunkTokens * tile_bytes);
         l.dw = take(ch * V * kChunkTokens * tile_bytes);
-        l.seed_s = take((size_t)s.segs * H * K * V * 4);
-        l.seed_g = take((size_t)s.segs * H * K * V * 4);
+        l.seed_s = take((size_t)s.borders * H * K * V * 4);
+        l.seed_g = take((size_t)s.borders * H * K * V * 4);
         l.dk_part = take((size_t)ntok * H * K * 4);
         if (Hk != H) {
             l.dq = take((size_t)ntok * H * K * 4);
@@ -405,7 +410,7 @@ Call prepare(const GdArgs &a, bool bwd) {
     const Sizes s = sizes(a.B, a.T, a.num_seqs, a.H, a.K, packed);
     x.l = layout(s, a.B * a.T, a.H, a.Hk, a.K, a.V, a.num_seqs, packed, bwd, tile_bytes(a.io_bf16, a.gates_fp32));
     x.ws = reinterpret_cast<char *>(a.workspace);
-    x.c.seqs = packed ? reinterpret_cast<const Seq *>(x.ws + x.l.seqs) : nullptr;
+    x.c.seqs = packed ? reinterpret_cast<const Packed *>(x.ws + x.l.seqs) : nullptr;
     x.c.order = packed ? reinterpret_cast<const int32_t *>(x.ws + x.l.order) : nullptr;
     x.c.T = a.T;
     x.c.ntok = a.B * a.T;
@@ -441,7 +446,7 @@ hipError_t prep_k(const GdArgs &a, const Common &c, bool bwd, hipStream_t st) {
 hipError_t make_records(const GdArgs &a, const Call &x, bool bwd, hipStream_t st) {
     if (x.c.seqs) {
         hipLaunchKernelGGL(kda_gd_table_kernel, dim3(1), dim3(1024), 0, st, a.cu_seqlens, a.num_seqs, (uint32_t)a.T,
-                           (uint32_t)x.c.seg, const_cast<Seq *>(x.c.seqs), const_cast<int32_t *>(x.c.order));
+                           (uint32_t)x.c.seg, const_cast<Packed *>(x.c.seqs), const_cast<int32_t *>(x.c.order));
         KDA_TRY(hipGetLastError());
     }
     if (a.T == 0) return hipSuccess;

@@ -49,9 +49,15 @@ constexpr int kChunkTokens = 32;
 // Chunks of a workgroup of the gradients' kernel: a power of two from 2 up to this (Common::seg).
 constexpr int segment_most(int K) { return K == 128 ? 16 : 8; }
 
-// A sequence: its tokens in the flattened [B * T], the number of its first chunk and of its first segment among all.
+// A sequence: its tokens in the flattened [B * T], the number of its first chunk and of its first segment among all, and that
+// of its first border between two segments.
 struct Seq {
-    int64_t t0, t1, first, seg;
+    int64_t t0, t1, first, seg, border;
+};
+// The same of a packed sequence, in the workspace: 32 bytes (fewer than 2^31 tokens in all, and 2^26 sequences).
+struct Packed {
+    int64_t t0, t1, first;
+    int32_t seg, border;
 };
 
 // A chunk's record, made once per (chunk, head) and read by the passes over the states. Matrices lie in the order in
@@ -64,7 +70,7 @@ constexpr int rec_bytes(bool bwd) { return (bwd ? 3 : 2) * kMatBytes + kWeights 
 constexpr int rec_weights(bool bwd) { return (bwd ? 3 : 2) * kMatBytes; }
 
 struct Common {
-    const Seq *seqs;   // or null: rows of T tokens
+    const Packed *seqs;   // or null: rows of T tokens
     const int32_t *order;  // the sequences in the order of their workgroups, or null
     int64_t T, ntok, slots, segs;  // slots, segs: chunks and segments of all sequences (upper bounds when packed)
     int32_t nch, nseg;  // per row (not packed)
@@ -82,7 +88,7 @@ struct StateArgs {
     void *o;                 // forward: [B,T,H,V]; reverse: dv
     char *rows;              // backward: [slots][H] tiles of [V][32]: the errors z, or the writes' gradients
     int32_t parts;           // of a tile's values, bf16 I/O: 2, or 3 for all their bits
-    float *seed;             // backward: states at the segments' borders [segs][H][K][V]
+    float *seed;             // backward: states at the borders between segments [borders][H][K][V]
     int32_t tiles;           // column tiles
 };
 
@@ -106,8 +112,11 @@ hipError_t grad_pass_fp32(const GradArgs &a, int K, int V, hipStream_t st);
 
 #ifdef __HIPCC__
 __device__ __forceinline__ Seq seq_of(const Common &c, int64_t n) {
-    if (c.seqs) return c.seqs[n];
-    return Seq{n * c.T, (n + 1) * c.T, n * c.nch, n * c.nseg};
+    if (c.seqs) {
+        const Packed p = c.seqs[n];
+        return Seq{p.t0, p.t1, p.first, p.seg, p.border};
+    }
+    return Seq{n * c.T, (n + 1) * c.T, n * c.nch, n * c.nseg, n * (c.nseg - 1)};
 }
 // The last sequence whose first chunk (segment) is at most `slot`, by 64 entries at a time. One wavefront, all lanes.
 template <bool SEG>

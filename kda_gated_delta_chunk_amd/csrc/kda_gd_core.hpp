@@ -506,9 +506,9 @@ __device__ __forceinline__ void state_pass(const StateArgs &A, int V, int64_t bl
             *reinterpret_cast<f32x4 *>(w + 4) = *reinterpret_cast<const f32x4 *>(wt + which * C + token_of(1, g));
         };
         if (MODE == kErrors && c > 0 && (c & (A.c.seg - 1)) == 0)
-            put_state(A.seed + ((sq.seg + c / A.c.seg) * A.c.H + h) * sstate);
+            put_state(A.seed + ((sq.border + c / A.c.seg - 1) * A.c.H + h) * sstate);
         if (MODE == kReverse && c + 1 < nch && ((c + 1) & (A.c.seg - 1)) == 0)
-            put_state(A.seed + ((sq.seg + c / A.c.seg) * A.c.H + h) * sstate);
+            put_state(A.seed + ((sq.border + c / A.c.seg) * A.c.H + h) * sstate);
 
         Frag8<BF> third[REV ? 2 : 1][2];
         if constexpr (BF && NP == 3) {

@@ -235,7 +235,8 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     };
     take(0);
     f32x4 st[VT];
-    get_state(c0 > 0 ? A.seed_s + (slot * A.c.H + h) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
+    const int64_t border_h = (sq.border + slot - sq.seg) * A.c.H + h;  // the border behind the segment
+    get_state(c0 > 0 ? A.seed_s + (border_h - A.c.H) * sstate : A.S0 ? A.S0 + nh * sstate : nullptr, st);
     hd::mfma_fence_state(reinterpret_cast<f32x4(&)[1][VT]>(st));
 
     const int rowv0 = RV::row_at(lane), rowk0 = RK::row_at(lane), rowc0 = RC::row_at(lane), tilev0 = RV::tile_at(lane);
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(K * 4, 2) void kda_gd_grad_kernel(const GradArgs A)
     f32x4 gt[VT];
     constexpr bool EARLY = NP == 2;
     const float *const behind =
-        c1 < all ? A.seed_g + (slot * A.c.H + h) * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr;
+        c1 < all ? A.seed_g + border_h * sstate : A.dS_final ? A.dS_final + nh * sstate : nullptr;
     for (int i = 0; i < nch; ++i) {
         const int64_t tc = sq.t0 + (int64_t)(c0 + i) * C;
         const int m = sq.t1 - tc < C ? (int)(sq.t1 - tc) : C;
