@@ -566,9 +566,11 @@ size_t kda_gd_chunk_bwd_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t
  *   o          [B, T, H, V] in `io`; rows of tokens outside every sequence
  *              are neither read nor written
  *   S_final    [num_seqs, H, K, V] fp32, or NULL to skip
- * The state is fp32 throughout; for bf16 I/O what is added to it enters with
- * all 24 bits, and what is read from it, and the pairs' weights, as a pair of
- * bf16 (2^-17 of a term). A non-finite q, k, v, g or beta spoils its own head
+ * The state is fp32 throughout, and so are all sums; for bf16 I/O what is
+ * added to the state enters with all 24 bits. What is read from it, the
+ * chunks' inverses, the pairs' weights and the rows between two products are
+ * each a pair of bf16 (2^-17 of a term), whatever the gates' type: S_final is
+ * off by some 5e-7 of its size. A non-finite q, k, v, g or beta spoils its own head
  * and sequence from its own token on (garbage behind a prompt that shares its
  * row does not reach it). Errors as for kda_chunk_fwd (INVALID_VALUE also for
  * H % Hk != 0, H >= 65536, num_seqs * H >= 2^26, gates of another type and a
@@ -587,11 +589,14 @@ kda_status_t kda_gd_chunk_fwd(const void *q, const void *k, const void *v, const
  *   dg, dbeta  [B, T, H] in `gates`
  *   dS0        [num_seqs, H, K, V] fp32, or NULL to skip
  * Nothing from a forward call is needed; the result is deterministic. Rows of
- * tokens outside every sequence are not written. A non-finite value reaches,
- * in its own head and sequence, what depends on it: a v dq and dk from its
- * token on, a q or d_o dk and dv up to its token (d_o also its dq), a k dq from
- * its token on, dv up to it and every dk, a g or beta all of these; and any of
- * them may spoil every dg and dbeta.
+ * tokens outside every sequence are not written. For bf16 I/O the operands
+ * that the call computes are pairs of bf16 beside bf16 gates and three bf16
+ * parts, all 24 bits, beside fp32 ones (the pairs' weights, of which dq and dk
+ * are made, are pairs beside either). A non-finite value reaches, in its own
+ * head and sequence, what depends on it: a v dq and dk from its token on, a q
+ * or d_o dk and dv up to its token (d_o also its dq), a k dq from its token on,
+ * dv up to it and every dk; a g or beta may spoil every dq, dk and dv, and any
+ * of them every dg and dbeta.
  */
 kda_status_t kda_gd_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
                               const float *S0, const int32_t *cu_seqlens, const void *d_o, const float *dS_final,

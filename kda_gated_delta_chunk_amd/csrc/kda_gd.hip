@@ -340,6 +340,8 @@ struct Sizes {
 // workgroups of the gradients' kernel for every place on the card that a sequence of 4096 tokens finds. A segment's start and
 // end cost about as much as 1.2 of its chunks and its states' way through memory (4096 x 96 heads: 533 us of 16 chunks, 554 of
 // 8), a long one leaves compute units idle (1531 tokens x 12 heads of 64 channels: 282 us of 16 chunks, 146 of 8, 84 of 2).
+// Short rows pay for it: a single one of 512 tokens of 96 heads is 96 workgroups (the whole call 210 us; segments of 8 chunks
+// would take 149), of 64 heads 191 (of 4: 95); four rows of 512 497 (of 8: 466), one of 1024 271 (of 8: 285).
 int32_t segment_chunks(int32_t H, int32_t K) {
     int32_t seg = segment_most(K);
     while (seg > 2 && (int64_t)seg * 512 > (int64_t)H * K) seg >>= 1;

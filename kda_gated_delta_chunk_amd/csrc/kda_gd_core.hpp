@@ -166,9 +166,6 @@ template <int NCOL> struct Rw<true, NCOL> {
         const uint2 u = *reinterpret_cast<const uint2 *>(t + quad(row, col));
         x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
     }
-    static __device__ __forceinline__ float load_one(const char *t, int row, int col) {
-        return bf2f(*reinterpret_cast<const uint16_t *>(t + quad(row, col) + 2 * (col & 3)));
-    }
 };
 template <int NCOL> struct Rw<false, NCOL> {
     static constexpr int NS = NCOL / 4, RB = (NCOL + 4) * 4;
@@ -262,7 +259,8 @@ struct BytesIn {
 };
 
 // ------------------------------------------------------------------ records
-// A tile of a record's matrix as an operand, and one of its entries: row m of the tile, source slot j of lane group g.
+// A tile of a record's matrix as an operand, and one of its entries: row m of the tile, source slot j of lane group g (bf16: of
+// two parts; a third is too small to matter beside values that are not finite, and the tokens before them keep 2^-17).
 template <bool BF>
 __device__ __forceinline__ Pair<BF> load_mat(const char *m, int tt, int lane) {
     Pair<BF> p;
@@ -363,8 +361,9 @@ struct StateLds {
 // are at once operands of the products with the state, so it never leaves the registers. A third of the wavefronts bring
 // the rows, a chunk ahead in LDS and another on its way: done by the rest beside their products it took 700 cycles a chunk.
 // bf16: products of inputs are exact, the state and computed operands go in as two bf16 parts, what is added to the state
-// as three (the state after 4096 tokens is off by 5e-7 of its size, an output by what its own rounding gives). NP = 3, the
-// gradients beside fp32 gates: all of them three (4100 tokens of 32 heads: 177 us for 157).
+// as three (the state after 4096 tokens is off by 5e-7 of its size, an output by what its own rounding gives: with three parts
+// in the forward pass neighbouring bf16 values would still flip with the order of the sums). NP = 3, the gradients beside fp32
+// gates: all of them three (4100 tokens of 32 heads: 177 us for 157).
 //
 // Bound by one wavefront's way through a chunk, whose steps wait for one another: forward 68 matrix instructions (1088
 // cycles), about 230 vector ones (1100), 40 reads of an LDS that three others read as well (870): 3300 cycles, 170 us for

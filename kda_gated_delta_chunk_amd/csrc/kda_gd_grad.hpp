@@ -139,7 +139,8 @@ struct GradLds {
 
 // One segment of a (sequence, head); a wavefront 16 columns of K, all V rows of the transposed states in its registers.
 // YF: dq and dk in fp32 per v head. NP: bf16 parts of computed operands, two beside bf16 gates, three beside fp32 ones (dg
-// is a difference of long sums: with two parts it was off by 1.4e-5 of its size, with three by 1e-6); GF: the gates'
+// is a difference of long sums: with two parts it was off by 1.4e-5 of its size, with three by 1e-6). The pairs' weights are two
+// parts in either: only dq and dk are made of them, dg's pairs come from the unrounded products. GF: the gates'
 // gradients in fp32. What adds to the log-decays' gradient stays in LDS by chunk until the segment's end: summed chunk by
 // chunk it held up every barrier (60 of 600 us).
 //

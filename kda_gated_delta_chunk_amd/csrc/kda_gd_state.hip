@@ -23,7 +23,12 @@ hipError_t launch(StateArgs a, StateArgs *e, int V, hipStream_t st) {
 // one: their products overlap, and they read the same rows (4096 tokens of 256 heads: 318 us for 401; of 64 heads 184 us
 // and 300). Packed sequences are balanced as they come, which takes several pieces for every compute unit (16 of 17011 tokens,
 // 32 heads: 251 us for 226). With three parts and K = 128 the registers of both tiles' wavefronts spill (backward passes of
-// 4096 tokens of 96 heads: 907 us for 531): one tile then.
+// 4096 tokens of 96 heads: 907 us for 531): one tile then. Of the others at K = V = 128 two tiles spill 2 (forward) and 4
+// (backward) of 168 registers in bf16, which shows nowhere (forward 17 to 20% faster), and 19 and 23 in fp32, which costs the
+// forward call what sharing gains (whole calls of 1024 tokens, two tiles for one: 160 heads 341 us for 351, 256 heads 388 for
+// 387, 512 heads 781 for 760) and the backward call less (96 heads 695 for 682, 256 heads 1326 for 1401; 8000 packed tokens
+// of 16 sequences, 64 heads 2768 for 2926). K = 32 in fp32 is the rule's worst: 160 to 256 heads forward 6 to 8% slower than
+// one tile, 512 heads 10% faster.
 template <bool BF, int K>
 hipError_t by_tile(const StateArgs &a, StateArgs *e, int V, hipStream_t st) {
     constexpr int64_t kUnits = 256;

@@ -238,8 +238,8 @@ def hd_chunk_bwd(q, k, v, g, do, S0=None, dS_final=None, cu_seqlens=None, scale:
     [num_seqs, H, K, V], or None: zero). Returns a dict: dq, dk, dv in the inputs' shapes and dtype (dq and dk summed
     over the heads that share them); dg [B, T, H] when g is per token and ``want_dg`` (a constant per head has no
     gradient here: give it per token and sum); dS0 fp32 when ``want_dS0``. ``out`` may hold preallocated results by
-    these names. Nothing of a forward call is needed; deterministic. q, k and v may each
-    be a Checkpoint8.
+    these names. Nothing of a forward call is needed; deterministic. q, k and v may each be a Checkpoint8: it is
+    restored to a tensor that the call allocates, whatever is preallocated.
     """
     lib = _lib.load()
     q, k, v = _restored(q, k, v)
