@@ -6,7 +6,7 @@ import torch
 
 import kda_gated_delta_chunk_amd as kda
 from oracle import delta as od
-from tests.test_gpu_delta import ARGS, check_bwd, inputs
+from tests.test_gpu_delta import ARGS, check_bwd, check_fwd, inputs
 from tests.test_gpu_layers import DT, U
 
 pytestmark = pytest.mark.gpu
@@ -27,7 +27,7 @@ def some_heads(x, r, Hk, group):
     few = sorted({0, Hk // 2, Hk - 1})
     v = [h * group + i for h in few for i in range(group)]
     cut = {n: t[:, :, few if n in ("q", "k") else v] if n not in ("S0", "dS") else t[:, v] for n, t in x.items()}
-    res = {n: t[:, :, few if n in ("dq", "dk") else v] if n != "dS0" else t[:, v] for n, t in r.items()}
+    res = {n: t[:, :, few if n in ("dq", "dk") else v] if n not in ("dS0", "S") else t[:, v] for n, t in r.items()}
     return {n: t.contiguous() for n, t in cut.items()}, res
 
 
@@ -50,6 +50,18 @@ def test_walks_of_few_to_many_chunks(T, io, gates):
     x = inputs(1, T, 64, 64, 128, 128, io, 60 + T, gates)
     r = kda.gd_chunk_bwd(*(x[n] for n in ARGS), x["do"], S0=x["S0"], dS_final=x["dS"])
     check_bwd(*some_heads(x, r, 64, 1))
+
+
+@pytest.mark.parametrize("io,gates", TYPES)
+@pytest.mark.parametrize("H,Hk,K", [(160, 80, 128), (144, 144, 64), (132, 33, 32)])
+def test_both_column_tiles_in_a_workgroup(H, Hk, K, io, gates):
+    """More column tiles of 64 than compute units, many chunks: the forward call and the gradients."""
+    x = inputs(1, 333, H, Hk, K, 128, io, 65, gates)
+    o, S = kda.gd_chunk_fwd(*(x[n] for n in ARGS), S0=x["S0"], scale=0.3)
+    r = kda.gd_chunk_bwd(*(x[n] for n in ARGS), x["do"], S0=x["S0"], dS_final=x["dS"], scale=0.3)
+    few, res = some_heads(x, {**r, "o": o, "S": S}, Hk, H // Hk)
+    check_fwd(few, res["o"], res["S"], scale=0.3)
+    check_bwd(few, res, scale=0.3)
 
 
 @pytest.mark.parametrize("io,gates", TYPES)
